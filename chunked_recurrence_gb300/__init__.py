@@ -19,7 +19,7 @@ import torch
 from . import build as _build
 
 GDN_OK = 0
-GDN_ERR_TIMEOUT, GDN_ERR_BOUNDS = 4, 6  # device-side statuses read from a workspace
+GDN_ERR_TIMEOUT, GDN_ERR_BOUNDS, GDN_ERR_PAGES = 4, 6, 7  # device-side statuses read from a workspace
 GDN_PATH_FUSED = 1                      # path word of a workspace after the fused kernel ran
 GDN_PATH_FRONT = 2                      # bit: gdn_layer_fwd's fused front end ran
 GDN_PATH_NORM = 4                       # bit: gdn_layer_fwd's norm ran in the scan's epilogue
@@ -31,6 +31,10 @@ GDN_FLAG_FUSED = 8
 GDN_FLAG_TEST_NO_WAIT = 16
 GDN_FLAG_LAYER_FRONT = 32
 GDN_FLAG_LAYER_NORM_EPILOGUE = 64
+GDN_FLAG_ROPE_INTERLEAVED = 128
+GDN_FLAG_ROPE_BACKWARD = 256
+GDN_ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+GDN_MAX_POOLS = 256
 CHUNK = 64
 
 _lib = None
@@ -48,8 +52,27 @@ class GdnShape(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
+class GdnCacheShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seqs", "n_tok", "Hq", "Hkv", "D", "dtype", "page_size", "n_pages",
+                                               "max_pages")]
+                + [(n, ctypes.c_int64) for n in ("table_stride", "page_stride", "slot_stride", "head_stride",
+                                                 "q_stride", "k_stride", "v_stride")])
+
+
+class GdnPageTables(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class GdnPagePools(ctypes.Structure):
+    _fields_ = [("pools", ctypes.POINTER(ctypes.c_void_p)), ("n_pools", ctypes.c_int32),
+                ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
 _P, _I32, _I64, _U32, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t)
+_F64 = ctypes.c_double
 _SIGS = {
     "gdn_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "gdn_version": ([], _I32),
@@ -79,6 +102,20 @@ _SIGS = {
     "gdn_chunk_bwd_workspace_bytes": ([ctypes.POINTER(GdnShape)], _SZ),
     "gdn_chunk_bwd": ([_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(GdnShape), _F32, _U32, _P, _P, _P, _P, _P,
                        _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "gdn_rope_inv_freq": ([_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P], ctypes.c_int),
+    "gdn_rope_freqs": ([_P, _I32, _P], ctypes.c_int),
+    "gdn_rope": ([_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _F32, _U32, _P, _P,
+                  _P], ctypes.c_int),
+    "gdn_kv_append": ([_P, _P, _P, _P, _P, _I32, _F32, _U32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+                      ctypes.c_int),
+    "gdn_paged_attn_workspace_bytes": ([_P, _I32], _SZ),
+    "gdn_paged_attn": ([_P, _P, _P, _P, _P, _P, _P, _I32, _F32, _I32, _U32, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "gdn_pages_workspace_bytes": ([_I32, _I32], _SZ),
+    "gdn_pages_grow": ([_P, _P, _P, _I32, _P, _SZ, _P], ctypes.c_int),
+    "gdn_pages_free": ([_P, _P, _I32, _P, _SZ, _P], ctypes.c_int),
+    "gdn_pages_fork": ([_P, _P, _P, _I32, _P, _P, _SZ, _P], ctypes.c_int),
+    "gdn_pages_compact": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
+    "gdn_pages_copy": ([_P, _P, _I32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
 }
 
 
@@ -548,3 +585,9 @@ def segment_parallel_fwd(q, k, v, g, beta, seg_bounds, h0=None, scale=None, l2no
     o, _ = gdn_chunk_fwd(q, k, v, g, beta, S_start, seg_bounds, scale, l2norm_qk,
                          want_h_T=False, stream=stream)
     return o, h_T
+
+
+# full attention over a paged cache
+from .paged import (cache_shape, gdn_kv_append, gdn_paged_attn, gdn_paged_attn_workspace_bytes,  # noqa: E402,F401
+                    gdn_pages_compact, gdn_pages_copy, gdn_pages_fork, gdn_pages_free, gdn_pages_grow,
+                    gdn_pages_workspace_bytes, gdn_rope, gdn_rope_freqs, gdn_rope_inv_freq)

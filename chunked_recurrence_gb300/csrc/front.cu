@@ -23,6 +23,7 @@ extern "C" const char *gdn_status_string(int status) {
     case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT";
     case GDN_ERR_WORKSPACE: return "GDN_ERR_WORKSPACE";
     case GDN_ERR_BOUNDS: return "GDN_ERR_BOUNDS";
+    case GDN_ERR_PAGES: return "GDN_ERR_PAGES";
     default: return "GDN_ERR_UNKNOWN";
   }
 }

@@ -1,0 +1,768 @@
+// paged_attn_tc.cu -- attention of new tokens over a paged cache on the tensor cores
+// (tcgen05, bf16; D = 64, 128 or 256).
+//
+// One pass over the keys with a running maximum m and sum l per query row,
+//     S = Q K^T,  P = 2^(c S - c m),  l += sum P,  O += P V,   c = scale log2 e,
+// and O, l scaled by 2^(c (m_old - m_new)) when m moves; o = O / l at the end.  m may lag
+// behind the true maximum by a factor 2^8 in P (fp32 sums and bf16 weights keep their relative
+// precision), so O is seldom touched after the first tiles.
+//
+// Query rows of a kv head (row = token * group + head in the group) are cut into items of R = 128 NQ
+// rows, keys into tiles of 128 positions.  NQ = 2 (D <= 128): two 128-row tiles share each K and V
+// tile and take turns, one's softmax under the other's MMAs.  NQ = 1: one row tile; S alternates between two TMEM
+// slots, so the next tile's S runs under this one's softmax.  TMEM: two S slots of 128 columns
+// (P, as bf16 pairs, lies over its S), then O.
+//
+// Work: (item, kv head, tile) in one line, cut into equal shares, one persistent block each, so ragged lengths
+// and causal shapes balance to a tile.  A share begins or ends inside an item where it must; such a piece leaves
+// (m, l, O) in the workspace and join_kernel adds the pieces up.  Every block finds its share by a
+// scan over the sequences' lengths: nothing is planned on the host, and the lengths stay on the
+// device.
+//
+// Warps: softmax warpgroups (one per row tile: a thread owns a query row), a TMA warp (pages by
+// their table entries, 64 columns x gcd(page_size, tile) slots a box, into 128B-swizzled panels), an MMA
+// thread.  K and V granules go through one ring in the order in which the MMAs read them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <numeric>
+
+#include "common.cuh"
+#include "paged_attn.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;              // positions a tile
+constexpr int kSms = 152;            // persistent blocks
+constexpr uint32_t kSpin = 1u << 22; // polls of a wait before it gives up
+constexpr int kData = 224 * 1024;    // Q and the ring
+constexpr float kLag = 8.f;          // m may lag by this many powers of two
+
+template <int D, int NQ>
+struct Cfg {
+  static constexpr int R = 128 * NQ;
+  static constexpr int KG = D == 256 ? 2 : 1;           // granules a K (by columns) or V (by positions) tile
+  static constexpr int kGran = KT * D * 2 / KG;         // bytes
+  static constexpr int kQ = R * D * 2;
+  static constexpr int kSlots = (kData - kQ) / kGran;
+  static constexpr int kPanelsK = (D / KG) / 64;        // 64-column panels of a K granule: KT rows each
+  static constexpr int kRowsV = KT / KG, kPanelsV = D / 64;
+  static constexpr int kThreads = 128 * NQ + 64;
+  static constexpr uint32_t kO = 256;                   // first TMEM column of O
+};
+
+struct TcArgs {
+  PagedSeqs seqs;
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *o;
+  float *lse;
+  const int32_t *table;
+  int64_t table_stride, q_stride;
+  int32_t G, Hkv, page_size, box, max_pages, n_pages, window;
+  float c;  // scale log2 e
+  float *part, *part_ml;
+  int4 *meta;
+  int32_t *status;
+  int32_t no_wait;
+};
+
+struct Ctl {
+  uint64_t full[16], empty[16], sfull[2], pready[2], odone[2], qready[2], drain;
+  uint32_t tmem;
+  volatile int abort;
+  int64_t sum[12];
+  int start_slot, start_h, start_j;
+};
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats to a bf16 pair (a in the low half), round to nearest even
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// a wait of all lanes, the same answer for all of them
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, kSpin, abort));
+}
+
+// A block's share of the line of work, piece by piece: `n` units from unit `j` of an item and head.
+struct Walk {
+  Item it;
+  int slot, h, j, n, units;
+  int64_t left;
+};
+__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slot, int h, int j, int64_t left) {
+  w.slot = slot, w.h = h, w.j = j, w.left = left;
+  if (left <= 0) return false;
+  w.it = item_at(a.seqs, slot, a.G, R, KT, a.window);
+  w.units = item_units(w.it);
+  w.n = (int)min((int64_t)(w.units - j), left);
+  return w.n > 0;
+}
+__device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int slots) {
+  w.left -= w.n;
+  if (w.left <= 0) return false;
+  w.j = 0;
+  if (++w.h == a.Hkv) {
+    w.h = 0;
+    do {
+      if (++w.slot >= slots) return false;
+      w.it = item_at(a.seqs, w.slot, a.G, R, KT, a.window);
+      w.units = item_units(w.it);
+    } while (w.units == 0);
+  }
+  w.n = (int)min((int64_t)w.units, w.left);
+  return true;
+}
+
+// Granules of a piece of n tiles in ring order.  NQ = 2: K0 V0 K1 V1 ...; NQ = 1: K0 K1 V0 K2 V1 ... V(n-1).
+template <int NQ, int KG>
+__device__ __forceinline__ uint32_t idx_k(uint32_t base, int j) {
+  return base + KG * (NQ == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1);
+}
+template <int NQ, int KG>
+__device__ __forceinline__ uint32_t idx_v(uint32_t base, int j, int n) {
+  return base + KG * (NQ == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1));
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const TcArgs a) {
+  using C = Cfg<D, NQ>;
+  constexpr int KG = C::KG, kSlots = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl ctl;
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *ring = sm + C::kQ;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarps = 4 * NQ + 2;
+
+  // ---- this block's share: units of every slot summed, then the slot its first unit lies in
+  const int slots = (int)item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, C::R);
+  int64_t mine = 0;
+  for (int s = tid; s < slots; s += C::kThreads) {
+    const Item it = item_at(a.seqs, s, a.G, C::R, KT, a.window);
+    if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
+    mine += (int64_t)item_units(it) * a.Hkv;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) ctl.sum[warp] = mine;
+  if (tid == 0) ctl.abort = 0, ctl.start_slot = -1;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += ctl.sum[i];
+  const int blocks = (int)min((int64_t)gridDim.x, total);  // shares of at least a unit, to the first blocks
+  const int64_t begin = share_begin(total, min((int)blockIdx.x, blocks), max(blocks, 1));
+  const int64_t end = share_begin(total, min((int)blockIdx.x + 1, blocks), max(blocks, 1));
+  if (begin >= end) {
+    if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  int64_t before = 0;
+  for (int base = 0; base < slots; base += C::kThreads) {
+    const int s = base + tid;
+    const int units = s < slots ? item_units(item_at(a.seqs, s, a.G, C::R, KT, a.window)) : 0;
+    const int64_t cost = (int64_t)units * a.Hkv;
+    int64_t x = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += u;
+    }
+    __syncthreads();
+    if (lane == 31) ctl.sum[warp] = x;
+    __syncthreads();
+    int64_t all = 0, upto = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) upto += ctl.sum[i];
+      all += ctl.sum[i];
+    }
+    const int64_t from = before + upto + x - cost;  // units before this slot
+    if (cost > 0 && begin >= from && begin < from + cost) {
+      ctl.start_slot = s;
+      ctl.start_h = (int)((begin - from) / units);
+      ctl.start_j = (int)((begin - from) % units);
+    }
+    before += all;
+    if (before > begin) break;
+  }
+
+  // ---- barriers and TMEM
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.sfull[i], 1);
+      mbar_init(&ctl.pready[i], 4);
+      mbar_init(&ctl.odone[i], 1);
+      mbar_init(&ctl.qready[i], 4);
+    }
+    mbar_init(&ctl.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = ctl.tmem;
+  volatile int *abort_flag = &ctl.abort;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    set_status(a.status, GDN_ERR_TIMEOUT);
+  };
+  Walk w;
+  uint32_t issued = 0;  // granules (the TMA warp's count)
+  bool more = walk_begin(a, w, C::R, ctl.start_slot, ctl.start_h, ctl.start_j, end - begin);
+
+  if (warp == kWarpTma) {
+    // ================================================= K and V granules, page by page
+    uint32_t base = 0;
+    bool ok = true;
+    const uint32_t box_bytes = (uint32_t)a.box * 128u;
+    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, int rows, int panels, uint32_t panel_bytes, int col0,
+                    const int32_t *row) {
+      const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
+      if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
+        ok = false;
+        return;
+      }
+      const int nb = rows / a.box;
+      int page = -1, at = 0;
+      if (lane < nb) {
+        const int pos = pos0 + lane * a.box;
+        // boxes past the last position that a row sees, or before the first, are not read
+        if (pos < w.it.hi && pos + a.box > w.it.lo) {
+          page = page_of(row, pos, a.page_size, a.max_pages, a.n_pages);
+          at = pos % a.page_size;
+          if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
+        }
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes * panels);
+      __syncwarp();
+      if (page >= 0)
+        for (int p = 0; p < panels; ++p)
+          tma_load_4d(ring + slot * C::kGran + p * panel_bytes + lane * box_bytes, map, &ctl.full[slot], col0 + 64 * p,
+                      at, w.h, page);
+      issued = idx + 1;
+    };
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    while (more && ok) {
+      if (w.it.n_tiles > 0) {
+        const int32_t *row = a.table + (int64_t)w.it.s * a.table_stride;
+        const int first = (w.it.tile0 + w.j) * KT;
+        auto load_k = [&](int j) {
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+            if (ok) load(&tm_k, idx_k<NQ, KG>(base, j) + g, first + j * KT, KT, C::kPanelsK, KT * 128, g * (D / KG), row);
+        };
+        auto load_v = [&](int j) {
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+            if (ok)
+              load(&tm_v, idx_v<NQ, KG>(base, j, w.n) + g, first + j * KT + g * C::kRowsV, C::kRowsV, C::kPanelsV,
+                   C::kRowsV * 128, 0, row);
+        };
+        load_k(0);
+        for (int j = 0; j < w.n && ok; ++j) {
+          if (NQ == 1 && j + 1 < w.n) load_k(j + 1);
+          if (ok) load_v(j);
+          if (NQ == 2 && j + 1 < w.n && ok) load_k(j + 1);
+        }
+        base += 2 * KG * w.n;
+      }
+      more = walk_next(a, w, C::R, slots);
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == kWarpMma) {
+    // ================================================= MMAs
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, KT, false, false);
+      const uint32_t id_o = idesc_bf16(128, D, false, true);
+      const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
+      const uint64_t d_k = smem_desc(smem_u32(ring), 16, 1024, 2);
+      const uint64_t d_v = smem_desc(smem_u32(ring), C::kRowsV * 128, 1024, 2);
+      uint32_t base = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // steps: P tiles consumed, per TMEM slot
+      uint32_t total_steps = 0;                         // NQ = 1: the S slots alternate across pieces
+      bool ok = !a.no_wait;
+      auto wait_full = [&](uint32_t idx) {
+        if (ok && !mbar_wait_spin(&ctl.full[idx % kSlots], (idx / kSlots) & 1, kSpin, abort_flag)) ok = false;
+      };
+      // S[slot] = Q[t] K(j)^T
+      auto issue_s = [&](int t, int slot, int j) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+          const uint32_t idx = idx_k<NQ, KG>(base, j) + g;
+          wait_full(idx);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t dk = d_k + (((idx % kSlots) * C::kGran) >> 4);
+          const uint64_t dq = d_q + ((t * 128 * D * 2 + g * C::kPanelsK * 16384) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / KG / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+            umma_bf16(tm + slot * 128, dq + off, dk + off, id_s, g > 0 || ks > 0);
+          }
+        }
+        umma_commit(&ctl.sfull[slot]);
+      };
+      // O[t] (+)= P[slot] V(j)
+      auto issue_o = [&](int t, int slot, int j) {
+        if (!mbar_wait_spin(&ctl.pready[slot], steps[slot] & 1, kSpin, abort_flag)) {
+          ok = false;
+          return;
+        }
+        ++steps[slot];
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+          const uint32_t idx = idx_v<NQ, KG>(base, j, w.n) + g;
+          wait_full(idx);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < C::kRowsV / 16; ++ks)
+            umma_ts(tm + C::kO + t * D, tm + slot * 128 + (g * (C::kRowsV / 16) + ks) * 8, dv + ((ks * 2048) >> 4), id_o,
+                    j > 0 || g > 0 || ks > 0);
+          if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
+        }
+      };
+      while (more && ok) {
+        const int n = w.it.n_tiles > 0 ? w.n : 0;
+        if (n > 0) {
+          const int nt = NQ == 2 && w.it.rows > 128 ? 2 : 1;
+          for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_spin(&ctl.qready[t], pieces[t]++ & 1, kSpin, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (NQ == 2) {
+            for (int t = 0; t < nt && ok; ++t) issue_s(t, t, 0);
+            for (int j = 0; j < n && ok; ++j)
+              for (int t = 0; t < nt && ok; ++t) {
+                issue_o(t, t, j);
+                if (!ok) break;
+                if (j + 1 < n) issue_s(t, t, j + 1);
+                else umma_commit(&ctl.odone[t]);
+              }
+          } else {
+            issue_s(0, total_steps & 1, 0);
+            for (int j = 0; j < n && ok; ++j, ++total_steps) {
+              if (j + 1 < n) issue_s(0, (total_steps + 1) & 1, j + 1);
+              if (ok) issue_o(0, total_steps & 1, j);
+            }
+          }
+          base += 2 * KG * n;
+        }
+        more = walk_next(a, w, C::R, slots);
+      }
+      if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
+        if (!ok) fail();
+        umma_commit(&ctl.drain);
+        mbar_wait(&ctl.drain, 0, kSpin);
+      }
+    }
+  } else {
+    // ================================================= softmax: a thread owns a query row
+    const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lq = (uint32_t)(quarter * 32) << 16;
+    const float lag = kLag / a.c;
+    uint32_t base = 0, steps = 0, sphase[2] = {0, 0}, pieces = 0;
+    int cont = 0, head = 0, head_slot = 0, head_h = 0;
+    bool ok = true;
+    while (more && ok) {
+      const Item &it = w.it;
+      const int rr = t * 128 + r;
+      const bool valid = rr < it.rows;
+      const int row = it.row0 + (valid ? rr : 0), i = row / a.G, g = row - i * a.G;
+      const int64_t tok = it.t0 + i, out = tok * (a.G * a.Hkv) + w.h * a.G + g;
+      const bool begins = w.j == 0, ends = w.j + w.n == w.units;
+      if (it.n_tiles == 0) {  // rows that see nothing
+        if (valid) {
+          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.o + out * D + d) = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[out] = -INFINITY;
+        }
+        more = walk_next(a, w, C::R, slots);
+        continue;
+      }
+      const int n = w.n, nt = it.rows > 128 ? 2 : 1;
+      const int first = (it.tile0 + w.j) * KT;
+      const bool live = t < nt && t * 128 + quarter * 32 < it.rows;  // this warp has a row
+      // ---- this row tile's queries, 16-byte pieces along a row across the lanes
+      {
+        constexpr int kL = D / 8, kRowsIt = 32 / kL > 0 ? 32 / kL : 1;
+        const int64_t off = valid ? tok * a.q_stride + (int64_t)(w.h * a.G + g) * D : -1;
+        uint8_t *qs = sm + t * 128 * D * 2;
+        if (t < nt)
+#pragma unroll 4
+          for (int x = 0; x < 32; x += kRowsIt) {
+            const int rl = x + (kL < 32 ? lane / kL : 0), ch = kL < 32 ? lane % kL : lane;
+            const int64_t of = __shfl_sync(0xffffffffu, off, rl);
+            const uint4 v = of >= 0 ? *reinterpret_cast<const uint4 *>(a.q + of + ch * 8) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * 16384 + sw128_off(quarter * 32 + rl, (ch & 7) * 8)) = v;
+          }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (t < nt && lane == 0) mbar_arrive(&ctl.qready[t]);
+      }
+      if (t < nt) {
+        const int p = it.first + i;
+        const int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+        float m = -INFINITY, l = 0.f;
+        const bool releases = NQ == 1 || t == nt - 1;  // this warpgroup gives ring slots back
+        for (int j = 0; j < n; ++j, ++steps) {
+          const int slot = NQ == 2 ? t : steps & 1;
+          if (!warp_wait(&ctl.sfull[slot], sphase[slot] & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ++sphase[slot];
+          tc_fence_after();
+          // S is there: K(j) has been read, and (NQ = 2) V(j - 1), whose product came before it
+          if (releases && tid == t * 128) {
+            for (int g2 = 0; g2 < KG; ++g2) mbar_arrive(&ctl.empty[(idx_k<NQ, KG>(base, j) + g2) % kSlots]);
+            if (NQ == 2 && j > 0) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, j - 1, n) % kSlots]);
+          }
+          const int pos = first + j * KT;
+          if (t == 0 && (pos < it.lo || pos + KT > it.hi)) {
+            // positions that no row sees: their V rows become zeros (P is 0 there, and 0 * NaN is not)
+            const int x = pos + r;
+            const uint32_t idx = idx_v<NQ, KG>(base, j, n) + r / C::kRowsV;
+            if (!warp_wait(&ctl.full[idx % kSlots], (idx / kSlots) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (x < it.lo || x >= it.hi) {
+              uint8_t *vr = ring + (idx % kSlots) * C::kGran + (r % C::kRowsV) * 128;
+              for (int pn = 0; pn < C::kPanelsV; ++pn)
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch)
+                  *reinterpret_cast<uint4 *>(vr + pn * C::kRowsV * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          if (live) {
+            float s[KT];
+#pragma unroll
+            for (int x = 0; x < KT; x += 32)
+              tmem_ld32u(tm + lq + slot * 128 + x, reinterpret_cast<uint32_t *>(s) + x);
+            tmem_wait_ld();
+            if (pos + KT > hi || pos < lo) {
+#pragma unroll
+              for (int x = 0; x < KT; ++x) s[x] = pos + x < hi && pos + x >= lo ? s[x] : -INFINITY;
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int x = 1; x < KT; ++x) mx = fmaxf(mx, s[x]);
+            if (j == 0) {
+              m = mx;
+            } else if (__any_sync(0xffffffffu, mx > m + lag)) {
+              // the products so far end before O is scaled
+              if (NQ == 1) {
+                const uint32_t idx = idx_v<NQ, KG>(base, j - 1, n) + KG - 1;
+                ok = ok && warp_wait(&ctl.empty[idx % kSlots], (idx / kSlots) & 1, abort_flag);
+                tc_fence_after();
+              }
+              const float top = mx > m + lag ? mx : m;
+              const float f = m == top ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * a.c);
+              m = top;
+              l *= f;
+#pragma unroll
+              for (int x = 0; x < D; x += 32) {
+                uint32_t u[32];
+                tmem_ld32u(tm + lq + C::kO + t * D + x, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(__uint_as_float(u[y]) * f);
+                tmem_st32u(tm + lq + C::kO + t * D + x, u);
+              }
+            }
+            const float mc = m == -INFINITY ? 0.f : m * a.c;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < KT; x += 64) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int y = 0; y < 64; y += 2) {
+                const float p0 = ex2(fmaf(s[x + y], a.c, -mc)), p1 = ex2(fmaf(s[x + y + 1], a.c, -mc));
+                sum[(y >> 1) & 3] += p0 + p1;
+                pk[y >> 1] = bf16x2(p0, p1);
+              }
+              tmem_st32u(tm + lq + slot * 128 + (x >> 1), pk);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.pready[slot]);
+        }
+        // ---- the last product done: O / l, or the piece for the join
+        if (ok) {
+          if (NQ == 2) {
+            ok = warp_wait(&ctl.odone[t], pieces & 1, abort_flag);
+            if (releases && tid == t * 128) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, n - 1, n) % kSlots]);
+          } else {
+            const uint32_t idx = idx_v<NQ, KG>(base, n - 1, n) + KG - 1;
+            ok = warp_wait(&ctl.empty[idx % kSlots], (idx / kSlots) & 1, abort_flag);
+          }
+          tc_fence_after();
+        }
+        if (ok && live) {
+          const bool whole = begins && ends;
+          const int which = 2 * blockIdx.x + (begins ? 1 : 0);
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          float *pp = a.part + ((int64_t)which * C::R + rr) * D;
+#pragma unroll
+          for (int x = 0; x < D; x += 32) {
+            uint32_t u[32];
+            tmem_ld32u(tm + lq + C::kO + t * D + x, u);
+            tmem_wait_ld();
+            if (valid) {
+              if (whole) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 8) {
+                  uint4 v;
+                  uint32_t *vv = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    vv[z] = bf16x2(__uint_as_float(u[y + 2 * z]) * inv, __uint_as_float(u[y + 2 * z + 1]) * inv);
+                  *reinterpret_cast<uint4 *>(a.o + out * D + x + y) = v;
+                }
+              } else {
+#pragma unroll
+                for (int y = 0; y < 32; y += 4)
+                  *reinterpret_cast<uint4 *>(pp + x + y) = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
+              }
+            }
+          }
+          if (valid) {
+            if (whole) {
+              if (a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
+            } else {
+              *reinterpret_cast<float2 *>(a.part_ml + ((int64_t)which * C::R + rr) * 2) = make_float2(m * a.c, l);
+            }
+          }
+        }
+        tc_fence_before();
+        ++pieces;
+      }
+      base += 2 * KG * n;
+      if (!begins) cont = ends ? 2 : 1;
+      else if (!ends) head = 1, head_slot = w.slot, head_h = w.h;
+      more = walk_next(a, w, C::R, slots);
+    }
+    if (!ok && lane == 0) fail();
+    if (tid == 0) a.meta[blockIdx.x] = make_int4(cont, head, head_slot, head_h);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // a wait gave up: copies in flight land before the block's memory goes
+    if (warp == kWarpTma)
+      for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
+        mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, kSpin);
+    __syncthreads();
+  }
+  if (warp == kWarpMma) tmem_dealloc(tm, 512);
+}
+
+// Items that lie in several blocks' shares: block b's last piece begins one, b + 1's first
+// continues it, until a first piece ends it.  A warp takes a row.
+template <int D, int NQ>
+__global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
+  constexpr int R = Cfg<D, NQ>::R, kE = D / 32;
+  const int4 me = a.meta[blockIdx.x];
+  if (!me.y) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Item it = item_at(a.seqs, me.z, a.G, R, KT, a.window);
+  int last = blockIdx.x + 1;
+  while (last < blocks && a.meta[last].x == 1) ++last;
+  if (last >= blocks) return;  // a share that gave up
+  for (int rr = blockIdx.y * 8 + warp; rr < it.rows; rr += gridDim.y * 8) {
+    auto at = [&](int b) { return (int64_t)(b == (int)blockIdx.x ? 2 * b + 1 : 2 * b) * R + rr; };
+    float top = -INFINITY;
+    for (int b = blockIdx.x + lane; b <= last; b += 32) top = fmaxf(top, a.part_ml[at(b) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float x[kE], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) x[e] = 0.f;
+#pragma unroll 4
+    for (int b = blockIdx.x; b <= last; ++b) {
+      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at(b) * 2);
+      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+      sum = fmaf(f, ml.y, sum);
+      const float *p = a.part + at(b) * D + lane * kE;
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p + e);
+        x[e] += f == 0.f ? 0.f : f * v.x;
+        x[e + 1] += f == 0.f ? 0.f : f * v.y;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int row = it.row0 + rr, i = row / a.G, g = row - i * a.G;
+    const int64_t out = (int64_t)(it.t0 + i) * (a.G * a.Hkv) + me.w * a.G + g;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2)
+      *reinterpret_cast<uint32_t *>(a.o + out * D + lane * kE + e) = bf16x2(x[e] * inv, x[e + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// [page][head][slot][D] of a cache, boxes of 64 columns x `box` slots
+bool make_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int box) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const int64_t heads = s.Hkv > 1 ? s.head_stride : s.D, pages = s.n_pages > 1 ? s.page_stride : s.slot_stride;
+  cuuint64_t dims[4] = {(cuuint64_t)s.D, (cuuint64_t)s.page_size, (cuuint64_t)s.Hkv, (cuuint64_t)s.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)s.slot_stride * 2, (cuuint64_t)heads * 2, (cuuint64_t)pages * 2};
+  cuuint32_t b[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, b, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int box_rows(const gdn_cache_shape &s) { return std::gcd(s.page_size, s.D == 256 ? 64 : KT); }
+
+template <int D, int NQ>
+gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {
+  using C = Cfg<D, NQ>;
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box)) return GDN_ERR_CUDA;
+  char *w = (char *)a.status;
+  a.meta = (int4 *)(w + 256);
+  a.part_ml = (float *)(w + 256 + sizeof(int4) * 256);
+  a.part = a.part_ml + (size_t)kSms * 2 * C::R * 2;
+  constexpr int smem = kData + 1024;
+  if (cudaFuncSetAttribute(paged_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return (void)cudaGetLastError(), GDN_ERR_CUDA;
+  paged_attn_kernel<D, NQ><<<kSms, C::kThreads, smem, st>>>(mk, mv, a);
+  paged_join_kernel<D, NQ><<<dim3(kSms, C::R / 32), 256, 0, st>>>(a, kSms);
+  return launch_status();
+}
+
+// Two row tiles a block where the rows fill them (they share K and V), else one.
+bool two_tiles(const gdn_cache_shape &s, int32_t max_new) {
+  return s.D <= 128 && (int64_t)max_new * (s.Hq / s.Hkv) > 128;
+}
+
+bool tc_shape(const gdn_cache_shape &s) {
+  return s.dtype == GDN_BF16 && (s.D == 64 || s.D == 128 || s.D == 256) && s.page_size % 8 == 0 &&
+         s.page_size <= 1 << 20 && s.n_pages > 0;
+}
+
+}  // namespace
+
+bool paged_attn_tc_supported(const void *q, const void *k, const void *v, const void *o, const gdn_cache_shape &s,
+                             float scale) {
+  if (!tc_shape(s) || !(scale > 1e-20f && scale < 1e20f)) return false;
+  for (const void *p : {q, k, v, o})
+    if (!aligned(p, 16)) return false;
+  for (int64_t x : {s.q_stride, s.slot_stride, s.Hkv > 1 ? s.head_stride : 8, s.n_pages > 1 ? s.page_stride : 8})
+    if (x % 8 || x >= 1LL << 39) return false;
+  return true;
+}
+
+size_t paged_attn_tc_workspace(const gdn_cache_shape &s, int32_t max_new) {
+  if (!tc_shape(s)) return 0;
+  const size_t rows = (size_t)kSms * 2 * (two_tiles(s, max_new) ? 256 : 128);
+  return 256 + sizeof(int4) * 256 + rows * (2 + s.D) * sizeof(float);
+}
+
+gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int32_t *table, const PagedSeqs &seqs,
+                         const gdn_cache_shape &s, int32_t max_new, float scale_log2, int32_t window, uint32_t flags,
+                         void *o, float *lse, void *workspace, cudaStream_t st) {
+  TcArgs a{};
+  a.seqs = seqs;
+  a.q = (const __nv_bfloat16 *)q, a.o = (__nv_bfloat16 *)o, a.lse = lse;
+  a.table = table, a.table_stride = s.table_stride, a.q_stride = s.q_stride;
+  a.G = s.Hq / s.Hkv, a.Hkv = s.Hkv;
+  a.page_size = s.page_size, a.box = box_rows(s), a.max_pages = s.max_pages, a.n_pages = s.n_pages;
+  a.window = window, a.c = scale_log2;
+  a.status = (int32_t *)workspace;
+  a.no_wait = flags & GDN_FLAG_TEST_NO_WAIT ? 1 : 0;
+  if (s.D == 256) return launch<256, 1>(k, v, s, a, st);
+  if (two_tiles(s, max_new)) return s.D == 128 ? launch<128, 2>(k, v, s, a, st) : launch<64, 2>(k, v, s, a, st);
+  return s.D == 128 ? launch<128, 1>(k, v, s, a, st) : launch<64, 1>(k, v, s, a, st);
+}
+
+}  // namespace gdn

@@ -47,7 +47,8 @@ typedef enum {
   GDN_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
   GDN_ERR_TIMEOUT = 4,     /* device status: a bounded wait gave up */
   GDN_ERR_WORKSPACE = 5,   /* workspace missing or smaller than required */
-  GDN_ERR_BOUNDS = 6       /* device status: an index check failed */
+  GDN_ERR_BOUNDS = 6,      /* device status: an index check failed */
+  GDN_ERR_PAGES = 7        /* device status: no free page left, or a page list that cannot be carried out */
 } gdn_status;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -343,6 +344,169 @@ gdn_status gdn_chain_reduce(const float *M, const float *S_local, const float *h
  * the device.  n_tokens may be 0 (then n_seqs = 0, cu_seqlens[0] = 0). */
 gdn_status gdn_cu_seqlens_from_position_ids(const int64_t *position_ids, int64_t n_tokens,
                                             int32_t *cu_seqlens, int32_t *n_seqs, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Full attention over a paged cache: the layers between the recurrent ones of a hybrid
+ * model ("feat: hybrid CP for Qwen3.5 MoE (DeltaNet + attention)", Approach: softmax
+ * attention on the remaining quarter of the layers).
+ *
+ * A cache is a k_cache and a v_cache of n_pages pages with page_size slots each; a slot
+ * holds one token's Hkv heads of D values.  Element (page, slot, head, d) lies at
+ * page * page_stride + slot * slot_stride + head * head_stride + d (in elements, the same
+ * for both; 64-bit arithmetic).  Row s of page_table (int32, table_stride elements apart)
+ * names the pages of sequence s in order; seq_lens[s] is its number of tokens.  Only the
+ * first ceil(seq_lens[s] / page_size) entries of a row are read, and of those only the
+ * ones that hold a position some query sees; what lies in slots past a sequence's end is
+ * never used, whatever it holds.
+ *
+ * Device-side checks: a length past max_pages * page_size, offsets that fall or leave
+ * [0, n_tok], and a page outside [0, n_pages) set GDN_ERR_BOUNDS in the workspace's status
+ * word and are not followed; the results of that sequence are then unspecified.
+ * ------------------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t n_seqs;       /* sequences of the call */
+  int32_t n_tok;        /* new tokens of all sequences */
+  int32_t Hq, Hkv, D;   /* query heads, kv heads (a divisor of Hq: query head h reads kv head h / (Hq / Hkv)), head width (1..256) */
+  int32_t dtype;        /* gdn_dtype of q, k, v, the cache and o */
+  int32_t page_size, n_pages;
+  int32_t max_pages;    /* entries of a page_table row that may be read */
+  int64_t table_stride; /* elements between rows of page_table; 0 = max_pages */
+  int64_t page_stride, slot_stride, head_stride; /* elements; all 0 = dense [n_pages, page_size, Hkv, D] */
+  int64_t q_stride;     /* elements between consecutive tokens of q; 0 = dense (Hq * D) */
+  int64_t k_stride, v_stride; /* of the new k and v (gdn_kv_append); 0 = dense (Hkv * D) */
+} gdn_cache_shape;
+
+#define GDN_FLAG_ROPE_INTERLEAVED 128u /* pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2) */
+#define GDN_FLAG_ROPE_BACKWARD 256u    /* gdn_rope: the transposed rotation, for gradients */
+
+/* Frequencies of the rotary pairs, on the HOST: inv_freq[i] (radians a position) for
+ * i < rotary_dim / 2, in double precision.
+ *   scaling GDN_ROPE_NONE:   base^(-2i / rotary_dim)
+ *   GDN_ROPE_LINEAR:         the same divided by factor (positions interpolated)
+ *   GDN_ROPE_BASE:           base replaced by base * factor^(r / (r - 2)), r = rotary_dim (> 2)
+ *   GDN_ROPE_PARTS:          by parts (Peng et al., "YaRN", 2023): with n = orig_len * inv / 2 pi turns
+ *                            over the original context and g = clamp((n - alpha) / (beta - alpha), 0, 1):
+ *                            (1 - g) inv / factor + g inv
+ * rotary_dim even, base > 0, factor > 0, beta > alpha and orig_len > 0 for GDN_ROPE_PARTS. */
+#define GDN_ROPE_NONE 0
+#define GDN_ROPE_LINEAR 1
+#define GDN_ROPE_BASE 2
+#define GDN_ROPE_PARTS 3
+gdn_status gdn_rope_inv_freq(int32_t rotary_dim, double base, int32_t scaling, double factor, double orig_len,
+                             double alpha, double beta, double *inv_freq);
+
+/* The table that gdn_rope and gdn_kv_append read, on the HOST: each frequency in turns a
+ * position as a 64-bit fixed-point fraction, round(inv / 2 pi * 2^64) mod 2^64.  A position
+ * times it, mod 2^64, is the angle to 2^-64 turns a position whatever the position, which a
+ * product in fp32 loses (0.06 rad at position 10^6).  Copy the n words to the device once. */
+gdn_status gdn_rope_freqs(const double *inv_freq, int32_t n, uint64_t *freqs);
+
+/* Rotary positions of q and k: for each token t, head and pair i < rotary_dim / 2, with
+ * a = positions[t] * inv_freq[i]:
+ *     y1 = scale (x1 cos a - x2 sin a),   y2 = scale (x2 cos a + x1 sin a)
+ * (x1, x2) = elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with GDN_FLAG_ROPE_INTERLEAVED;
+ * elements from rotary_dim on pass through unchanged.  With GDN_FLAG_ROPE_BACKWARD sin a has
+ * the other sign: given the gradients of the outputs, those of the inputs.
+ *   q: [n_tok, Hq, D], k: [n_tok, Hk, D] of dtype (Hq or Hk may be 0), token strides in
+ *   elements, 0 = dense, the same for the outputs;  positions: [n_tok] int64;
+ *   freqs: [rotary_dim / 2] device words of gdn_rope_freqs.  q_out may be q and k_out may be
+ *   k (with equal strides); otherwise nothing overlaps.  Arithmetic in fp32. */
+gdn_status gdn_rope(const void *q, const void *k, const int64_t *positions, const uint64_t *freqs, int32_t dtype,
+                    int32_t n_tok, int32_t Hq, int32_t Hk, int32_t D, int32_t rotary_dim, int64_t q_stride,
+                    int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, float scale, uint32_t flags,
+                    void *q_out, void *k_out, void *stream);
+
+/* The new tokens' k and v into the cache, with the rotary step on q and k on the way: new token
+ * i of sequence s takes position p = seq_lens[s] - n_new + i (seq_lens counts the new tokens
+ * already), slot p % page_size of page page_table[s][p / page_size].  A token whose p is
+ * negative is not stored.
+ *   k, v: [n_tok, Hkv, D];  q: [n_tok, Hq, D] or NULL (then q_out is unused);
+ *   q_out: [n_tok, Hq, D] dense, may be q when q is dense;  cu_seqlens: [n_seqs + 1] offsets of the
+ *   new tokens, or NULL (one each, n_tok = n_seqs);  freqs NULL: no rotation (rotary_dim 0);
+ *   positions: [n_tok] int64 rotary positions, or NULL: p.  flags: GDN_FLAG_ROPE_INTERLEAVED.
+ *   workspace: at least 256 bytes, 256-byte aligned (the status word).
+ * Two sequences must not name the same page for new tokens. */
+gdn_status gdn_kv_append(const void *q, const void *k, const void *v, const int64_t *positions,
+                         const uint64_t *freqs, int32_t rotary_dim, float scale, uint32_t flags,
+                         const int32_t *page_table, const int32_t *seq_lens, const int32_t *cu_seqlens,
+                         const gdn_cache_shape *shape, void *q_out, void *k_cache, void *v_cache, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Attention of the new tokens over the paged cache, which holds them already (gdn_kv_append).
+ * New token i of sequence s sits at p = seq_lens[s] - n_new + i and sees the positions
+ * max(0, p - window + 1) .. p (window = 0: 0 .. p):
+ *     o[t, h] = sum_j softmax_j(scale <q[t, h], k_j>) v_j,   lse[t, h] = log sum_j exp(scale <q[t, h], k_j>)
+ * A token that sees nothing (p < 0) gets o = 0 and lse = -inf.
+ *   q: [n_tok, Hq, D] (token stride shape->q_stride);  o: [n_tok, Hq, D] dense;  lse: [n_tok, Hq] fp32 or NULL
+ *   cu_seqlens: as for gdn_kv_append;  max_new: the host's bound on the new tokens of one
+ *   sequence (it picks the kernel and sizes the workspace; more new tokens are still right)
+ *   flags: GDN_FLAG_SIMT (the CUDA-core kernel), GDN_FLAG_TEST_NO_WAIT
+ *   workspace: gdn_paged_attn_workspace_bytes(shape, max_new), 256-byte aligned, not shared by
+ *   calls that may overlap; nothing in it has to be kept or cleared between calls.
+ * Scores, softmax and sums are fp32.  On the tensor-core path (bf16; D 64, 128 or 256; page_size
+ * a multiple of 8; 16-byte aligned pointers and strides) the softmax weights are rounded to
+ * bf16 before the product with v, and an infinity or NaN in v at a position of the
+ * sequence may reach its tile's earlier queries too (0 * inf); slots at or past seq_lens
+ * never do. */
+size_t gdn_paged_attn_workspace_bytes(const gdn_cache_shape *shape, int32_t max_new);
+gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *page_table,
+                          const int32_t *seq_lens, const int32_t *cu_seqlens, const gdn_cache_shape *shape,
+                          int32_t max_new, float scale, int32_t window, uint32_t flags, void *o, float *lse,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* The bookkeeping of the pages, all on the device: page_table [n_rows, max_pages], seq_lens
+ * [n_rows], refs [n_pages] (how many sequences hold a page; 0 = free).  Free pages are taken
+ * in rising order, so the results do not depend on scheduling.  The calls below check their
+ * lists on the device: a row outside [0, n_rows), a list that cannot be carried out, or too
+ * few free pages sets GDN_ERR_PAGES (a page outside the cache: GDN_ERR_BOUNDS) in the status
+ * word of `workspace` (gdn_pages_workspace_bytes(n_pages, n_rows) bytes, 256-byte aligned), and
+ * gdn_pages_grow and gdn_pages_fork then change nothing. */
+typedef struct {
+  int32_t *page_table, *seq_lens, *refs; /* device */
+  int32_t n_rows, max_pages;
+  int64_t table_stride; /* elements between rows of page_table; 0 = max_pages */
+  int32_t n_pages, page_size; /* n_pages < 2^21 */
+} gdn_page_tables;
+
+/* The caches that the pages index: n_pools device arrays (a HOST array of their addresses, at
+ * most GDN_MAX_POOLS: the k and v caches of every layer that shares the tables), page i of each
+ * at byte i * page_stride with page_bytes contiguous bytes. */
+#define GDN_MAX_POOLS 256
+typedef struct {
+  void *const *pools;
+  int32_t n_pools;
+  int64_t page_bytes, page_stride;
+} gdn_page_pools;
+
+size_t gdn_pages_workspace_bytes(int32_t n_pages, int32_t n_rows);
+
+/* Sequence seqs[i] (i < n, no row twice) grows to new_lens[i] tokens (not below its seq_lens):
+ * the pages it lacks come from the free ones, sequence after sequence, and seq_lens follows. */
+gdn_status gdn_pages_grow(const gdn_page_tables *t, const int32_t *seqs, const int32_t *new_lens, int32_t n,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Sequence seqs[i] (i < n; a row named twice counts once) gives its pages back: their refs go
+ * down by one, its table entries become -1 and its length 0.  Entries of -1 are skipped. */
+gdn_status gdn_pages_free(const gdn_page_tables *t, const int32_t *seqs, int32_t n, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Row children[i] (empty: length 0, no row twice, none of the parents) becomes a copy of row parents[i]:
+ * it shares the parent's full pages (refs up by one) and gets a free page, with the contents
+ * copied in every pool, for a part-filled last one.  Children are served in order. */
+gdn_status gdn_pages_fork(const gdn_page_tables *t, const int32_t *parents, const int32_t *children, int32_t n,
+                          const gdn_page_pools *pools, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The live pages (refs > 0, L of them) come together in pages [0, L): those at or past L move, in
+ * rising order, into the free ones below it, in every pool; tables and refs follow.  Pages below L
+ * stay. */
+gdn_status gdn_pages_compact(const gdn_page_tables *t, const gdn_page_pools *pools, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Page src[i] over page dst[i] in every pool, i < n (device int32 lists; no page both in src and
+ * in dst, none twice in dst; pairs with a page outside [0, n_pages) set GDN_ERR_BOUNDS and are skipped). */
+gdn_status gdn_pages_copy(const int32_t *src, const int32_t *dst, int32_t n, int32_t n_pages,
+                          const gdn_page_pools *pools, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
