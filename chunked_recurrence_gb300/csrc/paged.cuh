@@ -67,19 +67,24 @@ struct Item {
   bool ok;
 };
 
-GDN_HD Item item_at(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R, int32_t KT, int32_t window) {
+// The sequence whose slots hold `slot`.
+GDN_HD int32_t slot_seq(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R) {
   int32_t lo = 0, hi = q.n_seqs - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi + 1) >> 1;
     if (slot_base(q, mid, G, R) <= slot) lo = mid; else hi = mid - 1;
   }
+  return lo;
+}
+
+GDN_HD Item item_of(const PagedSeqs &q, int32_t s, int32_t slot, int32_t G, int32_t R, int32_t KT, int32_t window) {
   Item it;
-  const SeqSpan sp = seq_span(q, lo);
-  it.s = lo;
+  const SeqSpan sp = seq_span(q, s);
+  it.s = s;
   it.t0 = sp.t0;
   it.ok = sp.ok;
   it.first = sp.len - sp.n_new;
-  const int64_t row0 = (int64_t)(slot - slot_base(q, lo, G, R)) * R, all = (int64_t)sp.n_new * G;
+  const int64_t row0 = (int64_t)(slot - slot_base(q, s, G, R)) * R, all = (int64_t)sp.n_new * G;
   it.row0 = (int32_t)(row0 < all ? row0 : all);
   it.rows = (int32_t)(row0 < 0 || row0 >= all ? 0 : all - row0 < R ? all - row0 : R);
   it.lo = it.hi = it.tile0 = it.n_tiles = 0;
@@ -97,9 +102,15 @@ GDN_HD Item item_at(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R, int3
   }
   return it;
 }
+GDN_HD Item item_at(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R, int32_t KT, int32_t window) {
+  return item_of(q, slot_seq(q, slot, G, R), slot, G, R, KT, window);
+}
 
-// Units of work of an item and kv head: its tiles, or one unit that writes the rows' zeros.
-GDN_HD int32_t item_units(const Item &it) { return it.rows <= 0 ? 0 : it.n_tiles > 0 ? it.n_tiles : 1; }
+// Units of work of an item and kv head: its tiles, and `over` more in front of them for what
+// every item costs whatever its length (its queries in, its output out).
+GDN_HD int32_t item_units(const Item &it, int32_t over) { return it.rows <= 0 ? 0 : it.n_tiles + over; }
+// Tile that unit u (0 .. units) begins with, counted from the item's first.
+GDN_HD int32_t unit_tile(int32_t u, int32_t over) { return u > over ? u - over : 0; }
 
 // Block b's share [begin, end) of `total` units over `blocks` blocks.
 GDN_HD int64_t share_begin(int64_t total, int32_t b, int32_t blocks) { return total / blocks * b + total % blocks * b / blocks; }

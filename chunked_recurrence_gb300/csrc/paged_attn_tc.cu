@@ -29,6 +29,7 @@
 #include <numeric>
 
 #include "common.cuh"
+#include "conv_tap.cuh"
 #include "paged_attn.cuh"
 #include "sm100.cuh"
 
@@ -43,16 +44,20 @@ constexpr uint32_t kSpin = 1u << 22; // polls of a wait before it gives up
 constexpr int kData = 224 * 1024;    // Q and the ring
 constexpr float kLag = 8.f;          // m may lag by this many powers of two
 
+constexpr int kOver = 2;              // units an item costs beyond its tiles
+
 template <int D, int NQ>
 struct Cfg {
-  static constexpr int R = 128 * NQ;
+  static constexpr int R = 128 * NQ;                    // rows of TMEM lanes; an item fills tile_rows() of each 128
   static constexpr int KG = D == 256 ? 2 : 1;           // granules a K (by columns) or V (by positions) tile
   static constexpr int kGran = KT * D * 2 / KG;         // bytes
   static constexpr int kQ = R * D * 2;
   static constexpr int kSlots = (kData - kQ) / kGran;
   static constexpr int kPanelsK = (D / KG) / 64;        // 64-column panels of a K granule: KT rows each
   static constexpr int kRowsV = KT / KG, kPanelsV = D / 64;
-  static constexpr int kThreads = 128 * NQ + 64;
+  // softmax warpgroups, then the TMA and MMA warps; with two tiles a whole warpgroup for those, so that the
+  // registers can be split between the warpgroups
+  static constexpr int kThreads = NQ == 2 ? 384 : 192;
   static constexpr uint32_t kO = 256;                   // first TMEM column of O
 };
 
@@ -63,7 +68,7 @@ struct TcArgs {
   float *lse;
   const int32_t *table;
   int64_t table_stride, q_stride;
-  int32_t G, Hkv, page_size, box, max_pages, n_pages, window;
+  int32_t G, RT, Hkv, page_size, box, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole tokens
   float c;  // scale log2 e
   float *part, *part_ml;
   int4 *meta;
@@ -72,11 +77,11 @@ struct TcArgs {
 };
 
 struct Ctl {
-  uint64_t full[16], empty[16], sfull[2], pready[2], odone[2], qready[2], drain;
+  uint64_t full[16], empty[16], sfull[2], pready[2][2], odone[2], qfull[2], qfree[2], drain;
   uint32_t tmem;
   volatile int abort;
   int64_t sum[12];
-  int start_slot, start_h, start_j;
+  int start_slot, start_seq, start_h, start_u;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
@@ -139,34 +144,95 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, kSpin, abort));
 }
 
-// A block's share of the line of work, piece by piece: `n` units from unit `j` of an item and head.
+// A block's share of the line of work, piece by piece: `n` tiles from tile `j` of an item and
+// head (n = 0 for one without tiles, whose rows get zeros).
 struct Walk {
   Item it;
-  int slot, h, j, n, units;
+  int slot, h, j, n, u, units;
   int64_t left;
 };
-__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slot, int h, int j, int64_t left) {
-  w.slot = slot, w.h = h, w.j = j, w.left = left;
-  if (left <= 0) return false;
-  w.it = item_at(a.seqs, slot, a.G, R, KT, a.window);
-  w.units = item_units(w.it);
-  w.n = (int)min((int64_t)(w.units - j), left);
-  return w.n > 0;
+// cuts the next piece at unit u of the item; false where it holds nothing to do
+__device__ __forceinline__ bool walk_cut(Walk &w) {
+  const int end = (int)min((int64_t)w.units, w.u + w.left);
+  w.left -= end - w.u;
+  w.j = unit_tile(w.u, kOver);
+  w.n = unit_tile(end, kOver) - w.j;
+  return w.it.n_tiles > 0 ? w.n > 0 : w.u == 0;
 }
 __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int slots) {
-  w.left -= w.n;
-  if (w.left <= 0) return false;
-  w.j = 0;
-  if (++w.h == a.Hkv) {
-    w.h = 0;
-    do {
-      if (++w.slot >= slots) return false;
-      w.it = item_at(a.seqs, w.slot, a.G, R, KT, a.window);
-      w.units = item_units(w.it);
-    } while (w.units == 0);
+  while (w.left > 0) {
+    w.u = 0;
+    if (++w.h == a.Hkv) {
+      w.h = 0;
+      do {
+        if (++w.slot >= slots) return false;
+        int s = w.it.s;
+        while (s + 1 < a.seqs.n_seqs && slot_base(a.seqs, s + 1, a.G, R) <= w.slot) ++s;
+        w.it = item_of(a.seqs, s, w.slot, a.G, R, KT, a.window);
+        w.units = item_units(w.it, kOver);
+      } while (w.units == 0);
+    }
+    if (walk_cut(w)) return true;
   }
-  w.n = (int)min((int64_t)w.units, w.left);
-  return true;
+  return false;
+}
+__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, int slot, int seq, int h, int u,
+                                           int64_t left) {
+  w.slot = slot, w.h = h, w.u = u, w.left = left;
+  w.it = item_of(a.seqs, seq, slot, a.G, R, KT, a.window);
+  w.units = item_units(w.it, kOver);
+  return walk_cut(w) || walk_next(a, w, R, slots);
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// after tcgen05.wait::ld: no use of the loaded registers moves above it
+template <int N>
+__device__ __forceinline__ void settled(float (&v)[N], int from, int n) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i >= from && i < from + n) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// largest of n values (n a multiple of 8), four chains
+template <int N>
+__device__ __forceinline__ float max_of(const float (&v)[N], int from, int n, float start) {
+  float m[4] = {start, start, start, start};
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    if (i >= from && i < from + n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = max3(m[k], v[i + 2 * k], v[i + 2 * k + 1]);
+    }
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// 4 x 4 transpose of 16-byte pieces among four neighbouring lanes: lane i's piece k becomes lane k's piece i
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto swap = [&](uint4 &a, uint4 &b, int x) {  // with lane ^ x: the lower lane gives b, the upper one a
+    const bool up = lane & x;
+    uint4 give = up ? a : b, got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, x);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, x);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, x);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, x);
+    if (up) a = got; else b = got;
+  };
+  swap(v[0], v[1], 1);
+  swap(v[2], v[3], 1);
+  swap(v[0], v[2], 2);
+  swap(v[1], v[3], 2);
 }
 
 // Granules of a piece of n tiles in ring order.  NQ = 2: K0 V0 K1 V1 ...; NQ = 1: K0 K1 V0 K2 V1 ... V(n-1).
@@ -181,8 +247,8 @@ __device__ __forceinline__ uint32_t idx_v(uint32_t base, int j, int n) {
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const TcArgs a) {
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const TcArgs a) {
   using C = Cfg<D, NQ>;
   constexpr int KG = C::KG, kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -190,20 +256,54 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = sm + C::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarps = 4 * NQ + 2;
+  constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarps = C::kThreads / 32;
+  launch_dependents();
 
-  // ---- this block's share: units of every slot summed, then the slot its first unit lies in
-  const int slots = (int)item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, C::R);
+  if (tid == 0) {
+    ctl.abort = 0;
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.sfull[i], 1);
+      mbar_init(&ctl.pready[i][0], 4);  // the two halves of P apart: a warp may be done with both
+      mbar_init(&ctl.pready[i][1], 4);  // before another is with its first
+      mbar_init(&ctl.odone[i], 1);
+      mbar_init(&ctl.qfull[i], 1);
+      mbar_init(&ctl.qfree[i], 1);
+    }
+    mbar_init(&ctl.drain, 1);
+    fence_mbar_init();
+  }
+
+  // ---- this block's share: the units of all slots summed, then the slot its first unit lies in.  The lengths and
+  // offsets go through shared memory (where the ring will be), so that the search in them does not wait on L2.
+  const int R = a.RT * NQ;
+  const int slots = (int)item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, R);
+  PagedSeqs sq = a.seqs;
+  if (a.seqs.n_seqs < C::kSlots * C::kGran / 8 - 1) {
+    int32_t *len_s = reinterpret_cast<int32_t *>(ring), *cu_s = len_s + a.seqs.n_seqs;
+    for (int s = tid; s <= a.seqs.n_seqs; s += C::kThreads) {
+      if (s < a.seqs.n_seqs) len_s[s] = a.seqs.seq_lens[s];
+      if (a.seqs.cu) cu_s[s] = a.seqs.cu[s];
+    }
+    sq.seq_lens = len_s;
+    if (a.seqs.cu) sq.cu = cu_s;
+    __syncthreads();
+  }
   int64_t mine = 0;
+  int keep = 0;  // units of this thread's first slot
   for (int s = tid; s < slots; s += C::kThreads) {
-    const Item it = item_at(a.seqs, s, a.G, C::R, KT, a.window);
+    const Item it = item_at(sq, s, a.G, R, KT, a.window);
     if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
-    mine += (int64_t)item_units(it) * a.Hkv;
+    const int units = item_units(it, kOver);
+    if (s == tid) keep = units;
+    mine += (int64_t)units * a.Hkv;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) ctl.sum[warp] = mine;
-  if (tid == 0) ctl.abort = 0, ctl.start_slot = -1;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
@@ -218,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   int64_t before = 0;
   for (int base = 0; base < slots; base += C::kThreads) {
     const int s = base + tid;
-    const int units = s < slots ? item_units(item_at(a.seqs, s, a.G, C::R, KT, a.window)) : 0;
+    const int units = base == 0 ? keep : s < slots ? item_units(item_at(sq, s, a.G, R, KT, a.window), kOver) : 0;
     const int64_t cost = (int64_t)units * a.Hkv;
     int64_t x = cost;
 #pragma unroll
@@ -238,33 +338,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const int64_t from = before + upto + x - cost;  // units before this slot
     if (cost > 0 && begin >= from && begin < from + cost) {
       ctl.start_slot = s;
+      ctl.start_seq = slot_seq(sq, s, a.G, R);
       ctl.start_h = (int)((begin - from) / units);
-      ctl.start_j = (int)((begin - from) % units);
+      ctl.start_u = (int)((begin - from) % units);
     }
     before += all;
     if (before > begin) break;
   }
 
-  // ---- barriers and TMEM
-  if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.full[i], 1);
-      mbar_init(&ctl.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.sfull[i], 1);
-      mbar_init(&ctl.pready[i], 4);
-      mbar_init(&ctl.odone[i], 1);
-      mbar_init(&ctl.qready[i], 4);
-    }
-    mbar_init(&ctl.drain, 1);
-    fence_mbar_init();
-  }
   if (warp == kWarpMma) {
     tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
+  fence_proxy_async_smem();  // the lengths' reads of the ring end before copies into it
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = ctl.tmem;
@@ -273,22 +360,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     *abort_flag = 1;
     set_status(a.status, GDN_ERR_TIMEOUT);
   };
+  uint32_t issued = 0, q_issued[2] = {0, 0};  // granules and Q tiles (the TMA warp's count)
   Walk w;
-  uint32_t issued = 0;  // granules (the TMA warp's count)
-  bool more = walk_begin(a, w, C::R, ctl.start_slot, ctl.start_h, ctl.start_j, end - begin);
+  bool more = false;
 
   if (warp == kWarpTma) {
-    // ================================================= K and V granules, page by page
+    // ================================================= Q tiles; K and V granules, page by page
+    if (NQ == 2) set_regs_down<88>();
+    more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
     auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, int rows, int panels, uint32_t panel_bytes, int col0,
                     const int32_t *row) {
       const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
-      if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
-        ok = false;
-        return;
-      }
       const int nb = rows / a.box;
       int page = -1, at = 0;
       if (lane < nb) {
@@ -301,6 +386,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
       }
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+      if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
+        ok = false;
+        return;
+      }
       if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes * panels);
       __syncwarp();
       if (page >= 0)
@@ -310,6 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       issued = idx + 1;
     };
     if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -329,7 +419,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               load(&tm_v, idx_v<NQ, KG>(base, j, w.n) + g, first + j * KT + g * C::kRowsV, C::kRowsV, C::kPanelsV,
                    C::kRowsV * 128, 0, row);
         };
-        load_k(0);
+        // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
+        // sequences that come along are never used
+        const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
+        for (int t = 0; t < nt && ok; ++t) {
+          if (!warp_wait(&ctl.qfree[t], (q_issued[t] & 1) ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl.qfull[t], a.RT * D * 2);
+            for (int p = 0; p < D / 64; ++p)
+              tma_load_3d(sm + t * 128 * D * 2 + p * 16384, &tm_q, &ctl.qfull[t], 64 * p, w.h * a.G,
+                          w.it.t0 + w.it.row0 / a.G + t * (a.RT / a.G));
+          }
+          __syncwarp();
+          ++q_issued[t];
+        }
+        if (ok) load_k(0);
         for (int j = 0; j < w.n && ok; ++j) {
           if (NQ == 1 && j + 1 < w.n) load_k(j + 1);
           if (ok) load_v(j);
@@ -337,19 +444,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
         base += 2 * KG * w.n;
       }
-      more = walk_next(a, w, C::R, slots);
+      more = walk_next(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
   } else if (warp == kWarpMma) {
     // ================================================= MMAs
+    if (NQ == 2) set_regs_down<88>();
     if (lane == 0) {
+      more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
       const uint32_t id_s = idesc_bf16(128, KT, false, false);
       const uint32_t id_o = idesc_bf16(128, D, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint64_t d_k = smem_desc(smem_u32(ring), 16, 1024, 2);
       const uint64_t d_v = smem_desc(smem_u32(ring), C::kRowsV * 128, 1024, 2);
       uint32_t base = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // steps: P tiles consumed, per TMEM slot
-      uint32_t total_steps = 0;                         // NQ = 1: the S slots alternate across pieces
+      uint32_t total_steps = 0;                                  // NQ = 1: the S slots alternate across pieces
       bool ok = !a.no_wait;
       auto wait_full = [&](uint32_t idx) {
         if (ok && !mbar_wait_spin(&ctl.full[idx % kSlots], (idx / kSlots) & 1, kSpin, abort_flag)) ok = false;
@@ -372,33 +481,33 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
         umma_commit(&ctl.sfull[slot]);
       };
-      // O[t] (+)= P[slot] V(j)
+      // O[t] (+)= P[slot] V(j), the first half of the positions as soon as their P is there
       auto issue_o = [&](int t, int slot, int j) {
-        if (!mbar_wait_spin(&ctl.pready[slot], steps[slot] & 1, kSpin, abort_flag)) {
-          ok = false;
-          return;
-        }
-        ++steps[slot];
-        tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < KG; ++g) {
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait_spin(&ctl.pready[slot][half], steps[slot] & 1, kSpin, abort_flag)) {
+            ok = false;
+            return;
+          }
+          const int g = KG == 2 ? half : 0;
           const uint32_t idx = idx_v<NQ, KG>(base, j, w.n) + g;
-          wait_full(idx);
+          if (KG == 2 || half == 0) wait_full(idx);
           if (!ok) return;
           tc_fence_after();
           const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < C::kRowsV / 16; ++ks)
-            umma_ts(tm + C::kO + t * D, tm + slot * 128 + (g * (C::kRowsV / 16) + ks) * 8, dv + ((ks * 2048) >> 4), id_o,
-                    j > 0 || g > 0 || ks > 0);
-          if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(tm + C::kO + t * D, tm + slot * 128 + (half * 4 + ks) * 8,
+                    dv + (((KG == 2 ? ks : half * 4 + ks) * 2048) >> 4), id_o, j > 0 || half > 0 || ks > 0);
+          if (NQ == 1 && (KG == 2 || half == 1)) umma_commit(&ctl.empty[idx % kSlots]);
         }
+        ++steps[slot];
       };
       while (more && ok) {
         const int n = w.it.n_tiles > 0 ? w.n : 0;
         if (n > 0) {
-          const int nt = NQ == 2 && w.it.rows > 128 ? 2 : 1;
-          for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_spin(&ctl.qready[t], pieces[t]++ & 1, kSpin, abort_flag);
+          const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
+          for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_spin(&ctl.qfull[t], pieces[t]++ & 1, kSpin, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (NQ == 2) {
@@ -419,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           base += 2 * KG * n;
         }
-        more = walk_next(a, w, C::R, slots);
+        more = walk_next(a, w, R, slots);
       }
       if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
         if (!ok) fail();
@@ -427,50 +536,38 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         mbar_wait(&ctl.drain, 0, kSpin);
       }
     }
+  } else if (warp > kWarpMma) {
+    if (NQ == 2) set_regs_down<88>();
   } else {
     // ================================================= softmax: a thread owns a query row
+    if (NQ == 2) set_regs_up<208>();
+    more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lq = (uint32_t)(quarter * 32) << 16;
     const float lag = kLag / a.c;
+    const uint64_t c2 = f2_pack(a.c, a.c);
     uint32_t base = 0, steps = 0, sphase[2] = {0, 0}, pieces = 0;
     int cont = 0, head = 0, head_slot = 0, head_h = 0;
     bool ok = true;
     while (more && ok) {
       const Item &it = w.it;
-      const int rr = t * 128 + r;
-      const bool valid = rr < it.rows;
+      const int rr = t * a.RT + r;
+      const bool valid = r < a.RT && rr < it.rows;
       const int row = it.row0 + (valid ? rr : 0), i = row / a.G, g = row - i * a.G;
-      const int64_t tok = it.t0 + i, out = tok * (a.G * a.Hkv) + w.h * a.G + g;
-      const bool begins = w.j == 0, ends = w.j + w.n == w.units;
+      const int64_t out = (int64_t)(it.t0 + i) * (a.G * a.Hkv) + w.h * a.G + g;
       if (it.n_tiles == 0) {  // rows that see nothing
         if (valid) {
           for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.o + out * D + d) = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[out] = -INFINITY;
         }
-        more = walk_next(a, w, C::R, slots);
+        more = walk_next(a, w, R, slots);
         continue;
       }
-      const int n = w.n, nt = it.rows > 128 ? 2 : 1;
+      const int n = w.n, nt = NQ == 2 && it.rows > a.RT ? 2 : 1;
+      const bool begins = w.j == 0, ends = w.j + w.n == it.n_tiles;
       const int first = (it.tile0 + w.j) * KT;
-      const bool live = t < nt && t * 128 + quarter * 32 < it.rows;  // this warp has a row
-      // ---- this row tile's queries, 16-byte pieces along a row across the lanes
-      {
-        constexpr int kL = D / 8, kRowsIt = 32 / kL > 0 ? 32 / kL : 1;
-        const int64_t off = valid ? tok * a.q_stride + (int64_t)(w.h * a.G + g) * D : -1;
-        uint8_t *qs = sm + t * 128 * D * 2;
-        if (t < nt)
-#pragma unroll 4
-          for (int x = 0; x < 32; x += kRowsIt) {
-            const int rl = x + (kL < 32 ? lane / kL : 0), ch = kL < 32 ? lane % kL : lane;
-            const int64_t of = __shfl_sync(0xffffffffu, off, rl);
-            const uint4 v = of >= 0 ? *reinterpret_cast<const uint4 *>(a.q + of + ch * 8) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * 16384 + sw128_off(quarter * 32 + rl, (ch & 7) * 8)) = v;
-          }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (t < nt && lane == 0) mbar_arrive(&ctl.qready[t]);
-      }
       if (t < nt) {
+        const bool live = t * a.RT + quarter * 32 < it.rows && quarter * 32 < a.RT;  // this warp has a row
         const int p = it.first + i;
         const int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
@@ -484,9 +581,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           ++sphase[slot];
           tc_fence_after();
           // S is there: K(j) has been read, and (NQ = 2) V(j - 1), whose product came before it
-          if (releases && tid == t * 128) {
-            for (int g2 = 0; g2 < KG; ++g2) mbar_arrive(&ctl.empty[(idx_k<NQ, KG>(base, j) + g2) % kSlots]);
-            if (NQ == 2 && j > 0) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, j - 1, n) % kSlots]);
+          if (tid == t * 128) {
+            if (releases) {
+              for (int g2 = 0; g2 < KG; ++g2) mbar_arrive(&ctl.empty[(idx_k<NQ, KG>(base, j) + g2) % kSlots]);
+              if (NQ == 2 && j > 0) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, j - 1, n) % kSlots]);
+            }
+            if (j == n - 1) mbar_arrive(&ctl.qfree[t]);
           }
           const int pos = first + j * KT;
           if (t == 0 && (pos < it.lo || pos + KT > it.hi)) {
@@ -507,18 +607,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             fence_proxy_async_smem();
           }
           if (live) {
+            const uint32_t ts = tm + lq + slot * 128;
             float s[KT];
 #pragma unroll
-            for (int x = 0; x < KT; x += 32)
-              tmem_ld32u(tm + lq + slot * 128 + x, reinterpret_cast<uint32_t *>(s) + x);
+            for (int x = 0; x < KT; x += 32) tmem_ld32u(ts + x, reinterpret_cast<uint32_t *>(s) + x);
             tmem_wait_ld();
+            settled(s, 0, KT);
             if (pos + KT > hi || pos < lo) {
 #pragma unroll
               for (int x = 0; x < KT; ++x) s[x] = pos + x < hi && pos + x >= lo ? s[x] : -INFINITY;
             }
-            float mx = s[0];
-#pragma unroll
-            for (int x = 1; x < KT; ++x) mx = fmaxf(mx, s[x]);
+            const float mx = max_of(s, 0, KT, -INFINITY);
             if (j == 0) {
               m = mx;
             } else if (__any_sync(0xffffffffu, mx > m + lag)) {
@@ -532,35 +631,54 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               const float f = m == top ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * a.c);
               m = top;
               l *= f;
-#pragma unroll
+#pragma unroll 1
               for (int x = 0; x < D; x += 32) {
                 uint32_t u[32];
                 tmem_ld32u(tm + lq + C::kO + t * D + x, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(__uint_as_float(u[y]) * f);
+                for (int y = 0; y < 32; ++y) {
+                  asm volatile("" : "+r"(u[y]));
+                  u[y] = __float_as_uint(__uint_as_float(u[y]) * f);
+                }
                 tmem_st32u(tm + lq + C::kO + t * D + x, u);
               }
             }
             const float mc = m == -INFINITY ? 0.f : m * a.c;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t mc2 = f2_pack(-mc, -mc);
+            uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-            for (int x = 0; x < KT; x += 64) {
+            for (int half = 0; half < 2; ++half) {
               uint32_t pk[32];
 #pragma unroll
-              for (int y = 0; y < 64; y += 2) {
-                const float p0 = ex2(fmaf(s[x + y], a.c, -mc)), p1 = ex2(fmaf(s[x + y + 1], a.c, -mc));
-                sum[(y >> 1) & 3] += p0 + p1;
+              for (int y = 0; y < 64; y += 4) {
+                float p0, p1, p2, p3;
+                f2_unpack(f2_fma(f2_pack(s[half * 64 + y], s[half * 64 + y + 1]), c2, mc2), p0, p1);
+                f2_unpack(f2_fma(f2_pack(s[half * 64 + y + 2], s[half * 64 + y + 3]), c2, mc2), p2, p3);
+                p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+                sum0 = f2_add(sum0, f2_pack(p0, p1));
+                sum1 = f2_add(sum1, f2_pack(p2, p3));
                 pk[y >> 1] = bf16x2(p0, p1);
+                pk[(y >> 1) + 1] = bf16x2(p2, p3);
               }
-              tmem_st32u(tm + lq + slot * 128 + (x >> 1), pk);
+              tmem_st32u(ts + half * 32, pk);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.pready[slot][half]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
+            float s0, s1, s2, s3;
+            f2_unpack(sum0, s0, s1);
+            f2_unpack(sum1, s2, s3);
+            l += (s0 + s1) + (s2 + s3);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ctl.pready[slot][0]);
+              mbar_arrive(&ctl.pready[slot][1]);
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.pready[slot]);
         }
         // ---- the last product done: O / l, or the piece for the join
         if (ok) {
@@ -574,39 +692,52 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           tc_fence_after();
         }
         if (ok && live) {
-          const bool whole = begins && ends;
-          const int which = 2 * blockIdx.x + (begins ? 1 : 0);
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          float *pp = a.part + ((int64_t)which * C::R + rr) * D;
+          const uint32_t to = tm + lq + C::kO + t * D;
+          if (begins && ends) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // rows of this lane's quad, -1: none
+            int64_t rows4[4];
 #pragma unroll
-          for (int x = 0; x < D; x += 32) {
-            uint32_t u[32];
-            tmem_ld32u(tm + lq + C::kO + t * D + x, u);
-            tmem_wait_ld();
-            if (valid) {
-              if (whole) {
+            for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(0xffffffffu, valid ? out : -1, (lane & ~3) + k);
+#pragma unroll 2
+            for (int x = 0; x < D; x += 32) {
+              uint32_t u[32];
+              tmem_ld32u(to + x, u);
+              tmem_wait_ld();
+              uint4 v[4];
 #pragma unroll
-                for (int y = 0; y < 32; y += 8) {
-                  uint4 v;
-                  uint32_t *vv = reinterpret_cast<uint32_t *>(&v);
+              for (int y = 0; y < 4; ++y) {
+                uint32_t *vv = reinterpret_cast<uint32_t *>(&v[y]);
 #pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    vv[z] = bf16x2(__uint_as_float(u[y + 2 * z]) * inv, __uint_as_float(u[y + 2 * z + 1]) * inv);
-                  *reinterpret_cast<uint4 *>(a.o + out * D + x + y) = v;
+                for (int z = 0; z < 4; ++z) {
+                  asm volatile("" : "+r"(u[8 * y + 2 * z]), "+r"(u[8 * y + 2 * z + 1]));
+                  vv[z] = bf16x2(__uint_as_float(u[8 * y + 2 * z]) * inv, __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
                 }
-              } else {
+              }
+              quad_transpose(v);  // now piece k is of row k of the quad, columns 8 (lane % 4) ..
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (rows4[k] >= 0) *reinterpret_cast<uint4 *>(a.o + rows4[k] * D + x + (lane & 3) * 8) = v[k];
+            }
+            if (valid && a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
+          } else {
+            // the piece as [column / 4][row] fours, so that neighbouring rows lie side by side
+            const int64_t which = 2 * blockIdx.x + (begins ? 1 : 0);
+            uint4 *pp = reinterpret_cast<uint4 *>(a.part) + which * (C::R * D / 4) + t * 128 + r;
+#pragma unroll 2
+            for (int x = 0; x < D; x += 32) {
+              uint32_t u[32];
+              tmem_ld32u(to + x, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) asm volatile("" : "+r"(u[y]));
+              if (valid)
 #pragma unroll
                 for (int y = 0; y < 32; y += 4)
-                  *reinterpret_cast<uint4 *>(pp + x + y) = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
-              }
+                  pp[(x + y) / 4 * C::R] = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
             }
-          }
-          if (valid) {
-            if (whole) {
-              if (a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
-            } else {
-              *reinterpret_cast<float2 *>(a.part_ml + ((int64_t)which * C::R + rr) * 2) = make_float2(m * a.c, l);
-            }
+            if (valid)
+              *reinterpret_cast<float2 *>(a.part_ml + (which * C::R + t * 128 + r) * 2) = make_float2(m * a.c, l);
           }
         }
         tc_fence_before();
@@ -615,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       base += 2 * KG * n;
       if (!begins) cont = ends ? 2 : 1;
       else if (!ends) head = 1, head_slot = w.slot, head_h = w.h;
-      more = walk_next(a, w, C::R, slots);
+      more = walk_next(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
     if (tid == 0) a.meta[blockIdx.x] = make_int4(cont, head, head_slot, head_h);
@@ -624,55 +755,74 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {  // a wait gave up: copies in flight land before the block's memory goes
-    if (warp == kWarpTma)
+    if (warp == kWarpTma) {
       for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
         mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, kSpin);
+      for (int t = 0; t < NQ; ++t)
+        if (q_issued[t] > 0) mbar_wait(&ctl.qfull[t], (q_issued[t] - 1) & 1, kSpin);
+    }
     __syncthreads();
   }
   if (warp == kWarpMma) tmem_dealloc(tm, 512);
 }
 
 // Items that lie in several blocks' shares: block b's last piece begins one, b + 1's first
-// continues it, until a first piece ends it.  A warp takes a row.
+// continues it, until a first piece ends it.  A block takes 32 rows, a lane a row, a warp an eighth
+// of the columns; the rows go out through shared memory, whole rows at a time.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
-  constexpr int R = Cfg<D, NQ>::R, kE = D / 32;
+  constexpr int R = Cfg<D, NQ>::R, kV = D / 32;  // fours of columns a warp
+  __shared__ uint2 rows[32][D / 4 + 1];
+  grid_dependency_wait();
   const int4 me = a.meta[blockIdx.x];
   if (!me.y) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Item it = item_at(a.seqs, me.z, a.G, R, KT, a.window);
+  const Item it = item_at(a.seqs, me.z, a.G, a.RT * NQ, KT, a.window);
+  const int lr = blockIdx.y * 32 + lane, t = lr / 128, rr = t * a.RT + lr % 128;  // lane row, row of the item
+  const bool valid = lr % 128 < a.RT && rr < it.rows;
+  if (!__any_sync(0xffffffffu, valid)) return;  // the same for all warps
   int last = blockIdx.x + 1;
   while (last < blocks && a.meta[last].x == 1) ++last;
   if (last >= blocks) return;  // a share that gave up
-  for (int rr = blockIdx.y * 8 + warp; rr < it.rows; rr += gridDim.y * 8) {
-    auto at = [&](int b) { return (int64_t)(b == (int)blockIdx.x ? 2 * b + 1 : 2 * b) * R + rr; };
-    float top = -INFINITY;
-    for (int b = blockIdx.x + lane; b <= last; b += 32) top = fmaxf(top, a.part_ml[at(b) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float x[kE], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = 0.f;
+  auto at = [&](int b) { return (int64_t)(b == (int)blockIdx.x ? 2 * b + 1 : 2 * b); };
+  auto ml_of = [&](int b) {
+    return valid ? *reinterpret_cast<const float2 *>(a.part_ml + (at(b) * R + lr) * 2) : make_float2(-INFINITY, 0.f);
+  };
+  float top = -INFINITY;
 #pragma unroll 4
-    for (int b = blockIdx.x; b <= last; ++b) {
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at(b) * 2);
-      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
-      const float *p = a.part + at(b) * D + lane * kE;
+  for (int b = blockIdx.x; b <= last; ++b) top = fmaxf(top, ml_of(b).x);
+  float4 x[kV];
+  float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kE; e += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(p + e);
-        x[e] += f == 0.f ? 0.f : f * v.x;
-        x[e + 1] += f == 0.f ? 0.f : f * v.y;
+  for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int b = blockIdx.x; b <= last; ++b) {
+    const float2 ml = ml_of(b);
+    const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+    const float4 *p = reinterpret_cast<const float4 *>(a.part) + at(b) * (R * D / 4) + (warp * kV) * R + lr;
+    if (f != 0.f)
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        const float4 v = p[e * R];
+        x[e].x = fmaf(f, v.x, x[e].x);
+        x[e].y = fmaf(f, v.y, x[e].y);
+        x[e].z = fmaf(f, v.z, x[e].z);
+        x[e].w = fmaf(f, v.w, x[e].w);
       }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int row = it.row0 + rr, i = row / a.G, g = row - i * a.G;
-    const int64_t out = (int64_t)(it.t0 + i) * (a.G * a.Hkv) + me.w * a.G + g;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int e = 0; e < kE; e += 2)
-      *reinterpret_cast<uint32_t *>(a.o + out * D + lane * kE + e) = bf16x2(x[e] * inv, x[e + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  for (int e = 0; e < kV; ++e)
+    rows[lane][warp * kV + e] = make_uint2(bf16x2(x[e].x * inv, x[e].y * inv), bf16x2(x[e].z * inv, x[e].w * inv));
+  const int row = it.row0 + rr, i = row / a.G, g = row - i * a.G;
+  const int64_t out = valid ? (int64_t)(it.t0 + i) * (a.G * a.Hkv) + me.w * a.G + g : -1;
+  if (valid && warp == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  __syncthreads();
+  for (int q = warp; q < 32; q += 8) {
+    const int64_t to = __shfl_sync(0xffffffffu, out, q);
+    if (to >= 0)
+      for (int c = lane; c < D / 4; c += 32) *reinterpret_cast<uint2 *>(a.o + to * D + 4 * c) = rows[q][c];
   }
 }
 
@@ -701,13 +851,26 @@ bool make_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int bo
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [token][head][D] of q, boxes of 64 columns x the G heads of a group x as many tokens as fill RT rows
+bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int G, int RT) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)s.D, (cuuint64_t)s.Hq, (cuuint64_t)s.n_tok};
+  cuuint64_t strides[2] = {(cuuint64_t)s.D * 2, (cuuint64_t)s.q_stride * 2};
+  cuuint32_t b[3] = {64, (cuuint32_t)G, (cuuint32_t)(RT / G)}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, b, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int box_rows(const gdn_cache_shape &s) { return std::gcd(s.page_size, s.D == 256 ? 64 : KT); }
 
 template <int D, int NQ>
 gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {
   using C = Cfg<D, NQ>;
-  CUtensorMap mk, mv;
-  if (!make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box)) return GDN_ERR_CUDA;
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, a.q, s, a.G, a.RT) || !make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box))
+    return GDN_ERR_CUDA;
   char *w = (char *)a.status;
   a.meta = (int4 *)(w + 256);
   a.part_ml = (float *)(w + 256 + sizeof(int4) * 256);
@@ -715,8 +878,19 @@ gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs
   constexpr int smem = kData + 1024;
   if (cudaFuncSetAttribute(paged_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
-  paged_attn_kernel<D, NQ><<<kSms, C::kThreads, smem, st>>>(mk, mv, a);
-  paged_join_kernel<D, NQ><<<dim3(kSms, C::R / 32), 256, 0, st>>>(a, kSms);
+  paged_attn_kernel<D, NQ><<<kSms, C::kThreads, smem, st>>>(mq, mk, mv, a);
+  // the join starts up under the last blocks of the attention and waits for its end
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSms, C::R / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NQ>, (const TcArgs)a, kSms) != cudaSuccess)
+    return (void)cudaGetLastError(), GDN_ERR_CUDA;
   return launch_status();
 }
 
@@ -727,7 +901,7 @@ bool two_tiles(const gdn_cache_shape &s, int32_t max_new) {
 
 bool tc_shape(const gdn_cache_shape &s) {
   return s.dtype == GDN_BF16 && (s.D == 64 || s.D == 128 || s.D == 256) && s.page_size % 8 == 0 &&
-         s.page_size <= 1 << 20 && s.n_pages > 0;
+         s.page_size <= 1 << 20 && s.n_pages > 0 && s.Hq / s.Hkv <= 128;
 }
 
 }  // namespace
@@ -756,6 +930,7 @@ gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int3
   a.q = (const __nv_bfloat16 *)q, a.o = (__nv_bfloat16 *)o, a.lse = lse;
   a.table = table, a.table_stride = s.table_stride, a.q_stride = s.q_stride;
   a.G = s.Hq / s.Hkv, a.Hkv = s.Hkv;
+  a.RT = 128 / a.G * a.G;
   a.page_size = s.page_size, a.box = box_rows(s), a.max_pages = s.max_pages, a.n_pages = s.n_pages;
   a.window = window, a.c = scale_log2;
   a.status = (int32_t *)workspace;

@@ -63,7 +63,7 @@ def test_items_cover_every_row_once(host, G, R, window):
                 rows[(it["s"], r)] = slot
                 p = lens[it["s"]] - new[it["s"]] + r // G
                 seen += [(max(0, p - window + 1) if window else 0, p + 1)] if p >= 0 else []
-            assert it["units"] == max(1, it["n_tiles"])
+            assert it["units"] == it["n_tiles"] + 1
             if not seen:
                 assert it["lo"] == it["hi"] == it["n_tiles"] == 0
                 continue
