@@ -613,14 +613,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             for (int x = 0; x < KT; x += 32) tmem_ld32u(ts + x, reinterpret_cast<uint32_t *>(s) + x);
             tmem_wait_ld();
             settled(s, 0, KT);
-            if (pos + KT > hi || pos < lo) {
+            if (valid && (pos + KT > hi || pos < lo)) {  // rows past the item's are nobody's: no care for them
 #pragma unroll
               for (int x = 0; x < KT; ++x) s[x] = pos + x < hi && pos + x >= lo ? s[x] : -INFINITY;
             }
             const float mx = max_of(s, 0, KT, -INFINITY);
             if (j == 0) {
               m = mx;
-            } else if (__any_sync(0xffffffffu, mx > m + lag)) {
+            } else if (__any_sync(0xffffffffu, valid && mx > m + lag)) {
               // the products so far end before O is scaled
               if (NQ == 1) {
                 const uint32_t idx = idx_v<NQ, KG>(base, j - 1, n) + KG - 1;
@@ -767,49 +767,84 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 }
 
 // Items that lie in several blocks' shares: block b's last piece begins one, b + 1's first
-// continues it, until a first piece ends it.  A block takes 32 rows, a lane a row, a warp an eighth
-// of the columns; the rows go out through shared memory, whole rows at a time.
+// continues it, until a first piece ends it.  A block takes 32 rows, a lane a row.  The pieces'
+// maxima and sums are loaded at once, the warps taking turns; then a warp sums an eighth of the
+// columns over the pieces, and the rows go out through shared memory, whole rows at a time.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
   constexpr int R = Cfg<D, NQ>::R, kV = D / 32;  // fours of columns a warp
   __shared__ uint2 rows[32][D / 4 + 1];
+  __shared__ float weight[kSms][32], part[2][8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   const int4 me = a.meta[blockIdx.x];
   if (!me.y) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n = 0;  // pieces after the first
+  for (int base = blockIdx.x + 1;; base += 32) {
+    const int b = base + lane;
+    const uint32_t stop = __ballot_sync(0xffffffffu, b >= blocks || a.meta[b].x != 1);
+    if (stop) {
+      n += __ffs(stop);
+      break;
+    }
+    n += 32;
+  }
+  if ((int)blockIdx.x + n >= blocks || a.meta[blockIdx.x + n].x != 2) return;  // a share that gave up
   const Item it = item_at(a.seqs, me.z, a.G, a.RT * NQ, KT, a.window);
   const int lr = blockIdx.y * 32 + lane, t = lr / 128, rr = t * a.RT + lr % 128;  // lane row, row of the item
   const bool valid = lr % 128 < a.RT && rr < it.rows;
   if (!__any_sync(0xffffffffu, valid)) return;  // the same for all warps
-  int last = blockIdx.x + 1;
-  while (last < blocks && a.meta[last].x == 1) ++last;
-  if (last >= blocks) return;  // a share that gave up
-  auto at = [&](int b) { return (int64_t)(b == (int)blockIdx.x ? 2 * b + 1 : 2 * b); };
-  auto ml_of = [&](int b) {
-    return valid ? *reinterpret_cast<const float2 *>(a.part_ml + (at(b) * R + lr) * 2) : make_float2(-INFINITY, 0.f);
+  // piece i is slot 2 b + 1 of block b for the first, 2 (b + i) for the others
+  auto at = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
+  auto ml_of = [&](int i) {
+    return valid && i <= n ? *reinterpret_cast<const float2 *>(a.part_ml + (at(i) * R + lr) * 2)
+                           : make_float2(-INFINITY, 0.f);
   };
   float top = -INFINITY;
 #pragma unroll 4
-  for (int b = blockIdx.x; b <= last; ++b) top = fmaxf(top, ml_of(b).x);
-  float4 x[kV];
-  float sum = 0.f;
+  for (int i = warp; i <= n; i += 8) top = fmaxf(top, ml_of(i).x);
+  part[0][warp][lane] = top;
+  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, part[0][i][lane]);
+  float sum = 0.f;
 #pragma unroll 4
-  for (int b = blockIdx.x; b <= last; ++b) {
-    const float2 ml = ml_of(b);
+  for (int i = warp; i <= n; i += 8) {
+    const float2 ml = ml_of(i);
     const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
     sum = fmaf(f, ml.y, sum);
-    const float4 *p = reinterpret_cast<const float4 *>(a.part) + at(b) * (R * D / 4) + (warp * kV) * R + lr;
-    if (f != 0.f)
+    weight[i][lane] = f;
+  }
+  part[1][warp][lane] = sum;
+  __syncthreads();
+  sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        const float4 v = p[e * R];
-        x[e].x = fmaf(f, v.x, x[e].x);
-        x[e].y = fmaf(f, v.y, x[e].y);
-        x[e].z = fmaf(f, v.z, x[e].z);
-        x[e].w = fmaf(f, v.w, x[e].w);
-      }
+  for (int i = 0; i < 8; ++i) sum += part[1][i][lane];
+  float4 x[kV];
+#pragma unroll
+  for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAhead = 16 / kV;  // pieces in flight
+  for (int i0 = 0; i0 <= n; i0 += kAhead) {
+    float4 v[kAhead][kV];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float4 *p = reinterpret_cast<const float4 *>(a.part) + at(i0 + i) * (R * D / 4) + (warp * kV) * R + lr;
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        v[i][e] = i0 + i <= n && valid ? p[e * R] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float f = i0 + i <= n ? weight[i0 + i][lane] : 0.f;
+      if (f != 0.f)
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+          x[e].x = fmaf(f, v[i][e].x, x[e].x);
+          x[e].y = fmaf(f, v[i][e].y, x[e].y);
+          x[e].z = fmaf(f, v[i][e].z, x[e].z);
+          x[e].w = fmaf(f, v[i][e].w, x[e].w);
+        }
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll

@@ -9,10 +9,10 @@
 // exact for every 64-bit position; its top 32 bits (signed, so [-1/2, 1/2) turns) go to
 // sincospif.  A product in fp32 would be off by p * 2^-25 rad.
 //
-// Bound by HBM: every element is read and written once.  A block takes kTokens tokens; its
-// threads first put the tokens' cos and sin into shared memory (one sincospif a pair and
-// token, shared by all heads), then each thread keeps one place of a token's row (a 16-byte
-// vector of pair halves, or of elements that pass through) and walks the tokens.
+// Bound by HBM: every element is read and written once.  A block takes up to four tokens; its
+// threads put the tokens' cos and sin into shared memory (one sincospif a pair and token, shared
+// by all heads), and each thread keeps one place of a token's row (a 16-byte vector of pair halves,
+// or of elements that pass through).
 #include <math.h>
 
 #include "common.cuh"
@@ -46,9 +46,25 @@ struct alignas(VEC * sizeof(T)) Vec {
   T v[VEC];
 };
 
+// The sequence of a new token, by a whole warp: 32 probes a round.  The largest s with cu[s] <= t.
+__device__ __forceinline__ int seq_of_token_warp(const int32_t *cu, int n_seqs, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_seqs;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, s = lo + lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && cu[s] <= t);
+    const int k = below ? 31 - __clz(below) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
 // One place of a token's row: element offset of the vector in its head and what happens there.
 // VEC elements a vector; half layout: a rotary place holds VEC pairs (two vectors), interleaved:
 // VEC / 2 pairs (one vector; VEC = 1 then holds one pair as two vectors of one element).
+// A thread loads its place of all the block's tokens before the angles are worked out, so that
+// those (and the look-up of the slots) run under the loads.
 template <typename T, int VEC, bool APPEND, bool INTER, int TOK>
 __global__ void __launch_bounds__(kMaxThreads) rope_kernel(const RopeArgs a) {
   extern __shared__ float2 cs[];  // [TOK][rd / 2]
@@ -56,46 +72,22 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(const RopeArgs a) {
   __shared__ int64_t s_pos[TOK];
   const int t0 = blockIdx.x * TOK, nt = min(TOK, a.n_tok - t0);
   const int half = a.rd >> 1;
-  if ((int)threadIdx.x < nt) {
-    const int t = t0 + threadIdx.x;
-    int64_t p = a.positions ? a.positions[t] : 0;
-    if (APPEND) {
-      const int s = a.seqs.cu ? seq_of_token(a.seqs.cu, a.seqs.n_seqs, t) : t;
-      const SeqSpan sp = seq_span(a.seqs, s);
-      const int32_t at = sp.len - sp.n_new + (t - sp.t0);
-      const bool mine = t >= sp.t0 && t < sp.t0 + sp.n_new;
-      int64_t row = -1;
-      if (!sp.ok || !mine) {
-        set_status(a.status, GDN_ERR_BOUNDS);
-      } else if (at >= 0) {
-        const int32_t page = page_of(a.table + (int64_t)s * a.table_stride, at, a.page_size, a.max_pages, a.n_pages);
-        if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
-        else row = (int64_t)page * a.page_stride + (int64_t)(at % a.page_size) * a.slot_stride;
-      }
-      s_row[threadIdx.x] = row;
-      if (!a.positions) p = at;
-    }
-    s_pos[threadIdx.x] = p;
-  }
-  if (APPEND || half > 0) __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int t = i / half, c = i - t * half;
-    const uint64_t turns = (uint64_t)s_pos[t] * a.freqs[c];
-    float sn, cn;
-    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cn);
-    cs[i] = make_float2(cn * a.scale, sn * a.scale * a.sign);
-  }
-  __syncthreads();
-
   const int rot = INTER && VEC > 1 ? a.rd / VEC : half / VEC;  // rotary places of a head
   const int rest = (a.D - a.rd) / VEC;
   const int nq = rot + (a.copy_q ? rest : 0), nk = rot + (a.copy_k ? rest : 0), nv = APPEND ? a.D / VEC : 0;
   const int places = a.Hq * nq + a.Hk * nk + a.Hv * nv;
-  for (int pl = threadIdx.x; pl < places; pl += blockDim.x) {
-    const T *in;
-    T *out;
-    int64_t is, os = 0;
-    int c, h, kind;  // kind 0: q, 1: k, 2: v
+
+  const T *in;
+  T *out;
+  int64_t os;
+  int c, kind;  // kind 0: q, 1: k, 2: v
+  bool turn, two;
+  int apart;  // second vector (half layout, or VEC = 1)
+  Vec<T, VEC> x1[TOK], x2[TOK];
+  auto load = [&](int pl) {
+    int h;
+    int64_t is;
+    os = 0;
     if (pl < a.Hq * nq) {
       h = pl / nq, c = pl - h * nq, kind = 0;
       in = (const T *)a.q + (int64_t)h * a.D, is = a.qs;
@@ -111,57 +103,88 @@ __global__ void __launch_bounds__(kMaxThreads) rope_kernel(const RopeArgs a) {
       in = (const T *)a.v + (int64_t)h * a.D, is = a.vs;
       out = (T *)a.vo + (int64_t)h * a.head_stride;
     }
-    const bool turn = kind != 2 && c < rot;
-    const int e = turn ? (INTER ? (VEC > 1 ? c * VEC : 2 * c) : c * VEC)
-                       : (kind == 2 ? c * VEC : a.rd + (c - rot) * VEC);  // first element
-    const int e2 = INTER ? e + 1 : e + half;  // second vector (half layout, or VEC = 1)
-    const bool two = turn && (!INTER || VEC == 1);
+    turn = kind != 2 && c < rot;
+    two = turn && (!INTER || VEC == 1);
+    const int e = turn ? (INTER && VEC == 1 ? 2 * c : c * VEC) : (kind == 2 ? c * VEC : a.rd + (c - rot) * VEC);
+    apart = INTER ? 1 : half;
     in += (int64_t)t0 * is + e;
     out += e;
-    constexpr int kBatch = TOK < 4 ? TOK : 4;  // tokens whose loads are in flight together
-    for (int tb = 0; tb < nt; tb += kBatch) {
-      Vec<T, VEC> x1[kBatch], x2[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (tb + i < nt) {
-          x1[i] = *reinterpret_cast<const Vec<T, VEC> *>(in + (tb + i) * is);
-          if (two) x2[i] = *reinterpret_cast<const Vec<T, VEC> *>(in + (tb + i) * is + (e2 - e));
+    for (int t = 0; t < TOK; ++t)
+      if (t < nt) {
+        x1[t] = *reinterpret_cast<const Vec<T, VEC> *>(in + t * is);
+        if (two) x2[t] = *reinterpret_cast<const Vec<T, VEC> *>(in + t * is + apart);
+      }
+  };
+  int pl = threadIdx.x;
+  if (pl < places) load(pl);
+
+  if (APPEND) {
+    for (int i = threadIdx.x >> 5; i < nt; i += blockDim.x >> 5) {  // a warp a token
+      const int t = t0 + i, s = a.seqs.cu ? seq_of_token_warp(a.seqs.cu, a.seqs.n_seqs, t) : t;
+      if ((threadIdx.x & 31) == 0) {
+        const SeqSpan sp = seq_span(a.seqs, s);
+        const int32_t at = sp.len - sp.n_new + (t - sp.t0);
+        const bool mine = t >= sp.t0 && t < sp.t0 + sp.n_new;
+        int64_t row = -1;
+        if (!sp.ok || !mine) {
+          set_status(a.status, GDN_ERR_BOUNDS);
+        } else if (at >= 0) {
+          const int32_t page = page_of(a.table + (int64_t)s * a.table_stride, at, a.page_size, a.max_pages, a.n_pages);
+          if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
+          else row = (int64_t)page * a.page_stride + (int64_t)(at % a.page_size) * a.slot_stride;
         }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = tb + i;
-        if (t >= nt) break;
-        int64_t at;
-        if (APPEND && kind != 0) {
-          at = s_row[t];
-          if (at < 0) continue;
-        } else {
-          at = (int64_t)(t0 + t) * os;
-        }
-        if (turn) {
-          const float2 *w = cs + t * half;
-          if (two) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const float2 f = w[c * VEC + j];
-              const float u = to_f32<T>(x1[i].v[j]), z = to_f32<T>(x2[i].v[j]);
-              x1[i].v[j] = from_f32<T>(u * f.x - z * f.y);
-              x2[i].v[j] = from_f32<T>(z * f.x + u * f.y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j + 1 < VEC; j += 2) {
-              const float2 f = w[(c * VEC + j) >> 1];
-              const float u = to_f32<T>(x1[i].v[j]), z = to_f32<T>(x1[i].v[j + 1]);
-              x1[i].v[j] = from_f32<T>(u * f.x - z * f.y);
-              x1[i].v[j + 1] = from_f32<T>(z * f.x + u * f.y);
-            }
-          }
-        }
-        *reinterpret_cast<Vec<T, VEC> *>(out + at) = x1[i];
-        if (two) *reinterpret_cast<Vec<T, VEC> *>(out + at + (e2 - e)) = x2[i];
+        s_row[i] = row;
+        s_pos[i] = a.positions ? a.positions[t] : at;
       }
     }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+    const int t = i / half, f = i - t * half;
+    const uint64_t turns = (uint64_t)(APPEND ? s_pos[t] : a.positions[t0 + t]) * a.freqs[f];
+    float sn, cn;
+    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cn);
+    cs[i] = make_float2(cn * a.scale, sn * a.scale * a.sign);
+  }
+  __syncthreads();
+
+  for (; pl < places;) {
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+      if (t >= nt) break;
+      int64_t at;
+      if (APPEND && kind != 0) {
+        at = s_row[t];
+        if (at < 0) continue;
+      } else {
+        at = (int64_t)(t0 + t) * os;
+      }
+      if (turn) {
+        const float2 *w = cs + t * half;
+        if (two) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const float2 f = w[c * VEC + j];
+            const float u = to_f32<T>(x1[t].v[j]), z = to_f32<T>(x2[t].v[j]);
+            x1[t].v[j] = from_f32<T>(u * f.x - z * f.y);
+            x2[t].v[j] = from_f32<T>(z * f.x + u * f.y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j + 1 < VEC; j += 2) {
+            const float2 f = w[(c * VEC + j) >> 1];
+            const float u = to_f32<T>(x1[t].v[j]), z = to_f32<T>(x1[t].v[j + 1]);
+            x1[t].v[j] = from_f32<T>(u * f.x - z * f.y);
+            x1[t].v[j + 1] = from_f32<T>(z * f.x + u * f.y);
+          }
+        }
+      }
+      *reinterpret_cast<Vec<T, VEC> *>(out + at) = x1[t];
+      if (two) *reinterpret_cast<Vec<T, VEC> *>(out + at + apart) = x2[t];
+    }
+    pl += blockDim.x;
+    if (pl < places) load(pl);
   }
 }
 
@@ -182,12 +205,12 @@ gdn_status launch_vec(const RopeArgs &a, bool inter, cudaStream_t st) {
                          (APPEND ? (int64_t)a.Hv * (a.D / VEC) : 0);
   if (places > (1 << 30)) return GDN_ERR_UNSUPPORTED;
   if (places == 0) return GDN_OK;
-  // eight tokens a block share its set-up; with few tokens one each fills more of the GPU
-  const bool many = a.n_tok >= 8 * 152;
+  // four tokens a block share its set-up; with few tokens one each fills more of the GPU
+  const bool many = a.n_tok >= 4 * 2 * 152;
   if (inter)
-    return many ? launch_tok<T, VEC, APPEND, true, 8>(a, (int)places, st)
+    return many ? launch_tok<T, VEC, APPEND, true, 4>(a, (int)places, st)
                 : launch_tok<T, VEC, APPEND, true, 1>(a, (int)places, st);
-  return many ? launch_tok<T, VEC, APPEND, false, 8>(a, (int)places, st)
+  return many ? launch_tok<T, VEC, APPEND, false, 4>(a, (int)places, st)
               : launch_tok<T, VEC, APPEND, false, 1>(a, (int)places, st);
 }
 

@@ -13,6 +13,13 @@ from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT,
                _dtype_code, _need_cuda, _ptr, _stream, _ws_cache, load)
 
 
+def _handle(t, stream):
+    """The stream of a call on t's device, as an integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(t, stream).value or 0
+
+
 def gdn_rope_inv_freq(rotary_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0, alpha=1.0, beta=32.0):
     """Frequencies of the rotary pairs, fp64 on the CPU [rotary_dim / 2]: base^(-2i / rotary_dim), with
     scaling "linear" (over factor), "base" (a larger base) or "parts" (by parts, over orig_len positions)."""
@@ -65,27 +72,32 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     if positions.dtype != torch.int64 or positions.numel() != n_tok or not positions.is_contiguous():
         raise TypeError("positions must be contiguous int64 [n_tok]")
     rd = _rotary(freqs, D)
-    ptr, heads, ins, outs = [], [], [], []
-    for name, t, out in (("q", q, q_out), ("k", k, k_out)):
+    dtype = x.dtype
+
+    def side(name, t, out):
+        """(input, output, heads, input stride, output stride, output tensor)"""
         if t is None:
-            ptr += [None, None]
-            heads.append(0), ins.append(0), outs.append(0)
-            continue
-        if t.shape[0] != n_tok or t.dtype != x.dtype:
+            return None, None, 0, 0, 0, None
+        if t.shape[0] != n_tok or t.dtype != dtype:
             raise ValueError("q and k must have the same tokens and dtype")
         stride = _heads(name, t, D)
         if out is None:
-            out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        elif out.shape != t.shape or out.dtype != t.dtype:
-            raise ValueError(f"{name}_out must have {name}'s shape and dtype")
-        ptr += [t, out]
-        heads.append(t.shape[1]), ins.append(stride), outs.append(_heads(name + "_out", out, D))
+            out = torch.empty(t.shape, dtype=dtype, device=t.device)
+            out_stride = 0
+        else:
+            if out.shape != t.shape or out.dtype != dtype:
+                raise ValueError(f"{name}_out must have {name}'s shape and dtype")
+            out_stride = _heads(name + "_out", out, D)
+        return t.data_ptr(), out.data_ptr(), t.shape[1], stride, out_stride, out
+
+    qp, qop, hq, qs, qos, q_out = side("q", q, q_out)
+    kp, kop, hk, ks, kos, k_out = side("k", k, k_out)
     flags = (GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0) | (GDN_FLAG_ROPE_BACKWARD if backward else 0)
-    p = [None if t is None else t.data_ptr() for t in ptr]
-    _check(load().gdn_rope(p[0], p[2], positions.data_ptr(), _ptr(freqs), _dtype_code(x.dtype), n_tok, heads[0],
-                           heads[1], D, rd, ins[0], ins[1], outs[0], outs[1], scale, flags, p[1], p[3],
-                           _stream(x, stream)), "gdn_rope")
-    return ptr[1], ptr[3]
+    st = load().gdn_rope(qp, kp, positions.data_ptr(), None if freqs is None else freqs.data_ptr(), _dtype_code(dtype),
+                         n_tok, hq, hk, D, rd, qs, ks, qos, kos, scale, flags, qop, kop, _handle(x, stream))
+    if st:
+        _check(st, "gdn_rope")
+    return q_out, k_out
 
 
 _cache_shapes = {}
@@ -143,8 +155,8 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
 
 def _own_workspace(kind, nbytes, t, stream):
     """A workspace of this kind for calls on this device and stream, which run one after another."""
-    handle = _stream(t, stream)
-    key = (kind, t.device, handle.value)
+    handle = _handle(t, stream)
+    key = (kind, t.get_device(), handle)
     ws = _ws_cache.get(key)
     if ws is None or ws.nbytes < nbytes:
         ws = _ws_cache[key] = Workspace(nbytes, t.device)
@@ -168,7 +180,7 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous with q's shape and dtype")
-    ws, handle = ((workspace, _stream(k, stream)) if workspace is not None
+    ws, handle = ((workspace, _handle(k, stream)) if workspace is not None
                   else _own_workspace("cache", 256, k, stream))
     flags = GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
@@ -210,7 +222,7 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
         nbytes = gdn_paged_attn_workspace_bytes(sh, max_new)
         ws, handle = _own_workspace("attn", nbytes, q, stream)
     else:
-        ws, handle = workspace, _stream(q, stream)
+        ws, handle = workspace, _handle(q, stream)
     flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
     _check(load().gdn_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
                                  seq_lens.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
@@ -267,7 +279,7 @@ def _page_pools(pools, n_pages):
 
 def _pages_workspace(tables, t, workspace, stream):
     if workspace is not None:
-        return workspace, _stream(t, stream)
+        return workspace, _handle(t, stream)
     return _own_workspace("pages", gdn_pages_workspace_bytes(tables.n_pages, tables.n_rows), t, stream)
 
 
@@ -319,7 +331,7 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     _page_list("dst", dst, n)
     n_pages = pools[0].shape[0] if pools else 0
     p = _page_pools(pools, n_pages)
-    ws, handle = ((workspace, _stream(src, stream)) if workspace is not None
+    ws, handle = ((workspace, _handle(src, stream)) if workspace is not None
                   else _own_workspace("pages", 256, src, stream))
     _check(load().gdn_pages_copy(src.data_ptr(), dst.data_ptr(), n, n_pages, ctypes.byref(p), ws.ptr(), ws.nbytes,
                                  handle), "gdn_pages_copy")
