@@ -38,7 +38,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int KT = 128;              // positions a tile
 constexpr int kSms = 152;            // persistent blocks
 constexpr uint32_t kSpin = 1u << 22; // polls of a wait before it gives up
 constexpr int kData = 224 * 1024;    // Q and the ring
@@ -49,12 +48,11 @@ constexpr int kOver = 2;              // units an item costs beyond its tiles
 template <int D, int NQ>
 struct Cfg {
   static constexpr int R = 128 * NQ;                    // rows of TMEM lanes; an item fills tile_rows() of each 128
-  static constexpr int KG = D == 256 ? 2 : 1;           // granules a K (by columns) or V (by positions) tile
-  static constexpr int kGran = KT * D * 2 / KG;         // bytes
+  static constexpr int KT = D == 256 ? 64 : 128;        // positions a tile
+  static constexpr int kGran = KT * D * 2;              // bytes of a granule: a tile of K or V
   static constexpr int kQ = R * D * 2;
   static constexpr int kSlots = (kData - kQ) / kGran;
-  static constexpr int kPanelsK = (D / KG) / 64;        // 64-column panels of a K granule: KT rows each
-  static constexpr int kRowsV = KT / KG, kPanelsV = D / 64;
+  static constexpr int kPanel = KT * 128;               // bytes of 64 columns of it
   // softmax warpgroups, then the TMA and MMA warps; with two tiles a whole warpgroup for those, so that the
   // registers can be split between the warpgroups
   static constexpr int kThreads = NQ == 2 ? 384 : 192;
@@ -127,6 +125,15 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -159,6 +166,7 @@ __device__ __forceinline__ bool walk_cut(Walk &w) {
   w.n = unit_tile(end, kOver) - w.j;
   return w.it.n_tiles > 0 ? w.n > 0 : w.u == 0;
 }
+template <int KT>
 __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int slots) {
   while (w.left > 0) {
     w.u = 0;
@@ -176,12 +184,13 @@ __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int s
   }
   return false;
 }
+template <int KT>
 __device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, int slot, int seq, int h, int u,
                                            int64_t left) {
   w.slot = slot, w.h = h, w.u = u, w.left = left;
   w.it = item_of(a.seqs, seq, slot, a.G, R, KT, a.window);
   w.units = item_units(w.it, kOver);
-  return walk_cut(w) || walk_next(a, w, R, slots);
+  return walk_cut(w) || walk_next<KT>(a, w, R, slots);
 }
 
 template <int N>
@@ -236,13 +245,13 @@ __device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
 }
 
 // Granules of a piece of n tiles in ring order.  NQ = 2: K0 V0 K1 V1 ...; NQ = 1: K0 K1 V0 K2 V1 ... V(n-1).
-template <int NQ, int KG>
+template <int NQ>
 __device__ __forceinline__ uint32_t idx_k(uint32_t base, int j) {
-  return base + KG * (NQ == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1);
+  return base + (NQ == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1);
 }
-template <int NQ, int KG>
+template <int NQ>
 __device__ __forceinline__ uint32_t idx_v(uint32_t base, int j, int n) {
-  return base + KG * (NQ == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1));
+  return base + (NQ == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1));
 }
 
 template <int D, int NQ>
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TcArgs a) {
   using C = Cfg<D, NQ>;
-  constexpr int KG = C::KG, kSlots = C::kSlots;
+  constexpr int KT = C::KT, kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -367,14 +376,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   if (warp == kWarpTma) {
     // ================================================= Q tiles; K and V granules, page by page
     if (NQ == 2) set_regs_down<88>();
-    more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+    more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
-    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, int rows, int panels, uint32_t panel_bytes, int col0,
-                    const int32_t *row) {
+    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, const int32_t *row) {
       const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
-      const int nb = rows / a.box;
+      const int nb = KT / a.box;
       int page = -1, at = 0;
       if (lane < nb) {
         const int pos = pos0 + lane * a.box;
@@ -390,12 +398,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         ok = false;
         return;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes * panels);
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes * (D / 64));
       __syncwarp();
       if (page >= 0)
-        for (int p = 0; p < panels; ++p)
-          tma_load_4d(ring + slot * C::kGran + p * panel_bytes + lane * box_bytes, map, &ctl.full[slot], col0 + 64 * p,
-                      at, w.h, page);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p)
+          tma_load_4d(ring + slot * C::kGran + p * C::kPanel + lane * box_bytes, map, &ctl.full[slot], 64 * p, at, w.h,
+                      page);
       issued = idx + 1;
     };
     if (lane == 0) {
@@ -407,18 +416,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       if (w.it.n_tiles > 0) {
         const int32_t *row = a.table + (int64_t)w.it.s * a.table_stride;
         const int first = (w.it.tile0 + w.j) * KT;
-        auto load_k = [&](int j) {
-#pragma unroll
-          for (int g = 0; g < KG; ++g)
-            if (ok) load(&tm_k, idx_k<NQ, KG>(base, j) + g, first + j * KT, KT, C::kPanelsK, KT * 128, g * (D / KG), row);
-        };
-        auto load_v = [&](int j) {
-#pragma unroll
-          for (int g = 0; g < KG; ++g)
-            if (ok)
-              load(&tm_v, idx_v<NQ, KG>(base, j, w.n) + g, first + j * KT + g * C::kRowsV, C::kRowsV, C::kPanelsV,
-                   C::kRowsV * 128, 0, row);
-        };
+        auto load_k = [&](int j) { load(&tm_k, idx_k<NQ>(base, j), first + j * KT, row); };
+        auto load_v = [&](int j) { load(&tm_v, idx_v<NQ>(base, j, w.n), first + j * KT, row); };
         // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
         // sequences that come along are never used
         const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
@@ -442,21 +441,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (ok) load_v(j);
           if (NQ == 2 && j + 1 < w.n && ok) load_k(j + 1);
         }
-        base += 2 * KG * w.n;
+        base += 2 * w.n;
       }
-      more = walk_next(a, w, R, slots);
+      more = walk_next<KT>(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
   } else if (warp == kWarpMma) {
     // ================================================= MMAs
     if (NQ == 2) set_regs_down<88>();
     if (lane == 0) {
-      more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+      more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
       const uint32_t id_s = idesc_bf16(128, KT, false, false);
       const uint32_t id_o = idesc_bf16(128, D, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint64_t d_k = smem_desc(smem_u32(ring), 16, 1024, 2);
-      const uint64_t d_v = smem_desc(smem_u32(ring), C::kRowsV * 128, 1024, 2);
+      const uint64_t d_v = smem_desc(smem_u32(ring), C::kPanel, 1024, 2);
       uint32_t base = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // steps: P tiles consumed, per TMEM slot
       uint32_t total_steps = 0;                                  // NQ = 1: the S slots alternate across pieces
       bool ok = !a.no_wait;
@@ -465,43 +464,38 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       };
       // S[slot] = Q[t] K(j)^T
       auto issue_s = [&](int t, int slot, int j) {
+        const uint32_t idx = idx_k<NQ>(base, j);
+        wait_full(idx);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dk = d_k + (((idx % kSlots) * C::kGran) >> 4);
+        const uint64_t dq = d_q + ((t * 128 * D * 2) >> 4);
 #pragma unroll
-        for (int g = 0; g < KG; ++g) {
-          const uint32_t idx = idx_k<NQ, KG>(base, j) + g;
-          wait_full(idx);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t dk = d_k + (((idx % kSlots) * C::kGran) >> 4);
-          const uint64_t dq = d_q + ((t * 128 * D * 2 + g * C::kPanelsK * 16384) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / KG / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-            umma_bf16(tm + slot * 128, dq + off, dk + off, id_s, g > 0 || ks > 0);
-          }
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_bf16(tm + slot * KT, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                    dk + (((ks >> 2) * C::kPanel + (ks & 3) * 32) >> 4), id_s, ks > 0);
         umma_commit(&ctl.sfull[slot]);
+        if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
       };
       // O[t] (+)= P[slot] V(j), the first half of the positions as soon as their P is there
       auto issue_o = [&](int t, int slot, int j) {
+        const uint32_t idx = idx_v<NQ>(base, j, w.n);
+        const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait_spin(&ctl.pready[slot][half], steps[slot] & 1, kSpin, abort_flag)) {
             ok = false;
             return;
           }
-          const int g = KG == 2 ? half : 0;
-          const uint32_t idx = idx_v<NQ, KG>(base, j, w.n) + g;
-          if (KG == 2 || half == 0) wait_full(idx);
+          if (half == 0) wait_full(idx);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ts(tm + C::kO + t * D, tm + slot * 128 + (half * 4 + ks) * 8,
-                    dv + (((KG == 2 ? ks : half * 4 + ks) * 2048) >> 4), id_o, j > 0 || half > 0 || ks > 0);
-          if (NQ == 1 && (KG == 2 || half == 1)) umma_commit(&ctl.empty[idx % kSlots]);
+          for (int ks = half * (KT / 32); ks < (half + 1) * (KT / 32); ++ks)
+            umma_ts(tm + C::kO + t * D, tm + slot * KT + ks * 8, dv + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
         }
         ++steps[slot];
+        if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
       };
       while (more && ok) {
         const int n = w.it.n_tiles > 0 ? w.n : 0;
@@ -526,9 +520,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               if (ok) issue_o(0, total_steps & 1, j);
             }
           }
-          base += 2 * KG * n;
+          base += 2 * n;
         }
-        more = walk_next(a, w, R, slots);
+        more = walk_next<KT>(a, w, R, slots);
       }
       if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
         if (!ok) fail();
@@ -541,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else {
     // ================================================= softmax: a thread owns a query row
     if (NQ == 2) set_regs_up<208>();
-    more = walk_begin(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+    more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lq = (uint32_t)(quarter * 32) << 16;
     const float lag = kLag / a.c;
@@ -560,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.o + out * D + d) = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[out] = -INFINITY;
         }
-        more = walk_next(a, w, R, slots);
+        more = walk_next<KT>(a, w, R, slots);
         continue;
       }
       const int n = w.n, nt = NQ == 2 && it.rows > a.RT ? 2 : 1;
@@ -571,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const int p = it.first + i;
         const int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
-        const bool releases = NQ == 1 || t == nt - 1;  // this warpgroup gives ring slots back
+        const bool releases = t == nt - 1;  // this warpgroup gives ring slots back
         for (int j = 0; j < n; ++j, ++steps) {
           const int slot = NQ == 2 ? t : steps & 1;
           if (!warp_wait(&ctl.sfull[slot], sphase[slot] & 1, abort_flag)) {
@@ -580,11 +574,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           ++sphase[slot];
           tc_fence_after();
-          // S is there: K(j) has been read, and (NQ = 2) V(j - 1), whose product came before it
+          // S is there: K(j) has been read, and V(j - 1), whose product came before it (NQ = 1: the MMAs' own commits
+          // give the slots back, K(j) well before this warpgroup comes to S)
           if (tid == t * 128) {
-            if (releases) {
-              for (int g2 = 0; g2 < KG; ++g2) mbar_arrive(&ctl.empty[(idx_k<NQ, KG>(base, j) + g2) % kSlots]);
-              if (NQ == 2 && j > 0) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, j - 1, n) % kSlots]);
+            if (NQ == 2 && releases) {
+              mbar_arrive(&ctl.empty[idx_k<NQ>(base, j) % kSlots]);
+              if (j > 0) mbar_arrive(&ctl.empty[idx_v<NQ>(base, j - 1, n) % kSlots]);
             }
             if (j == n - 1) mbar_arrive(&ctl.qfree[t]);
           }
@@ -592,22 +587,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (t == 0 && (pos < it.lo || pos + KT > it.hi)) {
             // positions that no row sees: their V rows become zeros (P is 0 there, and 0 * NaN is not)
             const int x = pos + r;
-            const uint32_t idx = idx_v<NQ, KG>(base, j, n) + r / C::kRowsV;
+            const uint32_t idx = idx_v<NQ>(base, j, n);
             if (!warp_wait(&ctl.full[idx % kSlots], (idx / kSlots) & 1, abort_flag)) {
               ok = false;
               break;
             }
-            if (x < it.lo || x >= it.hi) {
-              uint8_t *vr = ring + (idx % kSlots) * C::kGran + (r % C::kRowsV) * 128;
-              for (int pn = 0; pn < C::kPanelsV; ++pn)
+            if (r < KT && (x < it.lo || x >= it.hi)) {
+              uint8_t *vr = ring + (idx % kSlots) * C::kGran + r * 128;
+              for (int pn = 0; pn < D / 64; ++pn)
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
-                  *reinterpret_cast<uint4 *>(vr + pn * C::kRowsV * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4 *>(vr + pn * C::kPanel + ch * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
           if (live) {
-            const uint32_t ts = tm + lq + slot * 128;
+            const uint32_t ts = tm + lq + slot * KT;
             float s[KT];
 #pragma unroll
             for (int x = 0; x < KT; x += 32) tmem_ld32u(ts + x, reinterpret_cast<uint32_t *>(s) + x);
@@ -623,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             } else if (__any_sync(0xffffffffu, valid && mx > m + lag)) {
               // the products so far end before O is scaled
               if (NQ == 1) {
-                const uint32_t idx = idx_v<NQ, KG>(base, j - 1, n) + KG - 1;
+                const uint32_t idx = idx_v<NQ>(base, j - 1, n);
                 ok = ok && warp_wait(&ctl.empty[idx % kSlots], (idx / kSlots) & 1, abort_flag);
                 tc_fence_after();
               }
@@ -649,19 +644,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t pk[32];
+              uint32_t pk[KT / 4];
 #pragma unroll
-              for (int y = 0; y < 64; y += 4) {
+              for (int y = 0; y < KT / 2; y += 4) {
+                const float *v = s + half * (KT / 2) + y;
                 float p0, p1, p2, p3;
-                f2_unpack(f2_fma(f2_pack(s[half * 64 + y], s[half * 64 + y + 1]), c2, mc2), p0, p1);
-                f2_unpack(f2_fma(f2_pack(s[half * 64 + y + 2], s[half * 64 + y + 3]), c2, mc2), p2, p3);
+                f2_unpack(f2_fma(f2_pack(v[0], v[1]), c2, mc2), p0, p1);
+                f2_unpack(f2_fma(f2_pack(v[2], v[3]), c2, mc2), p2, p3);
                 p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
                 sum0 = f2_add(sum0, f2_pack(p0, p1));
                 sum1 = f2_add(sum1, f2_pack(p2, p3));
                 pk[y >> 1] = bf16x2(p0, p1);
                 pk[(y >> 1) + 1] = bf16x2(p2, p3);
               }
-              tmem_st32u(ts + half * 32, pk);
+              if constexpr (KT == 128) tmem_st32u(ts + half * 32, pk);
+              else tmem_st16u(ts + half * 16, pk);
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
@@ -684,9 +681,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         if (ok) {
           if (NQ == 2) {
             ok = warp_wait(&ctl.odone[t], pieces & 1, abort_flag);
-            if (releases && tid == t * 128) mbar_arrive(&ctl.empty[idx_v<NQ, KG>(base, n - 1, n) % kSlots]);
+            if (releases && tid == t * 128) mbar_arrive(&ctl.empty[idx_v<NQ>(base, n - 1, n) % kSlots]);
           } else {
-            const uint32_t idx = idx_v<NQ, KG>(base, n - 1, n) + KG - 1;
+            const uint32_t idx = idx_v<NQ>(base, n - 1, n);
             ok = warp_wait(&ctl.empty[idx % kSlots], (idx / kSlots) & 1, abort_flag);
           }
           tc_fence_after();
@@ -743,10 +740,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         tc_fence_before();
         ++pieces;
       }
-      base += 2 * KG * n;
+      base += 2 * n;
       if (!begins) cont = ends ? 2 : 1;
       else if (!ends) head = 1, head_slot = w.slot, head_h = w.h;
-      more = walk_next(a, w, R, slots);
+      more = walk_next<KT>(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
     if (tid == 0) a.meta[blockIdx.x] = make_int4(cont, head, head_slot, head_h);
@@ -772,7 +769,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 // columns over the pieces, and the rows go out through shared memory, whole rows at a time.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
-  constexpr int R = Cfg<D, NQ>::R, kV = D / 32;  // fours of columns a warp
+  constexpr int R = Cfg<D, NQ>::R, KT = Cfg<D, NQ>::KT, kV = D / 32;  // fours of columns a warp
   __shared__ uint2 rows[32][D / 4 + 1];
   __shared__ float weight[kSms][32], part[2][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -898,7 +895,7 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int box_rows(const gdn_cache_shape &s) { return std::gcd(s.page_size, s.D == 256 ? 64 : KT); }
+int box_rows(const gdn_cache_shape &s) { return std::gcd(s.page_size, s.D == 256 ? 64 : 128); }
 
 template <int D, int NQ>
 gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {

@@ -6,23 +6,27 @@
 // the gradient is the transposed rotation, the same with sin a negated.
 //
 // The angle is kept in turns as a 64-bit fraction: p * freq mod 2^64, one integer multiply,
-// exact for every 64-bit position; its top 32 bits (signed, so [-1/2, 1/2) turns) go to
-// sincospif.  A product in fp32 would be off by p * 2^-25 rad.
+// exact for every 64-bit position, of which the top 32 bits are used.  A product in fp32 would be
+// off by p * 2^-25 rad.
 //
-// Bound by HBM: every element is read and written once.  A block takes up to four tokens; its
-// threads put the tokens' cos and sin into shared memory (one sincospif a pair and token, shared
-// by all heads), and each thread keeps one place of a token's row (a 16-byte vector of pair halves,
-// or of elements that pass through).
+// Bound by HBM: every element is read and written once.  A warp takes a token: it works out
+// the token's cos and sin once for all heads (through its own piece of shared memory, no block
+// barrier), then walks the heads.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
+#include "conv_tap.cuh"
 #include "paged.cuh"
 
 using namespace gdn;
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+// Two heads a lane in flight and three blocks an SM (80 registers): 31 us over the rows of 8192 tokens x 40 heads x
+// 128 bf16 (168 MB); four heads spill (37 us), four blocks 32 us, one head and five blocks 32 us.
+constexpr int kThreads = 256, kHeads = 2;
 
 struct RopeArgs {
   const void *q, *k, *v;  // v: gdn_kv_append only
@@ -51,8 +55,8 @@ __device__ __forceinline__ int seq_of_token_warp(const int32_t *cu, int n_seqs, 
   const int lane = threadIdx.x & 31;
   int lo = 0, n = n_seqs;  // the answer lies in [lo, lo + n)
   while (n > 1) {
-    const int step = (n + 31) / 32, s = lo + lane * step;
-    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && cu[s] <= t);
+    const int step = (n + 31) / 32;
+    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && cu[lo + lane * step] <= t);
     const int k = below ? 31 - __clz(below) : 0;
     lo += k * step;
     n = min(step, n - k * step);
@@ -60,158 +64,185 @@ __device__ __forceinline__ int seq_of_token_warp(const int32_t *cu, int n_seqs, 
   return lo;
 }
 
-// One place of a token's row: element offset of the vector in its head and what happens there.
-// VEC elements a vector; half layout: a rotary place holds VEC pairs (two vectors), interleaved:
-// VEC / 2 pairs (one vector; VEC = 1 then holds one pair as two vectors of one element).
-// A thread loads its place of all the block's tokens before the angles are worked out, so that
-// those (and the look-up of the slots) run under the loads.
-template <typename T, int VEC, bool APPEND, bool INTER, int TOK>
-__global__ void __launch_bounds__(kMaxThreads) rope_kernel(const RopeArgs a) {
-  extern __shared__ float2 cs[];  // [TOK][rd / 2]
-  __shared__ int64_t s_row[TOK];  // gdn_kv_append: offset of the token's slot in the caches, -1: none
-  __shared__ int64_t s_pos[TOK];
-  const int t0 = blockIdx.x * TOK, nt = min(TOK, a.n_tok - t0);
-  const int half = a.rd >> 1;
-  const int rot = INTER && VEC > 1 ? a.rd / VEC : half / VEC;  // rotary places of a head
-  const int rest = (a.D - a.rd) / VEC;
-  const int nq = rot + (a.copy_q ? rest : 0), nk = rot + (a.copy_k ? rest : 0), nv = APPEND ? a.D / VEC : 0;
-  const int places = a.Hq * nq + a.Hk * nk + a.Hv * nv;
-
-  const T *in;
-  T *out;
-  int64_t os;
-  int c, kind;  // kind 0: q, 1: k, 2: v
-  bool turn, two;
-  int apart;  // second vector (half layout, or VEC = 1)
-  Vec<T, VEC> x1[TOK], x2[TOK];
-  auto load = [&](int pl) {
-    int h;
-    int64_t is;
-    os = 0;
-    if (pl < a.Hq * nq) {
-      h = pl / nq, c = pl - h * nq, kind = 0;
-      in = (const T *)a.q + (int64_t)h * a.D, is = a.qs;
-      out = (T *)a.qo + (int64_t)h * a.D, os = a.qos;
-    } else if (pl < a.Hq * nq + a.Hk * nk) {
-      const int r = pl - a.Hq * nq;
-      h = r / nk, c = r - h * nk, kind = 1;
-      in = (const T *)a.k + (int64_t)h * a.D, is = a.ks;
-      out = (T *)a.ko + (APPEND ? (int64_t)h * a.head_stride : (int64_t)h * a.D), os = a.kos;
-    } else {
-      const int r = pl - a.Hq * nq - a.Hk * nk;
-      h = APPEND ? r / max(nv, 1) : 0, c = r - h * nv, kind = 2;
-      in = (const T *)a.v + (int64_t)h * a.D, is = a.vs;
-      out = (T *)a.vo + (int64_t)h * a.head_stride;
-    }
-    turn = kind != 2 && c < rot;
-    two = turn && (!INTER || VEC == 1);
-    const int e = turn ? (INTER && VEC == 1 ? 2 * c : c * VEC) : (kind == 2 ? c * VEC : a.rd + (c - rot) * VEC);
-    apart = INTER ? 1 : half;
-    in += (int64_t)t0 * is + e;
-    out += e;
-#pragma unroll
-    for (int t = 0; t < TOK; ++t)
-      if (t < nt) {
-        x1[t] = *reinterpret_cast<const Vec<T, VEC> *>(in + t * is);
-        if (two) x2[t] = *reinterpret_cast<const Vec<T, VEC> *>(in + t * is + apart);
-      }
-  };
-  int pl = threadIdx.x;
-  if (pl < places) load(pl);
-
-  if (APPEND) {
-    for (int i = threadIdx.x >> 5; i < nt; i += blockDim.x >> 5) {  // a warp a token
-      const int t = t0 + i, s = a.seqs.cu ? seq_of_token_warp(a.seqs.cu, a.seqs.n_seqs, t) : t;
-      if ((threadIdx.x & 31) == 0) {
-        const SeqSpan sp = seq_span(a.seqs, s);
-        const int32_t at = sp.len - sp.n_new + (t - sp.t0);
-        const bool mine = t >= sp.t0 && t < sp.t0 + sp.n_new;
-        int64_t row = -1;
-        if (!sp.ok || !mine) {
-          set_status(a.status, GDN_ERR_BOUNDS);
-        } else if (at >= 0) {
-          const int32_t page = page_of(a.table + (int64_t)s * a.table_stride, at, a.page_size, a.max_pages, a.n_pages);
-          if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
-          else row = (int64_t)page * a.page_stride + (int64_t)(at % a.page_size) * a.slot_stride;
-        }
-        s_row[i] = row;
-        s_pos[i] = a.positions ? a.positions[t] : at;
-      }
-    }
-    __syncthreads();
+// Where a new token goes: its position (where the call gives none) and the offset of its slot in
+// the caches, -1 for none.  A whole warp asks for the same token.
+__device__ __forceinline__ int64_t append_slot(const RopeArgs &a, int t, int64_t &pos) {
+  const int s = a.seqs.cu ? seq_of_token_warp(a.seqs.cu, a.seqs.n_seqs, t) : t;
+  const SeqSpan sp = seq_span(a.seqs, s);
+  const int32_t at = sp.len - sp.n_new + (t - sp.t0);
+  pos = at;
+  if (!sp.ok || t < sp.t0 || t >= sp.t0 + sp.n_new) {
+    set_status(a.status, GDN_ERR_BOUNDS);
+    return -1;
   }
-  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int t = i / half, f = i - t * half;
-    const uint64_t turns = (uint64_t)(APPEND ? s_pos[t] : a.positions[t0 + t]) * a.freqs[f];
-    float sn, cn;
-    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn, &cn);
-    cs[i] = make_float2(cn * a.scale, sn * a.scale * a.sign);
+  if (at < 0) return -1;
+  const int32_t page = page_of(a.table + (int64_t)s * a.table_stride, at, a.page_size, a.max_pages, a.n_pages);
+  if (page < 0) {
+    set_status(a.status, GDN_ERR_BOUNDS);
+    return -1;
   }
-  __syncthreads();
+  return (int64_t)page * a.page_stride + (int64_t)(at % a.page_size) * a.slot_stride;
+}
 
-  for (; pl < places;) {
+// cos and sin of a fraction of a turn, as a signed 32-bit fraction: the eighths of the circle by
+// its top bits, then the Taylor series on [-pi/4, pi/4] (the first term left out is below 2^-25).
+__device__ __forceinline__ float2 cos_sin(uint32_t turn) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;  // nearest quarter of the circle
+  const float y = (float)(int32_t)(turn - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), z = y * y;
+  float s = fmaf(z, 1.f / 362880, -1.f / 5040), c = fmaf(z, 1.f / 40320, -1.f / 720);
+  s = fmaf(z, s, 1.f / 120), c = fmaf(z, c, 1.f / 24);
+  s = fmaf(z, s, -1.f / 6), c = fmaf(z, c, -0.5f);
+  s = fmaf(y * z, s, y), c = fmaf(z, c, 1.f);
+  const float co = (quarter & 1) ? s : c, si = (quarter & 1) ? c : s;
+  return make_float2((quarter + 1) & 2 ? -co : co, quarter & 2 ? -si : si);
+}
+
+// Turns a place: pairs (x1[j], x2[j]) of two vectors.  bf16 vectors of eight go as fp32 pairs.
+template <typename T, int VEC, int P>
+__device__ __forceinline__ void turn_halves(Vec<T, VEC> &x1, Vec<T, VEC> &x2, const float (&cn)[P], const float (&sn)[P]) {
+  if constexpr (sizeof(T) == 2 && VEC == 8) {
+    uint32_t *a = reinterpret_cast<uint32_t *>(&x1), *b = reinterpret_cast<uint32_t *>(&x2);
 #pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      if (t >= nt) break;
-      int64_t at;
-      if (APPEND && kind != 0) {
-        at = s_row[t];
-        if (at < 0) continue;
-      } else {
-        at = (int64_t)(t0 + t) * os;
-      }
-      if (turn) {
-        const float2 *w = cs + t * half;
-        if (two) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float2 f = w[c * VEC + j];
-            const float u = to_f32<T>(x1[t].v[j]), z = to_f32<T>(x2[t].v[j]);
-            x1[t].v[j] = from_f32<T>(u * f.x - z * f.y);
-            x2[t].v[j] = from_f32<T>(z * f.x + u * f.y);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j + 1 < VEC; j += 2) {
-            const float2 f = w[(c * VEC + j) >> 1];
-            const float u = to_f32<T>(x1[t].v[j]), z = to_f32<T>(x1[t].v[j + 1]);
-            x1[t].v[j] = from_f32<T>(u * f.x - z * f.y);
-            x1[t].v[j + 1] = from_f32<T>(z * f.x + u * f.y);
-          }
-        }
-      }
-      *reinterpret_cast<Vec<T, VEC> *>(out + at) = x1[t];
-      if (two) *reinterpret_cast<Vec<T, VEC> *>(out + at + apart) = x2[t];
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t u = f2_from_bf16x2(a[j]), z = f2_from_bf16x2(b[j]);
+      const uint64_t c = f2_pack(cn[2 * j], cn[2 * j + 1]), s = f2_pack(sn[2 * j], sn[2 * j + 1]);
+      const uint64_t ns = f2_pack(-sn[2 * j], -sn[2 * j + 1]);
+      a[j] = bf16x2_from_f2(f2_fma(u, c, f2_mul(z, ns)));
+      b[j] = bf16x2_from_f2(f2_fma(z, c, f2_mul(u, s)));
     }
-    pl += blockDim.x;
-    if (pl < places) load(pl);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float u = to_f32<T>(x1.v[j]), z = to_f32<T>(x2.v[j]);
+      x1.v[j] = from_f32<T>(u * cn[j % P] - z * sn[j % P]);
+      x2.v[j] = from_f32<T>(z * cn[j % P] + u * sn[j % P]);
+    }
+  }
+}
+// The same for neighbours (x[2j], x[2j + 1]) in one vector.
+template <typename T, int VEC, int P>
+__device__ __forceinline__ void turn_neighbours(Vec<T, VEC> &x, const float (&cn)[P], const float (&sn)[P]) {
+  if constexpr (sizeof(T) == 2 && VEC == 8) {
+    uint32_t *a = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float u, z;
+      f2_unpack(f2_from_bf16x2(a[j]), u, z);
+      a[j] = bf16x2_from_f2(f2_pack(u * cn[j] - z * sn[j], z * cn[j] + u * sn[j]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j + 1 < VEC; j += 2) {
+      const float u = to_f32<T>(x.v[j]), z = to_f32<T>(x.v[j + 1]);
+      x.v[j] = from_f32<T>(u * cn[j / 2] - z * sn[j / 2]);
+      x.v[j + 1] = from_f32<T>(z * cn[j / 2] + u * sn[j / 2]);
+    }
   }
 }
 
-template <typename T, int VEC, bool APPEND, bool INTER, int TOK>
-gdn_status launch_tok(const RopeArgs &a, int places, cudaStream_t st) {
-  // threads: one round over the places where they fit, else even rounds
-  const int rounds = (places + kMaxThreads - 1) / kMaxThreads;
-  const int threads = max(64, ((places + rounds - 1) / rounds + 31) / 32 * 32);
-  rope_kernel<T, VEC, APPEND, INTER, TOK>
-      <<<(a.n_tok + TOK - 1) / TOK, threads, sizeof(float2) * TOK * (a.rd / 2), st>>>(a);
-  return launch_status();
+// A warp takes a token, or one of `parts` parts of its heads.  In a rotary column place a lane holds VEC
+// pairs of a head in the half layout (two vectors), VEC / 2 pairs interleaved (one vector; VEC = 1:
+// one pair as two vectors of one element); 32 / rot heads go side by side over the lanes.
+template <typename T, int VEC, bool APPEND, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int parts) {
+  constexpr int kPairs = INTER ? (VEC + 1) / 2 : VEC;  // of a place
+  __shared__ float2 s_cs[kThreads / 32][128];
+  const int lane = threadIdx.x & 31, half = a.rd >> 1;
+  const int64_t job = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int t = (int)(job / parts), part = (int)(job - (int64_t)t * parts);
+  if (t >= a.n_tok) return;
+  float2 *cs = s_cs[threadIdx.x >> 5];
+  const T *q = (const T *)a.q + t * a.qs, *k = (const T *)a.k + t * a.ks;
+  T *qo = (T *)a.qo + t * a.qos, *ko = (T *)a.ko + (APPEND ? 0 : t * a.kos);
+  const int64_t k_head = APPEND ? a.head_stride : a.D;
+  int64_t pos = 0, slot = 0;
+  if (APPEND) {
+    slot = append_slot(a, t, pos);
+    ko += slot;
+  }
+  if (half && a.positions) pos = a.positions[t];
+  for (int i = lane; i < half; i += 32) {
+    const float2 f = cos_sin((uint32_t)(((uint64_t)pos * a.freqs[i]) >> 32));
+    cs[i] = make_float2(f.x * a.scale, f.y * a.scale * a.sign);
+  }
+  __syncwarp();
+
+  // ---- what turns: columns [0, rd) of the heads of q, then of k
+  const int heads = a.Hq + (APPEND && slot < 0 ? 0 : a.Hk);
+  const int rot = half / kPairs;
+  for (int c0 = 0; c0 < rot; c0 += 32) {
+    const int cols = min(32, rot - c0), side = 32 / cols, c = c0 + lane % cols, hl = lane / cols;
+    const int e = INTER ? 2 * kPairs * c : VEC * c, apart = INTER ? 1 : half;
+    constexpr bool two = !INTER || VEC == 1;
+    float cn[kPairs], sn[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const float2 f = cs[c * kPairs + j];
+      cn[j] = f.x, sn[j] = f.y;
+    }
+    for (int h0 = part * side * kHeads; h0 < heads; h0 += parts * side * kHeads) {
+      Vec<T, VEC> x1[kHeads], x2[kHeads];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = h0 + i * side + hl;
+        const T *x = (h < a.Hq ? q : k - a.Hq * a.D) + h * a.D + e;
+        if (h < heads && hl < side) {
+          x1[i] = *reinterpret_cast<const Vec<T, VEC> *>(x);
+          if (two) x2[i] = *reinterpret_cast<const Vec<T, VEC> *>(x + apart);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = h0 + i * side + hl;
+        T *y = h < a.Hq ? qo + h * a.D + e : ko + (h - a.Hq) * k_head + e;
+        if constexpr (two) turn_halves(x1[i], x2[i], cn, sn);
+        else turn_neighbours(x1[i], cn, sn);
+        if (h < heads && hl < side) {
+          *reinterpret_cast<Vec<T, VEC> *>(y) = x1[i];
+          if (two) *reinterpret_cast<Vec<T, VEC> *>(y + apart) = x2[i];
+        }
+      }
+    }
+  }
+
+  // ---- what passes through: columns [rd, D) of q and k where they are not in place, all of v
+  auto copy = [&](const T *x, T *y, int64_t y_head, int n_heads, int from) {
+    const int cols = (a.D - from) / VEC, all = n_heads * cols;
+    constexpr int kAhead = 8;
+    // place i of a lane is (head h, column c); 32 places on, without a division
+    const int dh = 32 / cols, dc = 32 - dh * cols;
+    for (int i0 = part * 32 * kAhead + lane; i0 < all; i0 += parts * 32 * kAhead) {
+      Vec<T, VEC> v[kAhead];
+      int h = i0 / cols, c = i0 - h * cols;
+      const int h_first = h, c_first = c;
+      auto next = [&]() {
+        h += dh, c += dc;
+        if (c >= cols) c -= cols, ++h;
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i, next())
+        if (h < n_heads) v[i] = *reinterpret_cast<const Vec<T, VEC> *>(x + h * a.D + from + c * VEC);
+      h = h_first, c = c_first;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i, next())
+        if (h < n_heads) *reinterpret_cast<Vec<T, VEC> *>(y + h * y_head + from + c * VEC) = v[i];
+    }
+  };
+  if (a.rd < a.D) {
+    if (a.copy_q) copy(q, qo, a.D, a.Hq, a.rd);
+    if (a.copy_k && !(APPEND && slot < 0)) copy(k, ko, k_head, a.Hk, a.rd);
+  }
+  if (APPEND && slot >= 0) copy((const T *)a.v + t * a.vs, (T *)a.vo + slot, a.head_stride, a.Hv, 0);
 }
 
 template <typename T, int VEC, bool APPEND>
 gdn_status launch_vec(const RopeArgs &a, bool inter, cudaStream_t st) {
-  const int rot = inter && VEC > 1 ? a.rd / VEC : a.rd / 2 / VEC, rest = (a.D - a.rd) / VEC;
-  const int64_t places = (int64_t)a.Hq * (rot + (a.copy_q ? rest : 0)) + (int64_t)a.Hk * (rot + (a.copy_k ? rest : 0)) +
-                         (APPEND ? (int64_t)a.Hv * (a.D / VEC) : 0);
-  if (places > (1 << 30)) return GDN_ERR_UNSUPPORTED;
-  if (places == 0) return GDN_OK;
-  // four tokens a block share its set-up; with few tokens one each fills more of the GPU
-  const bool many = a.n_tok >= 4 * 2 * 152;
-  if (inter)
-    return many ? launch_tok<T, VEC, APPEND, true, 4>(a, (int)places, st)
-                : launch_tok<T, VEC, APPEND, true, 1>(a, (int)places, st);
-  return many ? launch_tok<T, VEC, APPEND, false, 4>(a, (int)places, st)
-              : launch_tok<T, VEC, APPEND, false, 1>(a, (int)places, st);
+  // a token's heads over several warps where the tokens alone would not fill the GPU
+  const int parts = std::max(1, std::min((a.Hq + a.Hk + a.Hv + 7) / 8, 152 * 16 / a.n_tok));
+  const int64_t blocks = ((int64_t)a.n_tok * parts * 32 + kThreads - 1) / kThreads;
+  if (inter) rope_kernel<T, VEC, APPEND, true><<<(unsigned)blocks, kThreads, 0, st>>>(a, parts);
+  else rope_kernel<T, VEC, APPEND, false><<<(unsigned)blocks, kThreads, 0, st>>>(a, parts);
+  return launch_status();
 }
 
 // 16-byte vectors where every row start, stride and part of a head is a multiple of them
