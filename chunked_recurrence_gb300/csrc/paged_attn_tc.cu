@@ -10,7 +10,7 @@
 // Query rows of a kv head (row = token * group + head in the group) are cut into items of R = 128 NQ
 // rows, keys into tiles of 128 positions.  NQ = 2 (D <= 128): two 128-row tiles share each K and V
 // tile and take turns, one's softmax under the other's MMAs.  NQ = 1: one row tile; S alternates between two TMEM
-// slots, so the next tile's S runs under this one's softmax.  TMEM: two S slots of 128 columns
+// slots, so the next tile's S runs under this one's softmax.  TMEM: two S slots of a tile's columns
 // (P, as bf16 pairs, lies over its S), then O.
 //
 // Work: (item, kv head, tile) in one line, cut into equal shares, one persistent block each, so ragged lengths
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const TcArgs a) {
   using C = Cfg<D, NQ>;
   constexpr int KT = C::KT, kSlots = C::kSlots;
+  static_assert(KT / 8 * (D / 64) <= 32, "a granule has at most one box a lane");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -380,31 +381,44 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
-    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, const int32_t *row) {
-      const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
-      const int nb = KT / a.box;
-      int page = -1, at = 0;
-      if (lane < nb) {
-        const int pos = pos0 + lane * a.box;
-        // boxes past the last position that a row sees, or before the first, are not read
-        if (pos < w.it.hi && pos + a.box > w.it.lo) {
-          page = page_of(row, pos, a.page_size, a.max_pages, a.n_pages);
-          at = pos % a.page_size;
-          if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
-        }
+    // Pages ahead of their use: lane l holds the page and slot of box 32 win + l, and of box 32 (win + 1) + l, or -1
+    // where the box holds no position that a row sees.  V comes last, K at most a tile before it, so two windows do;
+    // the next one's entries are asked for when V enters this one.  (An entry asked for when it is needed costs
+    // its L2 latency, 570 cycles a granule.)
+    int win = 0, page[2], at[2];
+    auto look_up = [&](int window, int i, const int32_t *row) {
+      const int64_t pos = (int64_t)(32 * window + lane) * a.box;
+      page[i] = -1, at[i] = 0;
+      if (pos < w.it.hi && pos + a.box > w.it.lo) {
+        page[i] = page_of(row, (int)pos, a.page_size, a.max_pages, a.n_pages);
+        at[i] = (int)pos % a.page_size;
+        if (page[i] < 0) set_status(a.status, GDN_ERR_BOUNDS);
       }
-      const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+    };
+    // a granule of K or V: its boxes (rows x 64-column panels) over the lanes, all in one instruction
+    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, const int32_t *row, bool last) {
+      const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
+      constexpr int kPanels = D / 64;
+      const int nb = KT / a.box, b0 = pos0 / a.box;  // nb divides 32: a granule lies in one window
+      if (last && b0 / 32 > win) {
+        ++win;
+        page[0] = page[1], at[0] = at[1];
+        look_up(win + 1, 1, row);
+      }
+      const int i = lane / kPanels, p = lane % kPanels, from = (b0 + i) & 31;
+      const int pg0 = __shfl_sync(0xffffffffu, page[0], from), pg1 = __shfl_sync(0xffffffffu, page[1], from);
+      const int at0 = __shfl_sync(0xffffffffu, at[0], from), at1 = __shfl_sync(0xffffffffu, at[1], from);
+      const bool ahead = b0 / 32 > win;
+      const int pg = i >= nb ? -1 : ahead ? pg1 : pg0, sl = ahead ? at1 : at0;
+      const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
       if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
         ok = false;
         return;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes * (D / 64));
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes);
       __syncwarp();
-      if (page >= 0)
-#pragma unroll
-        for (int p = 0; p < D / 64; ++p)
-          tma_load_4d(ring + slot * C::kGran + p * C::kPanel + lane * box_bytes, map, &ctl.full[slot], 64 * p, at, w.h,
-                      page);
+      if (pg >= 0)
+        tma_load_4d(ring + slot * C::kGran + p * C::kPanel + i * box_bytes, map, &ctl.full[slot], 64 * p, sl, w.h, pg);
       issued = idx + 1;
     };
     if (lane == 0) {
@@ -416,8 +430,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       if (w.it.n_tiles > 0) {
         const int32_t *row = a.table + (int64_t)w.it.s * a.table_stride;
         const int first = (w.it.tile0 + w.j) * KT;
-        auto load_k = [&](int j) { load(&tm_k, idx_k<NQ>(base, j), first + j * KT, row); };
-        auto load_v = [&](int j) { load(&tm_v, idx_v<NQ>(base, j, w.n), first + j * KT, row); };
+        win = first / a.box / 32;
+        look_up(win, 0, row);
+        look_up(win + 1, 1, row);
+        auto load_k = [&](int j) { load(&tm_k, idx_k<NQ>(base, j), first + j * KT, row, false); };
+        auto load_v = [&](int j) { load(&tm_v, idx_v<NQ>(base, j, w.n), first + j * KT, row, true); };
         // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
         // sequences that come along are never used
         const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
