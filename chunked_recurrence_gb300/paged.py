@@ -13,11 +13,57 @@ from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT,
                _dtype_code, _need_cuda, _ptr, _stream, _ws_cache, load)
 
 
+# What a call's layouts come to (sizes, strides, flags, the workspace's size), worked out and
+# checked once for each combination of shapes, strides and dtypes; addresses are never part of it.
+_plans = {}
+
+
+def _plan(key, make):
+    plan = _plans.get(key)
+    if plan is None:
+        plan = make()
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _lay(t):
+    """A tensor's part of a plan's key."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_fns = {}
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(load(), name)
+    return f
+
+
 def _handle(t, stream):
     """The stream of a call on t's device, as an integer."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(t.get_device())
     return _stream(t, stream).value or 0
+
+
+def _empty(like, shape, dtype, stream):
+    """An output of a call on `stream`: memory of that stream, so that its earlier users are done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(_as_stream(like, stream)):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _as_stream(like, stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=like.device)
 
 
 def gdn_rope_inv_freq(rotary_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0, alpha=1.0, beta=32.0):
@@ -68,39 +114,35 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     Returns (q_out, k_out)."""
     x = q if q is not None else k
     _need_cuda(q, k, positions, freqs, q_out, k_out)
-    n_tok, _, D = x.shape
-    if positions.dtype != torch.int64 or positions.numel() != n_tok or not positions.is_contiguous():
-        raise TypeError("positions must be contiguous int64 [n_tok]")
-    rd = _rotary(freqs, D)
-    dtype = x.dtype
 
-    def side(name, t, out):
-        """(input, output, heads, input stride, output stride, output tensor)"""
-        if t is None:
-            return None, None, 0, 0, 0, None
-        if t.shape[0] != n_tok or t.dtype != dtype:
-            raise ValueError("q and k must have the same tokens and dtype")
-        stride = _heads(name, t, D)
-        if out is None:
-            out = torch.empty(t.shape, dtype=dtype, device=t.device)
-            out_stride = 0
-        else:
-            if out.shape != t.shape or out.dtype != dtype:
+    def make():
+        n_tok, _, D = x.shape
+        if positions.dtype != torch.int64 or positions.numel() != n_tok or not positions.is_contiguous():
+            raise TypeError("positions must be contiguous int64 [n_tok]")
+        sides = []
+        for name, t, out in (("q", q, q_out), ("k", k, k_out)):
+            if t is None:
+                sides.append((0, 0, 0))
+                continue
+            if t.shape[0] != n_tok or t.dtype != x.dtype:
+                raise ValueError("q and k must have the same tokens and dtype")
+            if out is not None and (out.shape != t.shape or out.dtype != t.dtype):
                 raise ValueError(f"{name}_out must have {name}'s shape and dtype")
-            out_stride = _heads(name + "_out", out, D)
-        return t.data_ptr(), out.data_ptr(), t.shape[1], stride, out_stride, out
+            sides.append((t.shape[1], _heads(name, t, D), 0 if out is None else _heads(name + "_out", out, D)))
+        (hq, qs, qos), (hk, ks, kos) = sides
+        return _dtype_code(x.dtype), n_tok, hq, hk, D, _rotary(freqs, D), qs, ks, qos, kos
 
-    qp, qop, hq, qs, qos, q_out = side("q", q, q_out)
-    kp, kop, hk, ks, kos, k_out = side("k", k, k_out)
+    plan = _plan(("rope", _lay(q), _lay(k), _lay(positions), _lay(freqs), _lay(q_out), _lay(k_out)), make)
+    if q_out is None and q is not None:
+        q_out = _empty(q, q.shape, q.dtype, stream)
+    if k_out is None and k is not None:
+        k_out = _empty(k, k.shape, k.dtype, stream)
     flags = (GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0) | (GDN_FLAG_ROPE_BACKWARD if backward else 0)
-    st = load().gdn_rope(qp, kp, positions.data_ptr(), None if freqs is None else freqs.data_ptr(), _dtype_code(dtype),
-                         n_tok, hq, hk, D, rd, qs, ks, qos, kos, scale, flags, qop, kop, _handle(x, stream))
+    st = _fn("gdn_rope")(_addr(q), _addr(k), positions.data_ptr(), _addr(freqs), *plan, scale, flags, _addr(q_out),
+                         _addr(k_out), _handle(x, stream))
     if st:
         _check(st, "gdn_rope")
     return q_out, k_out
-
-
-_cache_shapes = {}
 
 
 def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=None, v=None) -> GdnCacheShape:
@@ -108,14 +150,6 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
     pages, slots and heads in memory; D contiguous), page_table int32 [n_seqs, max_pages], seq_lens
     int32 [n_seqs], cu_seqlens int32 [n_seqs + 1] or None, new k, v [n_tok, Hkv, D]."""
     x = q if q is not None else k
-    key = (None if q is None else (q.shape, q.stride()), k_cache.shape, k_cache.stride(), v_cache.shape,
-           v_cache.stride(), page_table.shape, page_table.stride(), seq_lens.shape,
-           None if cu_seqlens is None else cu_seqlens.shape, x.dtype, k_cache.dtype, v_cache.dtype,
-           None if k is None else (k.shape, k.stride(), k.dtype), None if v is None else (v.shape, v.stride(), v.dtype),
-           page_table.dtype, seq_lens.dtype, None if cu_seqlens is None else cu_seqlens.dtype)
-    sh = _cache_shapes.get(key)
-    if sh is not None:
-        return sh
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, D] with the same strides")
     n_pages, page_size, Hkv, D = k_cache.shape
@@ -143,14 +177,10 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
     if Hq % Hkv:
         raise ValueError("Hq must be a multiple of Hkv")
     st = k_cache.stride()
-    sh = GdnCacheShape(n_seqs, n_tok, Hq, Hkv, D, _dtype_code(x.dtype), page_size, n_pages, max_pages,
-                       page_table.stride(0) if n_seqs > 1 else max_pages, st[0], st[1], st[2],
-                       0 if q is None else _heads("q", q, D), 0 if k is None else _heads("k", k, D),
-                       0 if v is None else _heads("v", v, D))
-    if len(_cache_shapes) >= 4096:
-        _cache_shapes.clear()
-    _cache_shapes[key] = sh
-    return sh
+    return GdnCacheShape(n_seqs, n_tok, Hq, Hkv, D, _dtype_code(x.dtype), page_size, n_pages, max_pages,
+                         page_table.stride(0) if n_seqs > 1 else max_pages, st[0], st[1], st[2],
+                         0 if q is None else _heads("q", q, D), 0 if k is None else _heads("k", k, D),
+                         0 if v is None else _heads("v", v, D))
 
 
 def _own_workspace(kind, nbytes, t, stream):
@@ -159,7 +189,12 @@ def _own_workspace(kind, nbytes, t, stream):
     key = (kind, t.get_device(), handle)
     ws = _ws_cache.get(key)
     if ws is None or ws.nbytes < nbytes:
-        ws = _ws_cache[key] = Workspace(nbytes, t.device)
+        if stream is None:
+            ws = Workspace(nbytes, t.device)
+        else:  # cleared on the stream that uses it
+            with torch.cuda.stream(_as_stream(t, stream)):
+                ws = Workspace(nbytes, t.device)
+        _ws_cache[key] = ws
     return ws, handle
 
 
@@ -170,32 +205,34 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     tensor, or q itself).  positions int64 [n_tok] replaces the places in the sequences as rotary
     positions.  Returns q_out (None without q)."""
     _need_cuda(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions, q_out)
-    sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, k, v)
-    rd = _rotary(freqs, sh.D)
-    if positions is not None and (positions.dtype != torch.int64 or positions.shape != (sh.n_tok,)
-                                  or not positions.is_contiguous()):
-        raise TypeError("positions must be contiguous int64 [n_tok]")
-    if q is not None:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+
+    def make():
+        sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, k, v)
+        if positions is not None and (positions.dtype != torch.int64 or positions.shape != (sh.n_tok,)
+                                      or not positions.is_contiguous()):
+            raise TypeError("positions must be contiguous int64 [n_tok]")
+        if q_out is not None and (q is None or q_out.shape != q.shape or q_out.dtype != q.dtype
+                                  or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous with q's shape and dtype")
+        return sh, ctypes.byref(sh), _rotary(freqs, sh.D)
+
+    _, shape, rd = _plan(("append", _lay(q), _lay(k), _lay(v), _lay(k_cache), _lay(v_cache), _lay(page_table),
+                          _lay(seq_lens), _lay(cu_seqlens), _lay(freqs), _lay(positions), _lay(q_out)), make)
+    if q is not None and q_out is None:
+        q_out = _empty(q, q.shape, q.dtype, stream)
     ws, handle = ((workspace, _handle(k, stream)) if workspace is not None
                   else _own_workspace("cache", 256, k, stream))
-    flags = GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0
-    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _check(load().gdn_kv_append(p(q), k.data_ptr(), v.data_ptr(), p(positions), p(freqs), rd, scale, flags,
-                                page_table.data_ptr(), seq_lens.data_ptr(), p(cu_seqlens), ctypes.byref(sh),
-                                None if q is None else p(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.ptr(),
-                                ws.nbytes, handle), "gdn_kv_append")
-    return q_out if q is not None else None
+    st = _fn("gdn_kv_append")(_addr(q), k.data_ptr(), v.data_ptr(), _addr(positions), _addr(freqs), rd, scale,
+                              GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0, page_table.data_ptr(),
+                              seq_lens.data_ptr(), _addr(cu_seqlens), shape, _addr(q_out), k_cache.data_ptr(),
+                              v_cache.data_ptr(), ws.buf.data_ptr(), ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_kv_append")
+    return q_out
 
 
 def gdn_paged_attn_workspace_bytes(shape: GdnCacheShape, max_new: int) -> int:
     return int(load().gdn_paged_attn_workspace_bytes(ctypes.byref(shape), int(max_new)))
-
-
-_attn_bytes = {}
 
 
 def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, max_new=None, scale=None, window=0,
@@ -205,30 +242,31 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
     max_new: a bound on the new tokens of one sequence (default: all of them).  Returns
     (o [n_tok, Hq, D], lse [n_tok, Hq] fp32 or None)."""
     _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
-    sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
-    if max_new is None:
-        max_new = sh.n_tok if cu_seqlens is not None else 1
-    if scale is None:
-        scale = sh.D ** -0.5
+
+    def make():
+        sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
+        if o is not None and (o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous()):
+            raise ValueError("o must be contiguous with q's shape and dtype")
+        if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+            raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
+        new = max_new if max_new is not None else sh.n_tok if cu_seqlens is not None else 1
+        return sh, ctypes.byref(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5, tuple(q.shape[:2])
+
+    _, shape, new, nbytes, unit, rows = _plan(
+        ("attn", _lay(q), _lay(k_cache), _lay(v_cache), _lay(page_table), _lay(seq_lens), _lay(cu_seqlens), _lay(o),
+         _lay(lse), max_new), make)
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
-        raise ValueError("o must be contiguous with q's shape and dtype")
+        o = _empty(q, q.shape, q.dtype, stream)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
-    if workspace is None:
-        nbytes = gdn_paged_attn_workspace_bytes(sh, max_new)
-        ws, handle = _own_workspace("attn", nbytes, q, stream)
-    else:
-        ws, handle = workspace, _handle(q, stream)
+        lse = _empty(q, rows, torch.float32, stream)
+    ws, handle = ((workspace, _handle(q, stream)) if workspace is not None
+                  else _own_workspace("attn", nbytes, q, stream))
     flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
-    _check(load().gdn_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                                 seq_lens.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                                 ctypes.byref(sh), max_new, scale, window, flags, o.data_ptr(),
-                                 None if lse is None else lse.data_ptr(), ws.ptr(), ws.nbytes, handle),
-           "gdn_paged_attn")
+    st = _fn("gdn_paged_attn")(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                               seq_lens.data_ptr(), _addr(cu_seqlens), shape, new, unit if scale is None else scale,
+                               window, flags, o.data_ptr(), _addr(lse), ws.buf.data_ptr(), ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_paged_attn")
     return o, lse
 
 
@@ -238,14 +276,20 @@ def gdn_pages_workspace_bytes(n_pages: int, n_rows: int) -> int:
 
 def _page_tables(page_table, seq_lens, refs, page_size):
     _need_cuda(page_table, seq_lens, refs)
-    for name, t, dims in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("refs", refs, 1)):
-        if t.dtype != torch.int32 or t.dim() != dims or (t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1):
-            raise TypeError(f"{name} must be int32 with contiguous rows")
-    n_rows, max_pages = page_table.shape
-    if seq_lens.shape[0] != n_rows:
-        raise ValueError("seq_lens must have one entry a row of page_table")
-    return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), n_rows, max_pages,
-                         page_table.stride(0) if n_rows > 1 else max_pages, refs.shape[0], page_size)
+
+    def make():
+        for name, t, dims in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("refs", refs, 1)):
+            if t.dtype != torch.int32 or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                raise TypeError(f"{name} must be int32 with contiguous rows")
+        n_rows, max_pages = page_table.shape
+        if seq_lens.shape[0] != n_rows:
+            raise ValueError("seq_lens must have one entry a row of page_table")
+        n_pages = refs.shape[0]
+        return (n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages, n_pages, page_size,
+                gdn_pages_workspace_bytes(n_pages, n_rows))
+
+    *rest, nbytes = _plan(("tables", _lay(page_table), _lay(seq_lens), _lay(refs), page_size), make)
+    return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), *rest), nbytes
 
 
 def _page_list(name, t, n=None):
@@ -260,67 +304,71 @@ def _page_pools(pools, n_pages):
     pools = tuple(pools)
     if len(pools) > GDN_MAX_POOLS:
         raise ValueError(f"at most {GDN_MAX_POOLS} pools")
-    page_bytes = stride = 0
-    for t in pools:
-        _need_cuda(t)
-        if t.dim() < 2 or t.shape[0] != n_pages:
-            raise ValueError("a pool must be [n_pages, ...]")
-        span = 1 + sum((n - 1) * s for n, s in zip(t.shape[1:], t.stride()[1:]))
-        n = t.numel() // n_pages if n_pages else 0
-        if n_pages and span != n:
-            raise ValueError("a pool's pages must each be contiguous")
-        b, s = n * t.element_size(), (t.stride(0) if n_pages > 1 else n) * t.element_size()
-        if page_bytes and (b, s) != (page_bytes, stride):
-            raise ValueError("the pools' pages must have one size and stride")
-        page_bytes, stride = b, s
-    arr = (ctypes.c_void_p * max(1, len(pools)))(*[t.data_ptr() for t in pools])
-    return GdnPagePools(arr, len(pools), page_bytes, stride)
+    _need_cuda(*pools)
+
+    def make():
+        page_bytes = stride = 0
+        for t in pools:
+            if t.dim() < 2 or t.shape[0] != n_pages:
+                raise ValueError("a pool must be [n_pages, ...]")
+            span = 1 + sum((n - 1) * s for n, s in zip(t.shape[1:], t.stride()[1:]))
+            n = t.numel() // n_pages if n_pages else 0
+            if n_pages and span != n:
+                raise ValueError("a pool's pages must each be contiguous")
+            b, s = n * t.element_size(), (t.stride(0) if n_pages > 1 else n) * t.element_size()
+            if page_bytes and (b, s) != (page_bytes, stride):
+                raise ValueError("the pools' pages must have one size and stride")
+            page_bytes, stride = b, s
+        return ctypes.c_void_p * max(1, len(pools)), len(pools), page_bytes, stride
+
+    array, n, page_bytes, stride = _plan(("pools", n_pages, tuple(_lay(t) for t in pools)), make)
+    return GdnPagePools(array(*[t.data_ptr() for t in pools]), n, page_bytes, stride)
 
 
-def _pages_workspace(tables, t, workspace, stream):
+def _pages_workspace(nbytes, t, workspace, stream):
     if workspace is not None:
         return workspace, _handle(t, stream)
-    return _own_workspace("pages", gdn_pages_workspace_bytes(tables.n_pages, tables.n_rows), t, stream)
+    return _own_workspace("pages", nbytes, t, stream)
 
 
 def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, workspace=None, stream=None):
     """Sequences `seqs` grow to `new_lens` tokens (device int32 lists): missing pages come from the free
     ones in rising order.  Nothing changes (GDN_ERR_PAGES in the workspace's status) if they do not suffice."""
-    t = _page_tables(page_table, seq_lens, refs, page_size)
+    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
     n = _page_list("seqs", seqs)
     _page_list("new_lens", new_lens, n)
-    ws, handle = _pages_workspace(t, page_table, workspace, stream)
-    _check(load().gdn_pages_grow(ctypes.byref(t), seqs.data_ptr(), new_lens.data_ptr(), n, ws.ptr(), ws.nbytes,
+    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
+    _check(_fn("gdn_pages_grow")(ctypes.byref(t), seqs.data_ptr(), new_lens.data_ptr(), n, ws.buf.data_ptr(), ws.nbytes,
                                  handle), "gdn_pages_grow")
 
 
 def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, stream=None):
     """Sequences `seqs` give their pages back and become empty."""
-    t = _page_tables(page_table, seq_lens, refs, page_size)
+    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
     n = _page_list("seqs", seqs)
-    ws, handle = _pages_workspace(t, page_table, workspace, stream)
-    _check(load().gdn_pages_free(ctypes.byref(t), seqs.data_ptr(), n, ws.ptr(), ws.nbytes, handle),
+    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
+    _check(_fn("gdn_pages_free")(ctypes.byref(t), seqs.data_ptr(), n, ws.buf.data_ptr(), ws.nbytes, handle),
            "gdn_pages_free")
 
 
 def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_size, workspace=None, stream=None):
     """The empty rows `children` become copies of the rows `parents`: full pages shared, a part-filled last
     page copied in every pool ([n_pages, ...] tensors: the k and v caches of every layer)."""
-    t = _page_tables(page_table, seq_lens, refs, page_size)
+    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
     n = _page_list("parents", parents)
     _page_list("children", children, n)
     p = _page_pools(pools, refs.shape[0])
-    ws, handle = _pages_workspace(t, page_table, workspace, stream)
-    _check(load().gdn_pages_fork(ctypes.byref(t), parents.data_ptr(), children.data_ptr(), n, ctypes.byref(p),
-                                 ws.ptr(), ws.nbytes, handle), "gdn_pages_fork")
+    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
+    _check(_fn("gdn_pages_fork")(ctypes.byref(t), parents.data_ptr(), children.data_ptr(), n, ctypes.byref(p),
+                                 ws.buf.data_ptr(), ws.nbytes, handle), "gdn_pages_fork")
 
 
 def gdn_pages_compact(page_table, seq_lens, refs, pools, page_size, workspace=None, stream=None):
     """The live pages come together at the start of the pools; tables and refs follow."""
-    t = _page_tables(page_table, seq_lens, refs, page_size)
+    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
     p = _page_pools(pools, refs.shape[0])
-    ws, handle = _pages_workspace(t, page_table, workspace, stream)
-    _check(load().gdn_pages_compact(ctypes.byref(t), ctypes.byref(p), ws.ptr(), ws.nbytes, handle),
+    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
+    _check(_fn("gdn_pages_compact")(ctypes.byref(t), ctypes.byref(p), ws.buf.data_ptr(), ws.nbytes, handle),
            "gdn_pages_compact")
 
 
@@ -333,5 +381,5 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     p = _page_pools(pools, n_pages)
     ws, handle = ((workspace, _handle(src, stream)) if workspace is not None
                   else _own_workspace("pages", 256, src, stream))
-    _check(load().gdn_pages_copy(src.data_ptr(), dst.data_ptr(), n, n_pages, ctypes.byref(p), ws.ptr(), ws.nbytes,
-                                 handle), "gdn_pages_copy")
+    _check(_fn("gdn_pages_copy")(src.data_ptr(), dst.data_ptr(), n, n_pages, ctypes.byref(p), ws.buf.data_ptr(),
+                                 ws.nbytes, handle), "gdn_pages_copy")
