@@ -69,7 +69,8 @@ struct TcArgs {
   int32_t G, RT, Hkv, page_size, box, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole tokens
   float c;  // scale log2 e
   float *part, *part_ml;
-  int4 *meta;
+  int4 *meta;  // [blocks][2]: how the share's first piece goes on (1: beyond it, 2: to its item's end), whether its last
+               // one begins an item that the next share continues, that item's head and rows; its first token and row
   int32_t *status;
   int32_t no_wait;
 };
@@ -79,7 +80,8 @@ struct Ctl {
   uint32_t tmem;
   volatile int abort;
   int64_t sum[12];
-  int start_slot, start_seq, start_h, start_u;
+  int start_slot, start_h, start_u;
+  Item start;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
@@ -185,10 +187,9 @@ __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int s
   return false;
 }
 template <int KT>
-__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, int slot, int seq, int h, int u,
-                                           int64_t left) {
-  w.slot = slot, w.h = h, w.u = u, w.left = left;
-  w.it = item_of(a.seqs, seq, slot, a.G, R, KT, a.window);
+__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, const Ctl &c, int64_t left) {
+  w.slot = c.start_slot, w.h = c.start_h, w.u = c.start_u, w.left = left;
+  w.it = c.start;
   w.units = item_units(w.it, kOver);
   return walk_cut(w) || walk_next<KT>(a, w, R, slots);
 }
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   launch_dependents();
 
   if (tid == 0) {
+    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     ctl.abort = 0;
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.full[i], 1);
@@ -285,6 +287,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     }
     mbar_init(&ctl.drain, 1);
     fence_mbar_init();
+  }
+  if (warp == kWarpTma && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
   }
 
   // ---- this block's share: the units of all slots summed, then the slot its first unit lies in.  The lengths and
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   const int64_t begin = share_begin(total, min((int)blockIdx.x, blocks), max(blocks, 1));
   const int64_t end = share_begin(total, min((int)blockIdx.x + 1, blocks), max(blocks, 1));
   if (begin >= end) {
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == kWarpMma) tmem_dealloc(ctl.tmem, 512);
     return;
   }
   int64_t before = 0;
@@ -348,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const int64_t from = before + upto + x - cost;  // units before this slot
     if (cost > 0 && begin >= from && begin < from + cost) {
       ctl.start_slot = s;
-      ctl.start_seq = slot_seq(sq, s, a.G, R);
+      ctl.start = item_at(sq, s, a.G, R, KT, a.window);
       ctl.start_h = (int)((begin - from) / units);
       ctl.start_u = (int)((begin - from) % units);
     }
@@ -356,10 +367,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     if (before > begin) break;
   }
 
-  if (warp == kWarpMma) {
-    tmem_alloc(&ctl.tmem, 512);
-    tmem_relinquish();
-  }
   tc_fence_before();
   fence_proxy_async_smem();  // the lengths' reads of the ring end before copies into it
   __syncthreads();
@@ -376,8 +383,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 
   if (warp == kWarpTma) {
     // ================================================= Q tiles; K and V granules, page by page
-    if (NQ == 2) set_regs_down<88>();
-    more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+    if (NQ == 2) set_regs_down<104>();
+    more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
@@ -421,11 +428,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         tma_load_4d(ring + slot * C::kGran + p * C::kPanel + i * box_bytes, map, &ctl.full[slot], 64 * p, sl, w.h, pg);
       issued = idx + 1;
     };
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
     while (more && ok) {
       if (w.it.n_tiles > 0) {
         const int32_t *row = a.table + (int64_t)w.it.s * a.table_stride;
@@ -465,9 +467,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     if (!ok && lane == 0) fail();
   } else if (warp == kWarpMma) {
     // ================================================= MMAs
-    if (NQ == 2) set_regs_down<88>();
+    if (NQ == 2) set_regs_down<104>();
     if (lane == 0) {
-      more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+      more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
       const uint32_t id_s = idesc_bf16(128, KT, false, false);
       const uint32_t id_o = idesc_bf16(128, D, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
@@ -548,26 +550,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
     }
   } else if (warp > kWarpMma) {
-    if (NQ == 2) set_regs_down<88>();
+    if (NQ == 2) set_regs_down<104>();
   } else {
     // ================================================= softmax: a thread owns a query row
-    if (NQ == 2) set_regs_up<208>();
-    more = walk_begin<KT>(a, w, R, slots, ctl.start_slot, ctl.start_seq, ctl.start_h, ctl.start_u, end - begin);
+    if (NQ == 2) set_regs_up<200>();
+    more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lq = (uint32_t)(quarter * 32) << 16;
     const float lag = kLag / a.c;
     const uint64_t c2 = f2_pack(a.c, a.c);
     uint32_t base = 0, steps = 0, sphase[2] = {0, 0}, pieces = 0;
-    int cont = 0, head = 0, head_slot = 0, head_h = 0;
     bool ok = true;
     while (more && ok) {
       const Item &it = w.it;
       const int rr = t * a.RT + r;
       const bool valid = r < a.RT && rr < it.rows;
-      const int row = it.row0 + (valid ? rr : 0), i = row / a.G, g = row - i * a.G;
-      const int64_t out = (int64_t)(it.t0 + i) * (a.G * a.Hkv) + w.h * a.G + g;
+      // this thread's row of o, worked out where it is needed: the loop's registers are few
+      auto out_row = [&]() {
+        const int row = it.row0 + rr, i = row / a.G, g = row - i * a.G;
+        return (int64_t)(it.t0 + i) * (a.G * a.Hkv) + w.h * a.G + g;
+      };
       if (it.n_tiles == 0) {  // rows that see nothing
         if (valid) {
+          const int64_t out = out_row();
           for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.o + out * D + d) = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[out] = -INFINITY;
         }
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const int first = (it.tile0 + w.j) * KT;
       if (t < nt) {
         const bool live = t * a.RT + quarter * 32 < it.rows && quarter * 32 < a.RT;  // this warp has a row
-        const int p = it.first + i;
+        const int p = it.first + (it.row0 + rr) / a.G;
         const int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
         const bool releases = t == nt - 1;  // this warpgroup gives ring slots back
@@ -706,6 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           tc_fence_after();
         }
         if (ok && live) {
+          const int64_t out = out_row();
           const uint32_t to = tm + lq + C::kO + t * D;
           if (begins && ends) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -758,12 +764,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         ++pieces;
       }
       base += 2 * n;
-      if (!begins) cont = ends ? 2 : 1;
-      else if (!ends) head = 1, head_slot = w.slot, head_h = w.h;
+      if (tid == 0) {
+        if (!begins) {
+          a.meta[2 * blockIdx.x].x = ends ? 2 : 1;
+        } else if (!ends) {
+          a.meta[2 * blockIdx.x].y = 1, a.meta[2 * blockIdx.x].z = w.h, a.meta[2 * blockIdx.x].w = it.rows;
+          a.meta[2 * blockIdx.x + 1] = make_int4(it.t0, it.row0, 0, 0);
+        }
+      }
       more = walk_next<KT>(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
-    if (tid == 0) a.meta[blockIdx.x] = make_int4(cont, head, head_slot, head_h);
   }
   __syncwarp();
   tc_fence_before();
@@ -786,27 +797,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 // columns over the pieces, and the rows go out through shared memory, whole rows at a time.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
-  constexpr int R = Cfg<D, NQ>::R, KT = Cfg<D, NQ>::KT, kV = D / 32;  // fours of columns a warp
+  constexpr int R = Cfg<D, NQ>::R, kV = D / 32;  // fours of columns a warp
   __shared__ uint2 rows[32][D / 4 + 1];
   __shared__ float weight[kSms][32], part[2][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
-  const int4 me = a.meta[blockIdx.x];
-  if (!me.y) return;
+  const int4 me = a.meta[2 * blockIdx.x], me_at = a.meta[2 * blockIdx.x + 1];
   int n = 0;  // pieces after the first
   for (int base = blockIdx.x + 1;; base += 32) {
     const int b = base + lane;
-    const uint32_t stop = __ballot_sync(0xffffffffu, b >= blocks || a.meta[b].x != 1);
+    const int how = b < blocks ? a.meta[2 * b].x : 0;
+    const uint32_t stop = __ballot_sync(0xffffffffu, how != 1);
     if (stop) {
       n += __ffs(stop);
+      if (__shfl_sync(0xffffffffu, how, __ffs(stop) - 1) != 2) return;  // no item of this block's, or a share that gave up
       break;
     }
     n += 32;
   }
-  if ((int)blockIdx.x + n >= blocks || a.meta[blockIdx.x + n].x != 2) return;  // a share that gave up
-  const Item it = item_at(a.seqs, me.z, a.G, a.RT * NQ, KT, a.window);
-  const int lr = blockIdx.y * 32 + lane, t = lr / 128, rr = t * a.RT + lr % 128;  // lane row, row of the item
-  const bool valid = lr % 128 < a.RT && rr < it.rows;
+  if (!me.y) return;
+  const int item_rows = me.w, lr = blockIdx.y * 32 + lane, t = lr / 128, rr = t * a.RT + lr % 128;  // lane row, row of the item
+  const bool valid = lr % 128 < a.RT && rr < item_rows;
   if (!__any_sync(0xffffffffu, valid)) return;  // the same for all warps
   // piece i is slot 2 b + 1 of block b for the first, 2 (b + i) for the others
   auto at = [&](int i) { return 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
@@ -814,6 +825,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blo
     return valid && i <= n ? *reinterpret_cast<const float2 *>(a.part_ml + (at(i) * R + lr) * 2)
                            : make_float2(-INFINITY, 0.f);
   };
+  constexpr int kAhead = 16 / kV;  // pieces in flight
+  float4 v[kAhead][kV];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float4 *p = reinterpret_cast<const float4 *>(a.part) + at(i0 + i) * (R * D / 4) + (warp * kV) * R + lr;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) v[i][e] = i0 + i <= n && valid ? p[e * R] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(0);
   float top = -INFINITY;
 #pragma unroll 4
   for (int i = warp; i <= n; i += 8) top = fmaxf(top, ml_of(i).x);
@@ -837,16 +859,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blo
   float4 x[kV];
 #pragma unroll
   for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = 16 / kV;  // pieces in flight
   for (int i0 = 0; i0 <= n; i0 += kAhead) {
-    float4 v[kAhead][kV];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float4 *p = reinterpret_cast<const float4 *>(a.part) + at(i0 + i) * (R * D / 4) + (warp * kV) * R + lr;
-#pragma unroll
-      for (int e = 0; e < kV; ++e)
-        v[i][e] = i0 + i <= n && valid ? p[e * R] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const float f = i0 + i <= n ? weight[i0 + i][lane] : 0.f;
@@ -859,13 +872,14 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blo
           x[e].w = fmaf(f, v[i][e].w, x[e].w);
         }
     }
+    if (i0 + kAhead <= n) load(i0 + kAhead);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int e = 0; e < kV; ++e)
     rows[lane][warp * kV + e] = make_uint2(bf16x2(x[e].x * inv, x[e].y * inv), bf16x2(x[e].z * inv, x[e].w * inv));
-  const int row = it.row0 + rr, i = row / a.G, g = row - i * a.G;
-  const int64_t out = valid ? (int64_t)(it.t0 + i) * (a.G * a.Hkv) + me.w * a.G + g : -1;
+  const int row = me_at.y + rr, i = row / a.G, g = row - i * a.G;
+  const int64_t out = valid ? (int64_t)(me_at.x + i) * (a.G * a.Hkv) + me.z * a.G + g : -1;
   if (valid && warp == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
   __syncthreads();
   for (int q = warp; q < 32; q += 8) {
@@ -922,7 +936,7 @@ gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs
     return GDN_ERR_CUDA;
   char *w = (char *)a.status;
   a.meta = (int4 *)(w + 256);
-  a.part_ml = (float *)(w + 256 + sizeof(int4) * 256);
+  a.part_ml = (float *)(w + 256 + sizeof(int4) * 512);
   a.part = a.part_ml + (size_t)kSms * 2 * C::R * 2;
   constexpr int smem = kData + 1024;
   if (cudaFuncSetAttribute(paged_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -968,7 +982,7 @@ bool paged_attn_tc_supported(const void *q, const void *k, const void *v, const 
 size_t paged_attn_tc_workspace(const gdn_cache_shape &s, int32_t max_new) {
   if (!tc_shape(s)) return 0;
   const size_t rows = (size_t)kSms * 2 * (two_tiles(s, max_new) ? 256 : 128);
-  return 256 + sizeof(int4) * 256 + rows * (2 + s.D) * sizeof(float);
+  return 256 + sizeof(int4) * 512 + rows * (2 + s.D) * sizeof(float);
 }
 
 gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int32_t *table, const PagedSeqs &seqs,
