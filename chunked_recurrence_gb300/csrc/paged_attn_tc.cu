@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <numeric>
+#include <type_traits>
 
 #include "common.cuh"
 #include "conv_tap.cuh"
@@ -45,14 +46,20 @@ constexpr float kLag = 8.f;          // m may lag by this many powers of two
 
 constexpr int kOver = 2;              // units an item costs beyond its tiles
 
-template <int D, int NQ>
+template <int D, int NQ, bool PAIR>
 struct Cfg {
-  static constexpr int R = 128 * NQ;                    // rows of TMEM lanes; an item fills tile_rows() of each 128
-  static constexpr int KT = D == 256 ? 64 : 128;        // positions a tile
-  static constexpr int kGran = KT * D * 2;              // bytes of a granule: a tile of K or V
-  static constexpr int kQ = R * D * 2;
-  static constexpr int kSlots = (kData - kQ) / kGran;
-  static constexpr int kPanel = KT * 128;               // bytes of 64 columns of it
+  static constexpr int kPair = PAIR ? 2 : 1;            // blocks (of one cluster) that share an item
+  static constexpr int kTiles = NQ * kPair;             // 128-row tiles of an item
+  static constexpr int R = 128 * kTiles;                // TMEM lanes of an item; it fills RT of each 128
+  static constexpr int KT = D == 256 && !PAIR ? 64 : 128; // positions a tile
+  // A granule is a block's part of a tile of K or V.  A pair's MMA takes its second operand in halves of N from the two
+  // blocks: of K half the positions, of V half the columns.
+  static constexpr int kGran = KT * D * 2 / kPair;      // bytes
+  static constexpr int kRowsK = KT / kPair;
+  static constexpr int kPanelK = kRowsK * 128, kPanelV = KT * 128;  // bytes of 64 columns of it
+  static constexpr int kPanelsK = D / 64, kPanelsV = D / 64 / kPair;
+  static constexpr int kQ = 128 * NQ * D * 2;
+  static constexpr int kSlots = (kData - kQ) / kGran < 16 ? (kData - kQ) / kGran : 16;
   // softmax warpgroups, then the TMA and MMA warps; with two tiles a whole warpgroup for those, so that the
   // registers can be split between the warpgroups
   static constexpr int kThreads = NQ == 2 ? 384 : 192;
@@ -76,7 +83,7 @@ struct TcArgs {
 };
 
 struct Ctl {
-  uint64_t full[16], empty[16], sfull[2], pready[2][2], odone[2], qfull[2], qfree[2], drain;
+  uint64_t full[16], empty[16], land[16], sfull[2], pready[2][2], odone[2], qfull[2], qfree[2], drain;
   uint32_t tmem;
   volatile int abort;
   int64_t sum[12];
@@ -93,15 +100,86 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// The forms for a pair of blocks.  Their barriers are named by cluster addresses.
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                                 int c3) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// Arrivals at the other block's barrier order no memory of this block at cluster scope: a release at that
+// scope takes some 700 cycles, and P (tensor memory, ordered by the tcgen05 fences) and the copies (counted in
+// bytes) do not need it.  Where plain stores have to be seen, the caller fences.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// The MMAs and their commits, of one block or (issued by its first block) of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma_bf16(d, a, b, idesc, accumulate);
+}
+// both blocks' barrier at this place (PAIR), or this block's
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+template <bool PAIR>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t *r) {
@@ -255,34 +333,39 @@ __device__ __forceinline__ uint32_t idx_v(uint32_t base, int j, int n) {
   return base + (NQ == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1));
 }
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
+template <int D, int NQ, bool PAIR>
+__global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TcArgs a) {
-  using C = Cfg<D, NQ>;
+  using C = Cfg<D, NQ, PAIR>;
   constexpr int KT = C::KT, kSlots = C::kSlots;
-  static_assert(KT / 8 * (D / 64) <= 32, "a granule has at most one box a lane");
+  static_assert(C::kRowsK / 8 * C::kPanelsK <= 32 && KT / 8 * C::kPanelsV <= 32, "a granule has at most one box a lane");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = sm + C::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarps = C::kThreads / 32;
+  // a share belongs to a block, or to a pair of them: then rank 1 takes every second row tile and its halves of
+  // K and V, and rank 0 issues the MMAs of both, waiting on its own barriers, where both blocks arrive
+  const int rank = PAIR ? (int)cluster_ctarank() : 0, unit = blockIdx.x / C::kPair, units = gridDim.x / C::kPair;
+  auto leader = [&](uint64_t *bar) { return PAIR ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar); };
   launch_dependents();
 
   if (tid == 0) {
-    a.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (rank == 0) a.meta[2 * unit] = make_int4(0, 0, 0, 0);
     ctl.abort = 0;
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.full[i], C::kPair);
       mbar_init(&ctl.empty[i], 1);
+      mbar_init(&ctl.land[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.sfull[i], 1);
-      mbar_init(&ctl.pready[i][0], 4);  // the two halves of P apart: a warp may be done with both
-      mbar_init(&ctl.pready[i][1], 4);  // before another is with its first
+      mbar_init(&ctl.pready[i][0], 4 * C::kPair);  // the two halves of P apart: a warp may be done with both
+      mbar_init(&ctl.pready[i][1], 4 * C::kPair);  // before another is with its first
       mbar_init(&ctl.odone[i], 1);
-      mbar_init(&ctl.qfull[i], 1);
+      mbar_init(&ctl.qfull[i], C::kPair);
       mbar_init(&ctl.qfree[i], 1);
     }
     mbar_init(&ctl.drain, 1);
@@ -294,13 +377,26 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   if (warp == kWarpMma) {
-    tmem_alloc(&ctl.tmem, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&ctl.tmem, 512);
+    } else {
+      tmem_alloc(&ctl.tmem, 512);
+      tmem_relinquish();
+    }
   }
+  auto free_tmem = [&](uint32_t t) {
+    if constexpr (PAIR) tmem_dealloc_pair(t, 512);
+    else tmem_dealloc(t, 512);
+  };
+  // every thread of the block, or of the pair
+  auto sync_all = [&]() {
+    if constexpr (PAIR) cluster_sync_all();
+    else __syncthreads();
+  };
 
   // ---- this block's share: the units of all slots summed, then the slot its first unit lies in.  The lengths and
   // offsets go through shared memory (where the ring will be), so that the search in them does not wait on L2.
-  const int R = a.RT * NQ;
+  const int R = a.RT * C::kTiles;
   const int slots = (int)item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, R);
   PagedSeqs sq = a.seqs;
   if (a.seqs.n_seqs < C::kSlots * C::kGran / 8 - 1) {
@@ -329,11 +425,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   int64_t total = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) total += ctl.sum[i];
-  const int blocks = (int)min((int64_t)gridDim.x, total);  // shares of at least a unit, to the first blocks
-  const int64_t begin = share_begin(total, min((int)blockIdx.x, blocks), max(blocks, 1));
-  const int64_t end = share_begin(total, min((int)blockIdx.x + 1, blocks), max(blocks, 1));
-  if (begin >= end) {
-    if (warp == kWarpMma) tmem_dealloc(ctl.tmem, 512);
+  const int shares = (int)min((int64_t)units, total);  // of at least a unit, to the first blocks
+  const int64_t begin = share_begin(total, min(unit, shares), max(shares, 1));
+  const int64_t end = share_begin(total, min(unit + 1, shares), max(shares, 1));
+  if (begin >= end) {  // both blocks of a pair
+    sync_all();
+    if (warp == kWarpMma) free_tmem(ctl.tmem);
     return;
   }
   int64_t before = 0;
@@ -369,14 +466,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 
   tc_fence_before();
   fence_proxy_async_smem();  // the lengths' reads of the ring end before copies into it
-  __syncthreads();
+  sync_all();
   tc_fence_after();
   const uint32_t tm = ctl.tmem;
   volatile int *abort_flag = &ctl.abort;
   auto fail = [&]() {
     *abort_flag = 1;
+    if (PAIR) store_cluster(mapa_shared(smem_u32(const_cast<int *>(&ctl.abort)), rank ^ 1), 1);
     set_status(a.status, GDN_ERR_TIMEOUT);
   };
+  uint32_t landed = 0;  // PAIR: phase bits of the land barriers, as this warp has used them
   uint32_t issued = 0, q_issued[2] = {0, 0};  // granules and Q tiles (the TMA warp's count)
   Walk w;
   bool more = false;
@@ -403,11 +502,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
     };
     // a granule of K or V: its boxes (rows x 64-column panels) over the lanes, all in one instruction
-    auto load = [&](const CUtensorMap *map, uint32_t idx, int pos0, const int32_t *row, bool last) {
+    auto load = [&](auto is_v, uint32_t idx, int pos0, const int32_t *row) {
+      constexpr bool V = decltype(is_v)::value;
+      constexpr int kPanels = V ? C::kPanelsV : C::kPanelsK, kPanel = V ? C::kPanelV : C::kPanelK;
+      const CUtensorMap *map = V ? &tm_v : &tm_k;
       const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
-      constexpr int kPanels = D / 64;
-      const int nb = KT / a.box, b0 = pos0 / a.box;  // nb divides 32: a granule lies in one window
-      if (last && b0 / 32 > win) {
+      // nb divides 32: a granule lies in one window
+      const int nb = (V ? KT : C::kRowsK) / a.box, b0 = (pos0 + (V ? 0 : rank * C::kRowsK)) / a.box;
+      if (V && b0 / 32 > win) {
         ++win;
         page[0] = page[1], at[0] = at[1];
         look_up(win + 1, 1, row);
@@ -417,15 +519,32 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const int at0 = __shfl_sync(0xffffffffu, at[0], from), at1 = __shfl_sync(0xffffffffu, at[1], from);
       const bool ahead = b0 / 32 > win;
       const int pg = i >= nb ? -1 : ahead ? pg1 : pg0, sl = ahead ? at1 : at0;
-      const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
       if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
         ok = false;
         return;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], __popc(there) * box_bytes);
-      __syncwarp();
-      if (pg >= 0)
-        tma_load_4d(ring + slot * C::kGran + p * C::kPanel + i * box_bytes, map, &ctl.full[slot], 64 * p, sl, w.h, pg);
+      uint8_t *to = ring + slot * C::kGran + p * kPanel + i * box_bytes;
+      if constexpr (PAIR) {
+        // V rows that become zeros: the copy reports to this block, whose softmax holds the product back
+        const bool here = V && (pos0 < w.it.lo || pos0 + KT > w.it.hi);
+        const uint32_t bar = here ? smem_u32(&ctl.land[slot]) : leader(&ctl.full[slot]);
+        if (lane == 0) {
+          if (here) {
+            mbar_arrive_expect_tx(&ctl.land[slot], bytes);
+            arrive_cluster(leader(&ctl.full[slot]));
+          } else {
+            arrive_expect_cluster(bar, bytes);
+          }
+        }
+        if (here) landed = (landed ^ (landed >> (16 + slot) & 1) << slot) | 1u << (16 + slot);
+        __syncwarp();
+        if (pg >= 0) tma_load_4d_pair(to, map, bar, 64 * (p + (V ? rank * kPanels : 0)), sl, w.h, pg);
+      } else {
+        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
+        __syncwarp();
+        if (pg >= 0) tma_load_4d(to, map, &ctl.full[slot], 64 * p, sl, w.h, pg);
+      }
       issued = idx + 1;
     };
     while (more && ok) {
@@ -435,21 +554,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         win = first / a.box / 32;
         look_up(win, 0, row);
         look_up(win + 1, 1, row);
-        auto load_k = [&](int j) { load(&tm_k, idx_k<NQ>(base, j), first + j * KT, row, false); };
-        auto load_v = [&](int j) { load(&tm_v, idx_v<NQ>(base, j, w.n), first + j * KT, row, true); };
+        auto load_k = [&](int j) { load(std::false_type{}, idx_k<NQ>(base, j), first + j * KT, row); };
+        auto load_v = [&](int j) { load(std::true_type{}, idx_v<NQ>(base, j, w.n), first + j * KT, row); };
         // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
         // sequences that come along are never used
-        const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
+        const int nt = NQ == 2 && w.it.rows > a.RT * C::kPair ? 2 : 1;
         for (int t = 0; t < nt && ok; ++t) {
           if (!warp_wait(&ctl.qfree[t], (q_issued[t] & 1) ^ 1, abort_flag)) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl.qfull[t], a.RT * D * 2);
-            for (int p = 0; p < D / 64; ++p)
-              tma_load_3d(sm + t * 128 * D * 2 + p * 16384, &tm_q, &ctl.qfull[t], 64 * p, w.h * a.G,
-                          w.it.t0 + w.it.row0 / a.G + t * (a.RT / a.G));
+            const int tok = w.it.t0 + w.it.row0 / a.G + (t * C::kPair + rank) * (a.RT / a.G);
+            if constexpr (PAIR) arrive_expect_cluster(leader(&ctl.qfull[t]), a.RT * D * 2);
+            else mbar_arrive_expect_tx(&ctl.qfull[t], a.RT * D * 2);
+            for (int p = 0; p < D / 64; ++p) {
+              uint8_t *to = sm + t * 128 * D * 2 + p * 16384;
+              if constexpr (PAIR) tma_load_3d_pair(to, &tm_q, leader(&ctl.qfull[t]), 64 * p, w.h * a.G, tok);
+              else tma_load_3d(to, &tm_q, &ctl.qfull[t], 64 * p, w.h * a.G, tok);
+            }
           }
           __syncwarp();
           ++q_issued[t];
@@ -468,19 +591,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else if (warp == kWarpMma) {
     // ================================================= MMAs
     if (NQ == 2) set_regs_down<104>();
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
-      const uint32_t id_s = idesc_bf16(128, KT, false, false);
-      const uint32_t id_o = idesc_bf16(128, D, false, true);
+      const uint32_t id_s = idesc_bf16(128 * C::kPair, KT, false, false);
+      const uint32_t id_o = idesc_bf16(128 * C::kPair, D, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint64_t d_k = smem_desc(smem_u32(ring), 16, 1024, 2);
-      const uint64_t d_v = smem_desc(smem_u32(ring), C::kPanel, 1024, 2);
+      const uint64_t d_v = smem_desc(smem_u32(ring), C::kPanelV, 1024, 2);
       uint32_t base = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // steps: P tiles consumed, per TMEM slot
       uint32_t total_steps = 0;                                  // NQ = 1: the S slots alternate across pieces
       bool ok = !a.no_wait;
-      auto wait_full = [&](uint32_t idx) {
-        if (ok && !mbar_wait_spin(&ctl.full[idx % kSlots], (idx / kSlots) & 1, kSpin, abort_flag)) ok = false;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!ok) return;
+        ok = mbar_wait_spin(bar, parity, kSpin, abort_flag);
       };
+      auto wait_full = [&](uint32_t idx) { wait(&ctl.full[idx % kSlots], (idx / kSlots) & 1); };
       // S[slot] = Q[t] K(j)^T
       auto issue_s = [&](int t, int slot, int j) {
         const uint32_t idx = idx_k<NQ>(base, j);
@@ -491,10 +616,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const uint64_t dq = d_q + ((t * 128 * D * 2) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16(tm + slot * KT, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                    dk + (((ks >> 2) * C::kPanel + (ks & 3) * 32) >> 4), id_s, ks > 0);
-        umma_commit(&ctl.sfull[slot]);
-        if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
+          mma_ss<PAIR>(tm + slot * KT, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                       dk + (((ks >> 2) * C::kPanelK + (ks & 3) * 32) >> 4), id_s, ks > 0);
+        commit<PAIR>(&ctl.sfull[slot]);
+        if (NQ == 1) commit<PAIR>(&ctl.empty[idx % kSlots]);
       };
       // O[t] (+)= P[slot] V(j), the first half of the positions as soon as their P is there
       auto issue_o = [&](int t, int slot, int j) {
@@ -502,25 +627,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_spin(&ctl.pready[slot][half], steps[slot] & 1, kSpin, abort_flag)) {
-            ok = false;
-            return;
-          }
+          wait(&ctl.pready[slot][half], steps[slot] & 1);
           if (half == 0) wait_full(idx);
           if (!ok) return;
           tc_fence_after();
 #pragma unroll
           for (int ks = half * (KT / 32); ks < (half + 1) * (KT / 32); ++ks)
-            umma_ts(tm + C::kO + t * D, tm + slot * KT + ks * 8, dv + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
+            mma_ts<PAIR>(tm + C::kO + t * D, tm + slot * KT + ks * 8, dv + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
         }
         ++steps[slot];
-        if (NQ == 1) umma_commit(&ctl.empty[idx % kSlots]);
+        if (NQ == 1) commit<PAIR>(&ctl.empty[idx % kSlots]);
       };
       while (more && ok) {
         const int n = w.it.n_tiles > 0 ? w.n : 0;
         if (n > 0) {
-          const int nt = NQ == 2 && w.it.rows > a.RT ? 2 : 1;
-          for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_spin(&ctl.qfull[t], pieces[t]++ & 1, kSpin, abort_flag);
+          const int nt = NQ == 2 && w.it.rows > a.RT * C::kPair ? 2 : 1;
+          for (int t = 0; t < nt && ok; ++t) wait(&ctl.qfull[t], pieces[t]++ & 1);
           if (!ok) break;
           tc_fence_after();
           if (NQ == 2) {
@@ -530,7 +652,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                 issue_o(t, t, j);
                 if (!ok) break;
                 if (j + 1 < n) issue_s(t, t, j + 1);
-                else umma_commit(&ctl.odone[t]);
+                else commit<PAIR>(&ctl.odone[t]);
               }
           } else {
             issue_s(0, total_steps & 1, 0);
@@ -545,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
         if (!ok) fail();
-        umma_commit(&ctl.drain);
+        commit<PAIR>(&ctl.drain);
         mbar_wait(&ctl.drain, 0, kSpin);
       }
     }
@@ -557,13 +679,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lq = (uint32_t)(quarter * 32) << 16;
+    auto p_ready = [&](int slot, int half) {
+      if constexpr (PAIR) arrive_cluster(leader(&ctl.pready[slot][half]));
+      else mbar_arrive(&ctl.pready[slot][half]);
+    };
     const float lag = kLag / a.c;
     const uint64_t c2 = f2_pack(a.c, a.c);
     uint32_t base = 0, steps = 0, sphase[2] = {0, 0}, pieces = 0;
     bool ok = true;
     while (more && ok) {
       const Item &it = w.it;
-      const int rr = t * a.RT + r;
+      const int tile = t * C::kPair + rank, rr = tile * a.RT + r;
       const bool valid = r < a.RT && rr < it.rows;
       // this thread's row of o, worked out where it is needed: the loop's registers are few
       auto out_row = [&]() {
@@ -579,11 +705,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         more = walk_next<KT>(a, w, R, slots);
         continue;
       }
-      const int n = w.n, nt = NQ == 2 && it.rows > a.RT ? 2 : 1;
+      const int n = w.n, nt = NQ == 2 && it.rows > a.RT * C::kPair ? 2 : 1;
       const bool begins = w.j == 0, ends = w.j + w.n == it.n_tiles;
       const int first = (it.tile0 + w.j) * KT;
       if (t < nt) {
-        const bool live = t * a.RT + quarter * 32 < it.rows && quarter * 32 < a.RT;  // this warp has a row
+        const bool live = tile * a.RT + quarter * 32 < it.rows && quarter * 32 < a.RT;  // this warp has a row
         const int p = it.first + (it.row0 + rr) / a.G;
         const int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
@@ -610,18 +736,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             // positions that no row sees: their V rows become zeros (P is 0 there, and 0 * NaN is not)
             const int x = pos + r;
             const uint32_t idx = idx_v<NQ>(base, j, n);
-            if (!warp_wait(&ctl.full[idx % kSlots], (idx / kSlots) & 1, abort_flag)) {
+            uint64_t *there = PAIR ? &ctl.land[idx % kSlots] : &ctl.full[idx % kSlots];
+            if (!warp_wait(there, PAIR ? landed >> (idx % kSlots) & 1 : (idx / kSlots) & 1, abort_flag)) {
               ok = false;
               break;
             }
+            landed ^= 1u << (idx % kSlots);
             if (r < KT && (x < it.lo || x >= it.hi)) {
               uint8_t *vr = ring + (idx % kSlots) * C::kGran + r * 128;
-              for (int pn = 0; pn < D / 64; ++pn)
+              for (int pn = 0; pn < C::kPanelsV; ++pn)
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
-                  *reinterpret_cast<uint4 *>(vr + pn * C::kPanel + ch * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4 *>(vr + pn * C::kPanelV + ch * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
+            if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
           if (live) {
             const uint32_t ts = tm + lq + slot * KT;
@@ -684,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.pready[slot][half]);
+              if (lane == 0) p_ready(slot, half);
             }
             float s0, s1, s2, s3;
             f2_unpack(sum0, s0, s1);
@@ -694,8 +823,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(&ctl.pready[slot][0]);
-              mbar_arrive(&ctl.pready[slot][1]);
+              p_ready(slot, 0);
+              p_ready(slot, 1);
             }
           }
         }
@@ -742,8 +871,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             if (valid && a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
           } else {
             // the piece as [column / 4][row] fours, so that neighbouring rows lie side by side
-            const int64_t which = 2 * blockIdx.x + (begins ? 1 : 0);
-            uint4 *pp = reinterpret_cast<uint4 *>(a.part) + which * (C::R * D / 4) + t * 128 + r;
+            const int64_t which = 2 * unit + (begins ? 1 : 0);
+            uint4 *pp = reinterpret_cast<uint4 *>(a.part) + which * (C::R * D / 4) + tile * 128 + r;
 #pragma unroll 2
             for (int x = 0; x < D; x += 32) {
               uint32_t u[32];
@@ -757,19 +886,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                   pp[(x + y) / 4 * C::R] = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
             }
             if (valid)
-              *reinterpret_cast<float2 *>(a.part_ml + (which * C::R + t * 128 + r) * 2) = make_float2(m * a.c, l);
+              *reinterpret_cast<float2 *>(a.part_ml + (which * C::R + tile * 128 + r) * 2) = make_float2(m * a.c, l);
           }
         }
         tc_fence_before();
         ++pieces;
       }
       base += 2 * n;
-      if (tid == 0) {
+      if (tid == 0 && rank == 0) {
+        int4 *me = a.meta + 2 * unit;
         if (!begins) {
-          a.meta[2 * blockIdx.x].x = ends ? 2 : 1;
+          me->x = ends ? 2 : 1;
         } else if (!ends) {
-          a.meta[2 * blockIdx.x].y = 1, a.meta[2 * blockIdx.x].z = w.h, a.meta[2 * blockIdx.x].w = it.rows;
-          a.meta[2 * blockIdx.x + 1] = make_int4(it.t0, it.row0, 0, 0);
+          me->y = 1, me->z = w.h, me->w = it.rows;
+          me[1] = make_int4(it.t0, it.row0, 0, 0);
         }
       }
       more = walk_next<KT>(a, w, R, slots);
@@ -778,26 +908,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
-  if (*abort_flag) {  // a wait gave up: copies in flight land before the block's memory goes
-    if (warp == kWarpTma) {
+  sync_all();
+  if (*abort_flag) {  // a wait gave up: copies in flight land before the memory they go to does
+    if (warp == kWarpTma && rank == 0) {
       for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
         mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, kSpin);
       for (int t = 0; t < NQ; ++t)
         if (q_issued[t] > 0) mbar_wait(&ctl.qfull[t], (q_issued[t] - 1) & 1, kSpin);
     }
-    __syncthreads();
+    if (PAIR && warp == kWarpTma)
+      for (int i = 0; i < kSlots; ++i)
+        if (landed >> (16 + i) & 1) mbar_wait(&ctl.land[i], landed >> i & 1, kSpin);
   }
-  if (warp == kWarpMma) tmem_dealloc(tm, 512);
+  if (PAIR || *abort_flag) sync_all();
+  if (warp == kWarpMma) free_tmem(tm);
 }
 
 // Items that lie in several blocks' shares: block b's last piece begins one, b + 1's first
 // continues it, until a first piece ends it.  A block takes 32 rows, a lane a row.  The pieces'
 // maxima and sums are loaded at once, the warps taking turns; then a warp sums an eighth of the
 // columns over the pieces, and the rows go out through shared memory, whole rows at a time.
-template <int D, int NQ>
+template <int D, int NQ, bool PAIR>
 __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
-  constexpr int R = Cfg<D, NQ>::R, kV = D / 32;  // fours of columns a warp
+  constexpr int R = Cfg<D, NQ, PAIR>::R, kV = D / 32;  // fours of columns a warp
   __shared__ uint2 rows[32][D / 4 + 1];
   __shared__ float weight[kSms][32], part[2][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -926,40 +1059,55 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int box_rows(const gdn_cache_shape &s) { return std::gcd(s.page_size, s.D == 256 ? 64 : 128); }
-
-template <int D, int NQ>
+template <int D, int NQ, bool PAIR>
 gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {
-  using C = Cfg<D, NQ>;
+  using C = Cfg<D, NQ, PAIR>;
+  a.box = std::gcd(s.page_size, C::kRowsK);
   CUtensorMap mq, mk, mv;
   if (!make_q_map(&mq, a.q, s, a.G, a.RT) || !make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box))
     return GDN_ERR_CUDA;
+  constexpr int units = kSms / C::kPair;
   char *w = (char *)a.status;
   a.meta = (int4 *)(w + 256);
   a.part_ml = (float *)(w + 256 + sizeof(int4) * 512);
-  a.part = a.part_ml + (size_t)kSms * 2 * C::R * 2;
+  a.part = a.part_ml + (size_t)units * 2 * C::R * 2;
   constexpr int smem = kData + 1024;
-  if (cudaFuncSetAttribute(paged_attn_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  const auto kernel = paged_attn_kernel<D, NQ, PAIR>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
-  paged_attn_kernel<D, NQ><<<kSms, C::kThreads, smem, st>>>(mq, mk, mv, a);
-  // the join starts up under the last blocks of the attention and waits for its end
-  cudaLaunchAttribute pdl;
-  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kSms, C::R / 32);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(kSms);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &pdl;
+  if (PAIR) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, (const TcArgs)a) != cudaSuccess)
+    return (void)cudaGetLastError(), GDN_ERR_CUDA;
+  // the join starts up under the last blocks of the attention and waits for its end
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(units, C::R / 32);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NQ>, (const TcArgs)a, kSms) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NQ, PAIR>, (const TcArgs)a, units) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   return launch_status();
 }
 
-// Two row tiles a block where the rows fill them (they share K and V), else one.
-bool two_tiles(const gdn_cache_shape &s, int32_t max_new) {
-  return s.D <= 128 && (int64_t)max_new * (s.Hq / s.Hkv) > 128;
+// Rows of the longest chunk's kv head, and the row tiles that share K and V: one, two in a block, or (D 128 and 256)
+// twice as many in a pair of blocks.
+int64_t chunk_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_new * (s.Hq / s.Hkv); }
+bool two_tiles(const gdn_cache_shape &s, int32_t max_new) { return s.D <= 128 && chunk_rows(s, max_new) > 128; }
+bool pairs(const gdn_cache_shape &s, int32_t max_new) {
+  return (s.D == 128 && chunk_rows(s, max_new) > 256) || (s.D == 256 && chunk_rows(s, max_new) > 128);
 }
 
 bool tc_shape(const gdn_cache_shape &s) {
@@ -994,13 +1142,15 @@ gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int3
   a.table = table, a.table_stride = s.table_stride, a.q_stride = s.q_stride;
   a.G = s.Hq / s.Hkv, a.Hkv = s.Hkv;
   a.RT = 128 / a.G * a.G;
-  a.page_size = s.page_size, a.box = box_rows(s), a.max_pages = s.max_pages, a.n_pages = s.n_pages;
+  a.page_size = s.page_size, a.max_pages = s.max_pages, a.n_pages = s.n_pages;
   a.window = window, a.c = scale_log2;
   a.status = (int32_t *)workspace;
   a.no_wait = flags & GDN_FLAG_TEST_NO_WAIT ? 1 : 0;
-  if (s.D == 256) return launch<256, 1>(k, v, s, a, st);
-  if (two_tiles(s, max_new)) return s.D == 128 ? launch<128, 2>(k, v, s, a, st) : launch<64, 2>(k, v, s, a, st);
-  return s.D == 128 ? launch<128, 1>(k, v, s, a, st) : launch<64, 1>(k, v, s, a, st);
+  const bool pair = pairs(s, max_new);
+  if (s.D == 256) return pair ? launch<256, 1, true>(k, v, s, a, st) : launch<256, 1, false>(k, v, s, a, st);
+  if (pair) return launch<128, 2, true>(k, v, s, a, st);
+  if (two_tiles(s, max_new)) return s.D == 128 ? launch<128, 2, false>(k, v, s, a, st) : launch<64, 2, false>(k, v, s, a, st);
+  return s.D == 128 ? launch<128, 1, false>(k, v, s, a, st) : launch<64, 1, false>(k, v, s, a, st);
 }
 
 }  // namespace gdn
