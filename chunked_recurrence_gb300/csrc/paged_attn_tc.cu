@@ -44,8 +44,6 @@ constexpr uint32_t kSpin = 1u << 22; // polls of a wait before it gives up
 constexpr int kData = 224 * 1024;    // Q and the ring
 constexpr float kLag = 8.f;          // m may lag by this many powers of two
 
-constexpr int kOver = 2;              // units an item costs beyond its tiles
-
 template <int D, int NQ, bool PAIR>
 struct Cfg {
   static constexpr int kPair = PAIR ? 2 : 1;            // blocks (of one cluster) that share an item
@@ -64,6 +62,8 @@ struct Cfg {
   // registers can be split between the warpgroups
   static constexpr int kThreads = NQ == 2 ? 384 : 192;
   static constexpr uint32_t kO = 256;                   // first TMEM column of O
+  // units (tiles) an item costs beyond its tiles: its first S, the mask of its last tile, its output
+  static constexpr int kOver = NQ == 1 && !PAIR ? 2 : 4;
 };
 
 struct TcArgs {
@@ -73,7 +73,8 @@ struct TcArgs {
   float *lse;
   const int32_t *table;
   int64_t table_stride, q_stride;
-  int32_t G, RT, Hkv, page_size, box, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole tokens
+  int32_t G, RT, Hkv, page_size, page_mask, box, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole
+                                                                // tokens; page_mask: page_size - 1, or -1 where no power of two
   float c;  // scale log2 e
   float *part, *part_ml;
   int4 *meta;  // [blocks][2]: how the share's first piece goes on (1: beyond it, 2: to its item's end), whether its last
@@ -239,14 +240,15 @@ struct Walk {
   int64_t left;
 };
 // cuts the next piece at unit u of the item; false where it holds nothing to do
+template <class C>
 __device__ __forceinline__ bool walk_cut(Walk &w) {
   const int end = (int)min((int64_t)w.units, w.u + w.left);
   w.left -= end - w.u;
-  w.j = unit_tile(w.u, kOver);
-  w.n = unit_tile(end, kOver) - w.j;
+  w.j = unit_tile(w.u, C::kOver);
+  w.n = unit_tile(end, C::kOver) - w.j;
   return w.it.n_tiles > 0 ? w.n > 0 : w.u == 0;
 }
-template <int KT>
+template <class C>
 __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int slots) {
   while (w.left > 0) {
     w.u = 0;
@@ -256,20 +258,20 @@ __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int s
         if (++w.slot >= slots) return false;
         int s = w.it.s;
         while (s + 1 < a.seqs.n_seqs && slot_base(a.seqs, s + 1, a.G, R) <= w.slot) ++s;
-        w.it = item_of(a.seqs, s, w.slot, a.G, R, KT, a.window);
-        w.units = item_units(w.it, kOver);
+        w.it = item_of(a.seqs, s, w.slot, a.G, R, C::KT, a.window);
+        w.units = item_units(w.it, C::kOver);
       } while (w.units == 0);
     }
-    if (walk_cut(w)) return true;
+    if (walk_cut<C>(w)) return true;
   }
   return false;
 }
-template <int KT>
+template <class C>
 __device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, const Ctl &c, int64_t left) {
   w.slot = c.start_slot, w.h = c.start_h, w.u = c.start_u, w.left = left;
   w.it = c.start;
-  w.units = item_units(w.it, kOver);
-  return walk_cut(w) || walk_next<KT>(a, w, R, slots);
+  w.units = item_units(w.it, C::kOver);
+  return walk_cut<C>(w) || walk_next<C>(a, w, R, slots);
 }
 
 template <int N>
@@ -409,36 +411,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     if (a.seqs.cu) sq.cu = cu_s;
     __syncthreads();
   }
-  int64_t mine = 0;
-  int keep = 0;  // units of this thread's first slot
-  for (int s = tid; s < slots; s += C::kThreads) {
-    const Item it = item_at(sq, s, a.G, R, KT, a.window);
-    if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
-    const int units = item_units(it, kOver);
-    if (s == tid) keep = units;
-    mine += (int64_t)units * a.Hkv;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) ctl.sum[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += ctl.sum[i];
-  const int shares = (int)min((int64_t)units, total);  // of at least a unit, to the first blocks
-  const int64_t begin = share_begin(total, min(unit, shares), max(shares, 1));
-  const int64_t end = share_begin(total, min(unit + 1, shares), max(shares, 1));
-  if (begin >= end) {  // both blocks of a pair
-    sync_all();
-    if (warp == kWarpMma) free_tmem(ctl.tmem);
-    return;
-  }
-  int64_t before = 0;
-  for (int base = 0; base < slots; base += C::kThreads) {
+  // Slots in rounds of a thread each: inclusive sums of their units, the rounds before them added.  One round (the usual case)
+  // gives the total and the start at once; with more, a first pass finds the total.
+  int64_t x = 0, cost = 0, before = 0, total = 0;
+  auto round = [&](int base) {  // this thread's slot: units, and units up to it in the round; returns the round's
     const int s = base + tid;
-    const int units = base == 0 ? keep : s < slots ? item_units(item_at(sq, s, a.G, R, KT, a.window), kOver) : 0;
-    const int64_t cost = (int64_t)units * a.Hkv;
-    int64_t x = cost;
+    cost = 0;
+    if (s < slots) {
+      const Item it = item_at(sq, s, a.G, R, KT, a.window);
+      if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
+      cost = (int64_t)item_units(it, C::kOver) * a.Hkv;
+    }
+    x = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
@@ -447,18 +431,33 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     __syncthreads();
     if (lane == 31) ctl.sum[warp] = x;
     __syncthreads();
-    int64_t all = 0, upto = 0;
+    int64_t all = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) upto += ctl.sum[i];
+      if (i < warp) x += ctl.sum[i];
       all += ctl.sum[i];
     }
-    const int64_t from = before + upto + x - cost;  // units before this slot
+    return all;
+  };
+  for (int base = 0; base < slots; base += C::kThreads) total += round(base);
+  const int shares = (int)min((int64_t)units, total);  // of at least a unit, to the first blocks
+  const int64_t begin = share_begin(total, min(unit, shares), max(shares, 1));
+  const int64_t end = share_begin(total, min(unit + 1, shares), max(shares, 1));
+  if (begin >= end) {  // both blocks of a pair
+    sync_all();
+    if (warp == kWarpMma) free_tmem(ctl.tmem);
+    return;
+  }
+  for (int base = 0; base < slots; base += C::kThreads) {
+    const int64_t all = slots <= C::kThreads ? total : round(base);
+    const int64_t from = before + x - cost;  // units before this slot
     if (cost > 0 && begin >= from && begin < from + cost) {
+      const int s = base + tid;
       ctl.start_slot = s;
       ctl.start = item_at(sq, s, a.G, R, KT, a.window);
-      ctl.start_h = (int)((begin - from) / units);
-      ctl.start_u = (int)((begin - from) % units);
+      const int its = item_units(ctl.start, C::kOver);
+      ctl.start_h = (int)((begin - from) / its);
+      ctl.start_u = (int)((begin - from) % its);
     }
     before += all;
     if (before > begin) break;
@@ -483,23 +482,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   if (warp == kWarpTma) {
     // ================================================= Q tiles; K and V granules, page by page
     if (NQ == 2) set_regs_down<104>();
-    more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
+    more = walk_begin<C>(a, w, R, slots, ctl, end - begin);
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
-    // Pages ahead of their use: lane l holds the page and slot of box 32 win + l, and of box 32 (win + 1) + l, or -1
-    // where the box holds no position that a row sees.  V comes last, K at most a tile before it, so two windows do;
+    // Pages ahead of their use: lane l holds the page of box 32 win + l, and of box 32 (win + 1) + l, where the box holds
+    // a position that a row sees.  V comes last, K at most a tile before it, so two windows do;
     // the next one's entries are asked for when V enters this one.  (An entry asked for when it is needed costs
     // its L2 latency, 570 cycles a granule.)
-    int win = 0, page[2], at[2];
+    int win = 0, page[2];
+    bool used[2];
     auto look_up = [&](int window, int i, const int32_t *row) {
       const int64_t pos = (int64_t)(32 * window + lane) * a.box;
-      page[i] = -1, at[i] = 0;
-      if (pos < w.it.hi && pos + a.box > w.it.lo) {
-        page[i] = page_of(row, (int)pos, a.page_size, a.max_pages, a.n_pages);
-        at[i] = (int)pos % a.page_size;
-        if (page[i] < 0) set_status(a.status, GDN_ERR_BOUNDS);
-      }
+      used[i] = pos < w.it.hi && pos + a.box > w.it.lo;  // then pos lies within the table's row
+      page[i] = used[i] ? row[(int)pos / a.page_size] : -1;
     };
     // a granule of K or V: its boxes (rows x 64-column panels) over the lanes, all in one instruction
     auto load = [&](auto is_v, uint32_t idx, int pos0, const int32_t *row) {
@@ -511,14 +507,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       const int nb = (V ? KT : C::kRowsK) / a.box, b0 = (pos0 + (V ? 0 : rank * C::kRowsK)) / a.box;
       if (V && b0 / 32 > win) {
         ++win;
-        page[0] = page[1], at[0] = at[1];
+        page[0] = page[1], used[0] = used[1];
         look_up(win + 1, 1, row);
       }
       const int i = lane / kPanels, p = lane % kPanels, from = (b0 + i) & 31;
-      const int pg0 = __shfl_sync(0xffffffffu, page[0], from), pg1 = __shfl_sync(0xffffffffu, page[1], from);
-      const int at0 = __shfl_sync(0xffffffffu, at[0], from), at1 = __shfl_sync(0xffffffffu, at[1], from);
       const bool ahead = b0 / 32 > win;
-      const int pg = i >= nb ? -1 : ahead ? pg1 : pg0, sl = ahead ? at1 : at0;
+      int pg = ahead ? page[1] : page[0];
+      if (ahead ? used[1] : used[0]) {
+        if (pg < 0 || pg >= a.n_pages) set_status(a.status, GDN_ERR_BOUNDS), pg = -1;
+      }
+      pg = __shfl_sync(0xffffffffu, pg, from);
+      if (i >= nb) pg = -1;
+      const int at = (b0 + i) * a.box, sl = a.page_mask >= 0 ? at & a.page_mask : at % a.page_size;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
       if (!warp_wait(&ctl.empty[slot], ph ^ 1, abort_flag)) {
         ok = false;
@@ -585,14 +585,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         }
         base += 2 * w.n;
       }
-      more = walk_next<KT>(a, w, R, slots);
+      more = walk_next<C>(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
   } else if (warp == kWarpMma) {
     // ================================================= MMAs
     if (NQ == 2) set_regs_down<104>();
     if (lane == 0 && rank == 0) {
-      more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
+      more = walk_begin<C>(a, w, R, slots, ctl, end - begin);
       const uint32_t id_s = idesc_bf16(128 * C::kPair, KT, false, false);
       const uint32_t id_o = idesc_bf16(128 * C::kPair, D, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sm), 16, 1024, 2);
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           }
           base += 2 * n;
         }
-        more = walk_next<KT>(a, w, R, slots);
+        more = walk_next<C>(a, w, R, slots);
       }
       if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
         if (!ok) fail();
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   } else {
     // ================================================= softmax: a thread owns a query row
     if (NQ == 2) set_regs_up<200>();
-    more = walk_begin<KT>(a, w, R, slots, ctl, end - begin);
+    more = walk_begin<C>(a, w, R, slots, ctl, end - begin);
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lq = (uint32_t)(quarter * 32) << 16;
     auto p_ready = [&](int slot, int half) {
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.o + out * D + d) = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[out] = -INFINITY;
         }
-        more = walk_next<KT>(a, w, R, slots);
+        more = walk_next<C>(a, w, R, slots);
         continue;
       }
       const int n = w.n, nt = NQ == 2 && it.rows > a.RT * C::kPair ? 2 : 1;
@@ -734,7 +734,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           const int pos = first + j * KT;
           if (t == 0 && (pos < it.lo || pos + KT > it.hi)) {
             // positions that no row sees: their V rows become zeros (P is 0 there, and 0 * NaN is not)
-            const int x = pos + r;
             const uint32_t idx = idx_v<NQ>(base, j, n);
             uint64_t *there = PAIR ? &ctl.land[idx % kSlots] : &ctl.full[idx % kSlots];
             if (!warp_wait(there, PAIR ? landed >> (idx % kSlots) & 1 : (idx / kSlots) & 1, abort_flag)) {
@@ -742,12 +741,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
               break;
             }
             landed ^= 1u << (idx % kSlots);
-            if (r < KT && (x < it.lo || x >= it.hi)) {
-              uint8_t *vr = ring + (idx % kSlots) * C::kGran + r * 128;
-              for (int pn = 0; pn < C::kPanelsV; ++pn)
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch)
-                  *reinterpret_cast<uint4 *>(vr + pn * C::kPanelV + ch * 16) = make_uint4(0, 0, 0, 0);
+            const int z0 = max(it.lo - pos, 0), z1 = min(it.hi - pos, KT);  // rows [0, z0) and [z1, KT)
+            uint8_t *v = ring + (idx % kSlots) * C::kGran;
+            for (int pn = 0; pn < C::kPanelsV; ++pn, v += C::kPanelV) {
+              for (int x = r * 16; x < z0 * 128; x += 128 * 16) *reinterpret_cast<uint4 *>(v + x) = make_uint4(0, 0, 0, 0);
+              for (int x = z1 * 128 + r * 16; x < KT * 128; x += 128 * 16)
+                *reinterpret_cast<uint4 *>(v + x) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -759,9 +758,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
             for (int x = 0; x < KT; x += 32) tmem_ld32u(ts + x, reinterpret_cast<uint32_t *>(s) + x);
             tmem_wait_ld();
             settled(s, 0, KT);
-            if (valid && (pos + KT > hi || pos < lo)) {  // rows past the item's are nobody's: no care for them
+            if (valid && pos + KT > hi) {  // rows past the item's are nobody's: no care for them
+              const int to = hi - pos;
 #pragma unroll
-              for (int x = 0; x < KT; ++x) s[x] = pos + x < hi && pos + x >= lo ? s[x] : -INFINITY;
+              for (int x = 0; x < KT; ++x) s[x] = x < to ? s[x] : -INFINITY;
+            }
+            if (valid && pos < lo) {
+              const int from = lo - pos;
+#pragma unroll
+              for (int x = 0; x < KT; ++x) s[x] = x >= from ? s[x] : -INFINITY;
             }
             const float mx = max_of(s, 0, KT, -INFINITY);
             if (j == 0) {
@@ -902,7 +907,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           me[1] = make_int4(it.t0, it.row0, 0, 0);
         }
       }
-      more = walk_next<KT>(a, w, R, slots);
+      more = walk_next<C>(a, w, R, slots);
     }
     if (!ok && lane == 0) fail();
   }
@@ -1142,7 +1147,8 @@ gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int3
   a.table = table, a.table_stride = s.table_stride, a.q_stride = s.q_stride;
   a.G = s.Hq / s.Hkv, a.Hkv = s.Hkv;
   a.RT = 128 / a.G * a.G;
-  a.page_size = s.page_size, a.max_pages = s.max_pages, a.n_pages = s.n_pages;
+  a.page_size = s.page_size, a.page_mask = s.page_size & (s.page_size - 1) ? -1 : s.page_size - 1;
+  a.max_pages = s.max_pages, a.n_pages = s.n_pages;
   a.window = window, a.c = scale_log2;
   a.status = (int32_t *)workspace;
   a.no_wait = flags & GDN_FLAG_TEST_NO_WAIT ? 1 : 0;
