@@ -1,5 +1,6 @@
 // paged_attn.cu -- attention of new tokens over a paged cache (gdn_paged_attn): argument
-// checks, dispatch and the CUDA-core kernel.  The tensor-core kernel is in paged_attn_tc.cu.
+// checks, dispatch and the CUDA-core kernel (GDN_FLAG_SIMT).  The kernels that run by default are in
+// paged_attn_tc.cu (bf16 on tcgen05) and paged_attn_f32.cu (fp32, and what the first does not take).
 //
 //     o[t, h] = sum_j softmax_j(scale <q[t, h], k_j>) v_j   over the positions that t sees
 //
@@ -58,18 +59,6 @@ PagedSeqs paged_seqs(const gdn_cache_shape &s, const int32_t *seq_lens, const in
 namespace {
 
 constexpr int kWarps = 4, kRows = 4;
-
-struct SimtArgs {
-  PagedSeqs seqs;
-  const void *q, *k, *v;
-  void *o;
-  float *lse, *part;  // part: [splits][n_tok * Hq][D + 2], or null with one split
-  const int32_t *table;
-  int64_t table_stride, page_stride, slot_stride, head_stride, q_stride;
-  int32_t Hq, Hkv, D, page_size, max_pages, n_pages, window, splits;
-  float scale_log2;
-  int32_t *status;
-};
 
 template <typename T, int NE>
 __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const SimtArgs a) {
@@ -194,18 +183,13 @@ int simt_splits(const gdn_cache_shape &s) {
   const int64_t want = (152 * 8 + blocks - 1) / std::max<int64_t>(blocks, 1);
   return (int)std::max<int64_t>(1, std::min<int64_t>(16, want));
 }
-size_t simt_workspace(const gdn_cache_shape &s) {
-  const int n = simt_splits(s);
-  return 256 + (n > 1 ? (size_t)n * s.n_tok * s.Hq * (s.D + 2) * sizeof(float) : 0);
+size_t parts_bytes(const gdn_cache_shape &s, int splits) {
+  return 256 + (splits > 1 ? (size_t)splits * s.n_tok * s.Hq * (s.D + 2) * sizeof(float) : 0);
 }
 
 template <typename T, int NE>
 gdn_status launch_simt(const SimtArgs &a, int64_t slots, cudaStream_t st) {
   paged_attn_simt_kernel<T, NE><<<dim3((unsigned)slots, a.Hkv, a.splits), kWarps * 32, 0, st>>>(a);
-  if (a.part) {
-    const int64_t rows = (int64_t)a.seqs.n_tok * a.Hq;
-    simt_join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a.part, a.splits, rows, a.D, (T *)a.o, a.lse);
-  }
   return launch_status();
 }
 
@@ -221,6 +205,13 @@ gdn_status dispatch_simt(const SimtArgs &a, int64_t slots, cudaStream_t st) {
   }
 }
 
+template <typename T>
+gdn_status launch_join(const SimtArgs &a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.seqs.n_tok * a.Hq;
+  simt_join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a.part, a.splits, rows, a.D, (T *)a.o, a.lse);
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -231,7 +222,8 @@ extern "C" size_t gdn_paged_attn_workspace_bytes(const gdn_cache_shape *shape, i
   // any non-null offsets: the number of tokens is checked by the call
   static const int32_t some = 0;
   if (max_new < 0 || normalise_cache_shape(shape, &some, &s) != GDN_OK) return 0;
-  return std::max(simt_workspace(s), paged_attn_tc_workspace(s, max_new));
+  return std::max({parts_bytes(s, simt_splits(s)), parts_bytes(s, paged_attn_f32_splits(s, max_new)),
+                   paged_attn_tc_workspace(s, max_new)});
 }
 
 extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache,
@@ -254,11 +246,18 @@ extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const v
   if (!(flags & GDN_FLAG_SIMT) && paged_attn_tc_supported(q, k_cache, v_cache, o, s, scale))
     return paged_attn_tc(q, k_cache, v_cache, page_table, seqs, s, max_new, scale_log2, window, flags, o, lse,
                          workspace, st);
+  const bool simt = flags & GDN_FLAG_SIMT;
   SimtArgs a{seqs, q, k_cache, v_cache, o, lse, nullptr, page_table, s.table_stride, s.page_stride, s.slot_stride,
-             s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages, s.n_pages, window, simt_splits(s),
-             scale_log2, (int32_t *)workspace};
+             s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages, s.n_pages, window,
+             simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new), scale_log2, (int32_t *)workspace};
   if (a.splits > 1) a.part = (float *)((char *)workspace + 256);
-  const int64_t slots = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, kRows);
-  if (s.dtype == GDN_BF16) return dispatch_simt<__nv_bfloat16>(a, slots, st);
-  return dispatch_simt<float>(a, slots, st);
+  gdn_status r;
+  if (simt) {
+    const int64_t slots = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, kRows);
+    r = s.dtype == GDN_BF16 ? dispatch_simt<__nv_bfloat16>(a, slots, st) : dispatch_simt<float>(a, slots, st);
+  } else {
+    r = paged_attn_f32(a, s, max_new, st);
+  }
+  if (r != GDN_OK || !a.part) return r;
+  return s.dtype == GDN_BF16 ? launch_join<__nv_bfloat16>(a, st) : launch_join<float>(a, st);
 }

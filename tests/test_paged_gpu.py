@@ -241,7 +241,7 @@ def cu_of(new):
 
 
 def run_attn(crg, seed, dtype, new, lens, hq, hkv, d, page, window=0, order="token", gap=0, simt=False, max_new=None,
-             one=False, scale=None):
+             one=False, scale=None, tensor=None):
     cache = Cache(seed, dtype, lens, hkv, d, page, order, gap)
     q = randn(gen(seed + 1), (sum(new), hq, d), dtype)
     ws = crg.Workspace(1 << 28, DEV)
@@ -249,7 +249,7 @@ def run_attn(crg, seed, dtype, new, lens, hq, hkv, d, page, window=0, order="tok
                                 max_new=max_new, window=window, want_lse=True, simt=simt, workspace=ws, scale=scale)
     torch.cuda.synchronize()
     assert ws.status() == 0
-    assert_attn(o, lse, q, cache, new, window, scale, tensor=dtype == "bf16" and not simt)
+    assert_attn(o, lse, q, cache, new, window, scale, tensor=dtype == "bf16" and not simt if tensor is None else tensor)
     return cache, q, o, lse
 
 
@@ -269,8 +269,25 @@ def test_attn_simt(crg, case):
     run_attn(crg, 11, *case, simt=True)
 
 
-def test_attn_f32_takes_the_simt_kernel(crg):
-    run_attn(crg, 12, "f32", [1, 4], [900, 65], 8, 2, 128, 16)
+F32 = [  # dtype, new, lens, hq, hkv, d, page, window: what the tcgen05 kernel does not take
+    ("f32", [1, 4], [900, 65], 8, 2, 128, 16, 0),
+    ("f32", [1, 1, 1], [1, 17, 3000], 4, 2, 64, 16, 0),
+    ("f32", [5, 0, 37], [5, 0, 90], 6, 2, 64, 16, 0),
+    ("f32", [130, 1], [200, 1], 3, 1, 128, 1, 50),
+    ("f32", [90], [400], 4, 2, 256, 48, 0),
+    ("f32", [1, 1], [400, 70], 5, 1, 256, 48, 33),
+    ("f32", [20, 2], [7, 1], 4, 2, 96, 3, 0),      # rows that see nothing
+    ("f32", [33], [70], 2, 1, 7, 5, 0),
+    ("bf16", [9, 3], [40, 3], 4, 4, 96, 5, 0),
+    ("bf16", [70], [133], 8, 1, 200, 12, 1),
+    ("bf16", [1, 1], [1000, 64], 3, 1, 40, 16, 0),
+    ("bf16", [3], [77], 130, 1, 64, 16, 0),        # more heads a group than a tile has rows
+]
+
+
+@pytest.mark.parametrize("case", F32, ids=str)
+def test_attn_f32(crg, case):
+    run_attn(crg, 12, *case, tensor=False)
 
 
 TC = [  # new, lens, hq, hkv, d, page, window
@@ -348,7 +365,7 @@ def test_attn_strided_q_and_given_outputs(crg):
     assert_attn(o, None, q, cache, [20, 4])
 
 
-def test_attn_unaligned_takes_the_simt_kernel(crg):
+def test_attn_unaligned(crg):
     cache = Cache(22, "bf16", [90], 2, 64, 16)
     buf = torch.zeros(3 * 4 * 64 + 1, dtype=torch.bfloat16, device=DEV)
     q = buf[1:].view(3, 4, 64)
