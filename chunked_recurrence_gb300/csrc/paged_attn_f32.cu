@@ -31,7 +31,8 @@ template <typename T, int DP, bool FEW>
 struct Cfg {
   static constexpr bool kExact = sizeof(T) == 2;   // values exact in TF32
   static constexpr int R = FEW ? 16 : 64;
-  static constexpr int BN = DP == 256 ? 32 : 64;   // positions a tile
+  static constexpr int BN = DP == 256 || FEW ? 32 : 64;  // positions a tile (FEW: two blocks an SM; 24 single tokens over 1000,
+                                                          // D 128: 92 us, 128 us with 64)
   static constexpr int kMine = FEW ? BN / 4 : BN;  // of them a warp's
   static constexpr int kPitch = DP + 4;            // floats a row: the fragments' loads meet no bank conflict
   static constexpr int kTile = BN * kPitch;
@@ -294,8 +295,9 @@ bool few_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_n
 // Parts that a block's positions are cut into: enough blocks for the GPU, no part below two tiles of the longest
 // sequence that the table can hold, at most 64.
 int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new) {
-  const int64_t blocks = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, few_rows(s, max_new) ? 16 : 64) * s.Hkv;
-  const int64_t want = (152 * 3 + blocks - 1) / std::max<int64_t>(blocks, 1);
+  const bool few = few_rows(s, max_new);
+  const int64_t blocks = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, few ? 16 : 64) * s.Hkv;
+  const int64_t want = (152 * (few ? 3 : 2) + blocks - 1) / std::max<int64_t>(blocks, 1);
   const int64_t most = ((int64_t)s.max_pages * s.page_size + 127) / 128;
   return (int)std::max<int64_t>(1, std::min<int64_t>({64, want, most}));
 }
