@@ -58,9 +58,9 @@ struct Cfg {
   static constexpr int kPanelsK = D / 64, kPanelsV = D / 64 / kPair;
   static constexpr int kQ = 128 * NQ * D * 2;
   static constexpr int kSlots = (kData - kQ) / kGran < 16 ? (kData - kQ) / kGran : 16;
-  // softmax warpgroups, then the TMA and MMA warps; with two tiles a whole warpgroup for those, so that the
-  // registers can be split between the warpgroups
-  static constexpr int kThreads = NQ == 2 ? 384 : 192;
+  // softmax warpgroups, then the warps of K's copies (and Q's), the MMAs and V's copies; with two tiles a whole
+  // warpgroup for those, so that the registers can be split between the warpgroups
+  static constexpr int kThreads = NQ == 2 ? 384 : 224;
   static constexpr uint32_t kO = 256;                   // first TMEM column of O
   // units (tiles) an item costs beyond its tiles: its first S, the mask of its last tile, its output
   static constexpr int kOver = NQ == 1 && !PAIR ? 2 : 4;
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = sm + C::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarps = C::kThreads / 32;
+  constexpr int kWarpTma = 4 * NQ, kWarpMma = 4 * NQ + 1, kWarpTmaV = 4 * NQ + 2, kWarps = C::kThreads / 32;
   // a share belongs to a block, or to a pair of them: then rank 1 takes every second row tile and its halves of
   // K and V, and rank 0 issues the MMAs of both, waiting on its own barriers, where both blocks arrive
   const int rank = PAIR ? (int)cluster_ctarank() : 0, unit = blockIdx.x / C::kPair, units = gridDim.x / C::kPair;
@@ -475,21 +475,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     set_status(a.status, GDN_ERR_TIMEOUT);
   };
   uint32_t landed = 0;  // PAIR: phase bits of the land barriers, as this warp has used them
-  uint32_t issued = 0, q_issued[2] = {0, 0};  // granules and Q tiles (the TMA warp's count)
+  uint32_t issued = 0, phase = 0;  // ring slots that this warp's copies went to, and their phases at the last of them
+  uint32_t q_issued[2] = {0, 0};
   Walk w;
   bool more = false;
 
-  if (warp == kWarpTma) {
-    // ================================================= Q tiles; K and V granules, page by page
+  if (warp == kWarpTma || warp == kWarpTmaV) {
+    // ================================================= Q tiles and K granules, V granules: page by page.  Two warps: with
+    // pages of 16 a granule is 16 copies, and one warp issuing K and V falls behind HBM
+    const bool for_v = warp == kWarpTmaV;
     if (NQ == 2) set_regs_down<104>();
     more = walk_begin<C>(a, w, R, slots, ctl, end - begin);
     uint32_t base = 0;
     bool ok = true;
     const uint32_t box_bytes = (uint32_t)a.box * 128u;
     // Pages ahead of their use: lane l holds the page of box 32 win + l, and of box 32 (win + 1) + l, where the box holds
-    // a position that a row sees.  V comes last, K at most a tile before it, so two windows do;
-    // the next one's entries are asked for when V enters this one.  (An entry asked for when it is needed costs
-    // its L2 latency, 570 cycles a granule.)
+    // a position that a row sees.  The next window's entries are asked for when this one is entered (an entry asked for
+    // when it is needed costs its L2 latency, 570 cycles a granule).
     int win = 0, page[2];
     bool used[2];
     auto look_up = [&](int window, int i, const int32_t *row) {
@@ -505,17 +507,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
       // nb divides 32: a granule lies in one window
       const int nb = (V ? KT : C::kRowsK) / a.box, b0 = (pos0 + (V ? 0 : rank * C::kRowsK)) / a.box;
-      if (V && b0 / 32 > win) {
+      if (b0 / 32 > win) {
         ++win;
         page[0] = page[1], used[0] = used[1];
         look_up(win + 1, 1, row);
       }
       const int i = lane / kPanels, p = lane % kPanels, from = (b0 + i) & 31;
-      const bool ahead = b0 / 32 > win;
-      int pg = ahead ? page[1] : page[0];
-      if (ahead ? used[1] : used[0]) {
-        if (pg < 0 || pg >= a.n_pages) set_status(a.status, GDN_ERR_BOUNDS), pg = -1;
-      }
+      int pg = page[0];
+      if (used[0] && (pg < 0 || pg >= a.n_pages)) set_status(a.status, GDN_ERR_BOUNDS), pg = -1;
       pg = __shfl_sync(0xffffffffu, pg, from);
       if (i >= nb) pg = -1;
       const int at = (b0 + i) * a.box, sl = a.page_mask >= 0 ? at & a.page_mask : at % a.page_size;
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         __syncwarp();
         if (pg >= 0) tma_load_4d(to, map, &ctl.full[slot], 64 * p, sl, w.h, pg);
       }
-      issued = idx + 1;
+      issued |= 1u << slot, phase = (phase & ~(1u << slot)) | ph << slot;
     };
     while (more && ok) {
       if (w.it.n_tiles > 0) {
@@ -554,12 +553,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         win = first / a.box / 32;
         look_up(win, 0, row);
         look_up(win + 1, 1, row);
-        auto load_k = [&](int j) { load(std::false_type{}, idx_k<NQ>(base, j), first + j * KT, row); };
-        auto load_v = [&](int j) { load(std::true_type{}, idx_v<NQ>(base, j, w.n), first + j * KT, row); };
         // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
         // sequences that come along are never used
         const int nt = NQ == 2 && w.it.rows > a.RT * C::kPair ? 2 : 1;
-        for (int t = 0; t < nt && ok; ++t) {
+        for (int t = 0; t < nt && ok && !for_v; ++t) {
           if (!warp_wait(&ctl.qfree[t], (q_issued[t] & 1) ^ 1, abort_flag)) {
             ok = false;
             break;
@@ -577,11 +574,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           __syncwarp();
           ++q_issued[t];
         }
-        if (ok) load_k(0);
         for (int j = 0; j < w.n && ok; ++j) {
-          if (NQ == 1 && j + 1 < w.n) load_k(j + 1);
-          if (ok) load_v(j);
-          if (NQ == 2 && j + 1 < w.n && ok) load_k(j + 1);
+          if (for_v) load(std::true_type{}, idx_v<NQ>(base, j, w.n), first + j * KT, row);
+          else load(std::false_type{}, idx_k<NQ>(base, j), first + j * KT, row);
         }
         base += 2 * w.n;
       }
@@ -671,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         mbar_wait(&ctl.drain, 0, kSpin);
       }
     }
-  } else if (warp > kWarpMma) {
+  } else if (warp > kWarpTmaV) {
     if (NQ == 2) set_regs_down<104>();
   } else {
     // ================================================= softmax: a thread owns a query row
@@ -915,15 +910,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   tc_fence_before();
   sync_all();
   if (*abort_flag) {  // a wait gave up: copies in flight land before the memory they go to does
-    if (warp == kWarpTma && rank == 0) {
-      for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
-        mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, kSpin);
-      for (int t = 0; t < NQ; ++t)
+    if (warp == kWarpTma || warp == kWarpTmaV) {
+      for (int i = 0; i < kSlots && rank == 0; ++i)
+        if (issued >> i & 1) mbar_wait(&ctl.full[i], phase >> i & 1, kSpin);
+      for (int t = 0; t < NQ && rank == 0; ++t)
         if (q_issued[t] > 0) mbar_wait(&ctl.qfull[t], (q_issued[t] - 1) & 1, kSpin);
-    }
-    if (PAIR && warp == kWarpTma)
-      for (int i = 0; i < kSlots; ++i)
+      for (int i = 0; i < kSlots && PAIR; ++i)
         if (landed >> (16 + i) & 1) mbar_wait(&ctl.land[i], landed >> i & 1, kSpin);
+    }
   }
   if (PAIR || *abort_flag) sync_all();
   if (warp == kWarpMma) free_tmem(tm);
