@@ -55,7 +55,7 @@ GDN_HD SeqSpan seq_span(const PagedSeqs &q, int32_t s) {
 // floor((c + n) / R) - floor(c / R) + 1 items), so a slot is found from the offsets alone, and
 // item_slots bounds their number from what the host knows.  Slots without an item stay empty.
 GDN_HD int32_t slot_base(const PagedSeqs &q, int32_t s, int32_t G, int32_t R) {
-  return (int32_t)((int64_t)cu_at(q, s) * G / R) + s;
+  return cu_at(q, s) * G / R + s;  // the call checked that n_tok * G fits 32 bits
 }
 GDN_HD int64_t item_slots(int64_t n_tok, int32_t n_seqs, int32_t G, int32_t R) { return n_tok * G / R + n_seqs; }
 

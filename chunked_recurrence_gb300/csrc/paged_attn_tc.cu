@@ -73,7 +73,7 @@ struct TcArgs {
   float *lse;
   const int32_t *table;
   int64_t table_stride, q_stride;
-  int32_t G, RT, Hkv, page_size, page_mask, box, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole
+  int32_t G, RT, Hkv, page_size, page_mask, box, box_log2, max_pages, n_pages, window;  // RT: rows of a 128-row tile in use, whole
                                                                 // tokens; page_mask: page_size - 1, or -1 where no power of two
   float c;  // scale log2 e
   float *part, *part_ml;
@@ -414,11 +414,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   // Slots in rounds of a thread each: inclusive sums of their units, the rounds before them added.  One round (the usual case)
   // gives the total and the start at once; with more, a first pass finds the total.
   int64_t x = 0, cost = 0, before = 0, total = 0;
+  Item it;
   auto round = [&](int base) {  // this thread's slot: units, and units up to it in the round; returns the round's
     const int s = base + tid;
     cost = 0;
     if (s < slots) {
-      const Item it = item_at(sq, s, a.G, R, KT, a.window);
+      it = item_at(sq, s, a.G, R, KT, a.window);
       if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
       cost = (int64_t)item_units(it, C::kOver) * a.Hkv;
     }
@@ -452,12 +453,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     const int64_t all = slots <= C::kThreads ? total : round(base);
     const int64_t from = before + x - cost;  // units before this slot
     if (cost > 0 && begin >= from && begin < from + cost) {
-      const int s = base + tid;
-      ctl.start_slot = s;
-      ctl.start = item_at(sq, s, a.G, R, KT, a.window);
-      const int its = item_units(ctl.start, C::kOver);
-      ctl.start_h = (int)((begin - from) / its);
-      ctl.start_u = (int)((begin - from) % its);
+      const uint32_t its = item_units(it, C::kOver), into = (uint32_t)(begin - from);  // below units * Hkv
+      ctl.start_slot = base + tid;
+      ctl.start = it;
+      ctl.start_h = into / its;
+      ctl.start_u = into % its;
     }
     before += all;
     if (before > begin) break;
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       const CUtensorMap *map = V ? &tm_v : &tm_k;
       const uint32_t slot = idx % kSlots, ph = (idx / kSlots) & 1;
       // nb divides 32: a granule lies in one window
-      const int nb = (V ? KT : C::kRowsK) / a.box, b0 = (pos0 + (V ? 0 : rank * C::kRowsK)) / a.box;
-      if (b0 / 32 > win) {
+      const int nb = (V ? KT : C::kRowsK) >> a.box_log2, b0 = (pos0 + (V ? 0 : rank * C::kRowsK)) >> a.box_log2;
+      if (b0 >> 5 > win) {
         ++win;
         page[0] = page[1], used[0] = used[1];
         look_up(win + 1, 1, row);
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       if (w.it.n_tiles > 0) {
         const int32_t *row = a.table + (int64_t)w.it.s * a.table_stride;
         const int first = (w.it.tile0 + w.j) * KT;
-        win = first / a.box / 32;
+        win = first >> a.box_log2 >> 5;
         look_up(win, 0, row);
         look_up(win + 1, 1, row);
         // the row tiles' queries: whole tokens with the heads of the group, a box each 64 columns; rows of other
@@ -1061,7 +1061,8 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
 template <int D, int NQ, bool PAIR>
 gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {
   using C = Cfg<D, NQ, PAIR>;
-  a.box = std::gcd(s.page_size, C::kRowsK);
+  a.box = std::gcd(s.page_size, C::kRowsK);  // a power of two
+  a.box_log2 = __builtin_ctz(a.box);
   CUtensorMap mq, mk, mv;
   if (!make_q_map(&mq, a.q, s, a.G, a.RT) || !make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box))
     return GDN_ERR_CUDA;
