@@ -61,6 +61,7 @@ struct Cfg {
   // softmax warpgroups, then the warps of K's copies (and Q's), the MMAs and V's copies; with two tiles a whole
   // warpgroup for those, so that the registers can be split between the warpgroups
   static constexpr int kThreads = NQ == 2 ? 384 : 224;
+  static constexpr int kHalves = NQ == 1 ? 2 : 1;       // parts in which P is handed over
   static constexpr uint32_t kO = 256;                   // first TMEM column of O
   // units (tiles) an item costs beyond its tiles: its first S, the mask of its last tile, its output
   static constexpr int kOver = NQ == 1 && !PAIR ? 2 : 4;
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       // S[slot] = Q[t] K(j)^T
       auto issue_s = [&](int t, int slot, int j) {
         const uint32_t idx = idx_k<NQ>(base, j);
-        wait_full(idx);
+        if (t == 0) wait_full(idx);  // the second row tile reads the same K
         if (!ok) return;
         tc_fence_after();
         const uint64_t dk = d_k + (((idx % kSlots) * C::kGran) >> 4);
@@ -616,18 +617,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         commit<PAIR>(&ctl.sfull[slot]);
         if (NQ == 1) commit<PAIR>(&ctl.empty[idx % kSlots]);
       };
-      // O[t] (+)= P[slot] V(j), the first half of the positions as soon as their P is there
+      // O[t] (+)= P[slot] V(j).  With one row tile the first half of the positions goes as soon as their P is there; with two the
+      // other tile's products cover the wait, and each wait costs this thread some 90 cycles
       auto issue_o = [&](int t, int slot, int j) {
         const uint32_t idx = idx_v<NQ>(base, j, w.n);
         const uint64_t dv = d_v + (((idx % kSlots) * C::kGran) >> 4);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < C::kHalves; ++half) {
           wait(&ctl.pready[slot][half], steps[slot] & 1);
-          if (half == 0) wait_full(idx);
+          if (t == 0 && half == 0) wait_full(idx);
           if (!ok) return;
           tc_fence_after();
+          constexpr int kSteps = KT / 16 / C::kHalves;
 #pragma unroll
-          for (int ks = half * (KT / 32); ks < (half + 1) * (KT / 32); ++ks)
+          for (int ks = half * kSteps; ks < (half + 1) * kSteps; ++ks)
             mma_ts<PAIR>(tm + C::kO + t * D, tm + slot * KT + ks * 8, dv + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
         }
         ++steps[slot];
@@ -810,10 +813,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
               }
               if constexpr (KT == 128) tmem_st32u(ts + half * 32, pk);
               else tmem_st16u(ts + half * 16, pk);
+              if (half + 1 < 2 && C::kHalves == 1) continue;
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) p_ready(slot, half);
+              if (lane == 0) p_ready(slot, C::kHalves == 1 ? 0 : half);
             }
             float s0, s1, s2, s3;
             f2_unpack(sum0, s0, s1);
@@ -824,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
             __syncwarp();
             if (lane == 0) {
               p_ready(slot, 0);
-              p_ready(slot, 1);
+              if (C::kHalves == 2) p_ready(slot, 1);
             }
           }
         }
