@@ -1046,7 +1046,7 @@ bool make_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int bo
   cuuint64_t strides[3] = {(cuuint64_t)s.slot_stride * 2, (cuuint64_t)heads * 2, (cuuint64_t)pages * 2};
   cuuint32_t b[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, b, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
