@@ -3,6 +3,10 @@
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
 objects are linked into chunked_recurrence_gb300/_build/libgdn.so.  Nothing is
 installed: the library stays in the tree, next to the Python binding.
+
+csrc/marshal.cpp, a small CPython module that shortens the binding's host time, is
+built beside it against the installed torch where that has its C++ headers; the binding
+works without it.
 """
 from __future__ import annotations
 
@@ -18,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libgdn.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(OUT_DIR, "gdn_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,12 +46,42 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return any(os.path.getmtime(p) > t for p in _deps() + [MARSHAL_SRC])
 
 
 def flags(extra=()):
     return ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                    "-I", CSRC, "--expt-relaxed-constexpr"] + list(extra)
+
+
+def _build_marshal(verbose: bool = False):
+    """The binding's C++ module; without torch's headers or a C++ compiler it is left out."""
+    import sysconfig
+
+    try:
+        import torch
+    except ImportError:
+        return
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(root, "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], MARSHAL_SRC,
+           "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr if r.returncode else ""
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        if verbose:
+            print("gdn_marshal left out:", failed[-2000:], flush=True)
+        return
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -69,7 +105,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(_build_marshal, verbose)
         objs = list(ex.map(compile_one, sources()))
+        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -5,16 +5,43 @@ package's __init__; the functions are reached through the package.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
+from . import build as _build
 from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT, GDN_FLAG_TEST_NO_WAIT,
                GDN_MAX_POOLS, GDN_ROPE_SCALING, GdnCacheShape, GdnPagePools, GdnPageTables, Workspace, _check,
                _dtype_code, _need_cuda, _ptr, _stream, _ws_cache, load)
 
 
+def _load_marshal():
+    """lays and like of the C++ module, or the same in Python where there is none for this torch."""
+    if os.path.exists(_build.MARSHAL):
+        try:
+            spec = importlib.util.spec_from_file_location("gdn_marshal", _build.MARSHAL)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            if module.torch_version == torch.__version__.split("+")[0]:
+                return module.lays, module.like
+        except ImportError:
+            pass
+
+    def lays(*tensors):
+        return tuple(None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors)
+
+    def like(t, dims, f32):
+        return torch.empty(t.shape[:dims], dtype=torch.float32 if f32 else t.dtype, device=t.device)
+
+    return lays, like
+
+
+_lays, _like = _load_marshal()
+
 # What a call's layouts come to (sizes, strides, flags, the workspace's size), worked out and
-# checked once for each combination of shapes, strides and dtypes; addresses are never part of it.
+# checked once for each combination of shapes, strides, dtypes and devices; addresses are never
+# part of it.
 _plans = {}
 
 
@@ -26,11 +53,6 @@ def _plan(key, make):
             _plans.clear()
         _plans[key] = plan
     return plan
-
-
-def _lay(t):
-    """A tensor's part of a plan's key."""
-    return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
 def _addr(t):
@@ -54,12 +76,12 @@ def _handle(t, stream):
     return _stream(t, stream).value or 0
 
 
-def _empty(like, shape, dtype, stream):
+def _empty(t, dims, f32, stream):
     """An output of a call on `stream`: memory of that stream, so that its earlier users are done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(_as_stream(like, stream)):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _like(t, dims, f32)
+    with torch.cuda.stream(_as_stream(t, stream)):
+        return _like(t, dims, f32)
 
 
 def _as_stream(like, stream):
@@ -113,9 +135,9 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     takes gradients of the outputs to those of the inputs.  q_out / k_out may be q / k.
     Returns (q_out, k_out)."""
     x = q if q is not None else k
-    _need_cuda(q, k, positions, freqs, q_out, k_out)
 
     def make():
+        _need_cuda(q, k, positions, freqs, q_out, k_out)
         n_tok, _, D = x.shape
         if positions.dtype != torch.int64 or positions.numel() != n_tok or not positions.is_contiguous():
             raise TypeError("positions must be contiguous int64 [n_tok]")
@@ -132,11 +154,11 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
         (hq, qs, qos), (hk, ks, kos) = sides
         return _dtype_code(x.dtype), n_tok, hq, hk, D, _rotary(freqs, D), qs, ks, qos, kos
 
-    plan = _plan(("rope", _lay(q), _lay(k), _lay(positions), _lay(freqs), _lay(q_out), _lay(k_out)), make)
+    plan = _plan(("rope", _lays(q, k, positions, freqs, q_out, k_out)), make)
     if q_out is None and q is not None:
-        q_out = _empty(q, q.shape, q.dtype, stream)
+        q_out = _empty(q, 3, False, stream)
     if k_out is None and k is not None:
-        k_out = _empty(k, k.shape, k.dtype, stream)
+        k_out = _empty(k, 3, False, stream)
     flags = (GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0) | (GDN_FLAG_ROPE_BACKWARD if backward else 0)
     st = _fn("gdn_rope")(_addr(q), _addr(k), positions.data_ptr(), _addr(freqs), *plan, scale, flags, _addr(q_out),
                          _addr(k_out), _handle(x, stream))
@@ -204,9 +226,9 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     them already), k rotated on the way with freqs, and q [n_tok, Hq, D] rotated into q_out (a new
     tensor, or q itself).  positions int64 [n_tok] replaces the places in the sequences as rotary
     positions.  Returns q_out (None without q)."""
-    _need_cuda(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions, q_out)
 
     def make():
+        _need_cuda(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions, q_out)
         sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, k, v)
         if positions is not None and (positions.dtype != torch.int64 or positions.shape != (sh.n_tok,)
                                       or not positions.is_contiguous()):
@@ -216,10 +238,10 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
             raise ValueError("q_out must be contiguous with q's shape and dtype")
         return sh, ctypes.byref(sh), _rotary(freqs, sh.D)
 
-    _, shape, rd = _plan(("append", _lay(q), _lay(k), _lay(v), _lay(k_cache), _lay(v_cache), _lay(page_table),
-                          _lay(seq_lens), _lay(cu_seqlens), _lay(freqs), _lay(positions), _lay(q_out)), make)
+    _, shape, rd = _plan(("append", _lays(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions,
+                                          q_out)), make)
     if q is not None and q_out is None:
-        q_out = _empty(q, q.shape, q.dtype, stream)
+        q_out = _empty(q, 3, False, stream)
     ws, handle = ((workspace, _handle(k, stream)) if workspace is not None
                   else _own_workspace("cache", 256, k, stream))
     st = _fn("gdn_kv_append")(_addr(q), k.data_ptr(), v.data_ptr(), _addr(positions), _addr(freqs), rd, scale,
@@ -241,24 +263,23 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
     the token at position p of its sequence sees the last `window` positions up to p (0: all).
     max_new: a bound on the new tokens of one sequence (default: all of them).  Returns
     (o [n_tok, Hq, D], lse [n_tok, Hq] fp32 or None)."""
-    _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
 
     def make():
+        _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
         sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
         if o is not None and (o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous()):
             raise ValueError("o must be contiguous with q's shape and dtype")
         if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
             raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
         new = max_new if max_new is not None else sh.n_tok if cu_seqlens is not None else 1
-        return sh, ctypes.byref(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5, tuple(q.shape[:2])
+        return sh, ctypes.byref(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5
 
-    _, shape, new, nbytes, unit, rows = _plan(
-        ("attn", _lay(q), _lay(k_cache), _lay(v_cache), _lay(page_table), _lay(seq_lens), _lay(cu_seqlens), _lay(o),
-         _lay(lse), max_new), make)
+    _, shape, new, nbytes, unit = _plan(
+        ("attn", max_new, _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
     if o is None:
-        o = _empty(q, q.shape, q.dtype, stream)
+        o = _empty(q, 3, False, stream)
     if lse is None and want_lse:
-        lse = _empty(q, rows, torch.float32, stream)
+        lse = _empty(q, 2, True, stream)
     ws, handle = ((workspace, _handle(q, stream)) if workspace is not None
                   else _own_workspace("attn", nbytes, q, stream))
     flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
@@ -275,9 +296,8 @@ def gdn_pages_workspace_bytes(n_pages: int, n_rows: int) -> int:
 
 
 def _page_tables(page_table, seq_lens, refs, page_size):
-    _need_cuda(page_table, seq_lens, refs)
-
     def make():
+        _need_cuda(page_table, seq_lens, refs)
         for name, t, dims in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("refs", refs, 1)):
             if t.dtype != torch.int32 or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
                 raise TypeError(f"{name} must be int32 with contiguous rows")
@@ -288,7 +308,7 @@ def _page_tables(page_table, seq_lens, refs, page_size):
         return (n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages, n_pages, page_size,
                 gdn_pages_workspace_bytes(n_pages, n_rows))
 
-    *rest, nbytes = _plan(("tables", _lay(page_table), _lay(seq_lens), _lay(refs), page_size), make)
+    *rest, nbytes = _plan(("tables", page_size, _lays(page_table, seq_lens, refs)), make)
     return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), *rest), nbytes
 
 
@@ -304,9 +324,9 @@ def _page_pools(pools, n_pages):
     pools = tuple(pools)
     if len(pools) > GDN_MAX_POOLS:
         raise ValueError(f"at most {GDN_MAX_POOLS} pools")
-    _need_cuda(*pools)
 
     def make():
+        _need_cuda(*pools)
         page_bytes = stride = 0
         for t in pools:
             if t.dim() < 2 or t.shape[0] != n_pages:
@@ -321,7 +341,7 @@ def _page_pools(pools, n_pages):
             page_bytes, stride = b, s
         return ctypes.c_void_p * max(1, len(pools)), len(pools), page_bytes, stride
 
-    array, n, page_bytes, stride = _plan(("pools", n_pages, tuple(_lay(t) for t in pools)), make)
+    array, n, page_bytes, stride = _plan(("pools", n_pages, _lays(*pools)), make)
     return GdnPagePools(array(*[t.data_ptr() for t in pools]), n, page_bytes, stride)
 
 
