@@ -63,7 +63,7 @@ def _build_marshal(verbose: bool = False):
     except ImportError:
         return
     root = os.path.dirname(torch.__file__)
-    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
     lib = os.path.join(root, "lib")
     tmp = MARSHAL + f".tmp{os.getpid()}"

@@ -1,11 +1,16 @@
 // marshal.cpp -- what the paged operators' Python binding does on every call, in C++: a key of its tensors'
-// layouts (the checks of a layout run once, when its key is new) and its outputs.  A call's host time is a
-// third less than with the same in Python, which the binding falls back to where this module is not built.
+// layouts (the checks of a layout run once, when its key is new), its outputs, and the library call itself.
+// The binding does the same in Python where this module is not built, at twice the host time a call.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
+
+#include <tuple>
+#include <type_traits>
+
+#include "gdn.h"
 
 namespace {
 
@@ -65,9 +70,78 @@ PyObject *like(PyObject *, PyObject *const *args, Py_ssize_t n) {
   }
 }
 
+struct PyRaised {};  // a Python error has been set
+
+// One argument of a library call: a pointer is a tensor's data, an address or None.
+template <typename P>
+P argument(PyObject *o) {
+  if constexpr (std::is_pointer_v<P>) {
+    if (o == Py_None) return nullptr;
+    if (THPVariable_Check(o)) return (P)THPVariable_Unpack(o).data_ptr();
+    void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw PyRaised{};
+    return (P)p;
+  } else if constexpr (std::is_floating_point_v<P>) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw PyRaised{};
+    return (P)x;
+  } else {
+    const long long x = PyLong_AsLongLong(o);
+    if (x == -1 && PyErr_Occurred()) throw PyRaised{};
+    if ((P)x != x) {
+      PyErr_SetString(PyExc_OverflowError, "an argument does not fit its type");
+      throw PyRaised{};
+    }
+    return (P)x;
+  }
+}
+
+template <typename... P, size_t... I>
+gdn_status invoke(gdn_status (*f)(P...), PyObject *const *args, std::index_sequence<I...>) {
+  const std::tuple<P...> a{argument<P>(args[I])...};
+  PyThreadState *state = PyEval_SaveThread();
+  const gdn_status st = f(std::get<I>(a)...);
+  PyEval_RestoreThread(state);
+  return st;
+}
+
+template <typename F>
+struct Entry;
+// call(address of the library's function, its arguments) -> status
+template <typename... P>
+struct Entry<gdn_status(P...)> {
+  static PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 1 + (Py_ssize_t)sizeof...(P)) {
+      PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+      return nullptr;
+    }
+    try {
+      auto *f = (gdn_status(*)(P...))argument<void *>(args[0]);
+      return PyLong_FromLong(invoke(f, args + 1, std::index_sequence_for<P...>{}));
+    } catch (const PyRaised &) {
+    } catch (const std::exception &e) {
+      PyErr_SetString(PyExc_RuntimeError, e.what());
+    }
+    return nullptr;
+  }
+};
+
+PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f));
+}
+
+#define GDN_ENTRY(name) {#name, fast(Entry<decltype(name)>::call), METH_FASTCALL, "library call"}
 PyMethodDef methods[] = {
-    {"lays", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(lays)), METH_FASTCALL, "key of layouts"},
-    {"like", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(like)), METH_FASTCALL, "new tensor"},
+    {"lays", fast(lays), METH_FASTCALL, "key of layouts"},
+    {"like", fast(like), METH_FASTCALL, "new tensor"},
+    GDN_ENTRY(gdn_rope),
+    GDN_ENTRY(gdn_kv_append),
+    GDN_ENTRY(gdn_paged_attn),
+    GDN_ENTRY(gdn_pages_grow),
+    GDN_ENTRY(gdn_pages_free),
+    GDN_ENTRY(gdn_pages_fork),
+    GDN_ENTRY(gdn_pages_compact),
+    GDN_ENTRY(gdn_pages_copy),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_marshal", "paged operators' marshalling", -1, methods};
 

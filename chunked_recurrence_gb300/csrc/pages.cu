@@ -17,6 +17,8 @@
 #include "sm100.cuh"
 
 using namespace gdn;
+using sm100::grid_dependency_wait;
+using sm100::launch_dependents;
 
 namespace {
 
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
   __shared__ int sh[33];
   const Plan pl = plan_of(workspace, t.n_pages);
   bool bad = false;
+  launch_dependents();  // the moves' blocks wait for this one's end where they read
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int c = children[i];
     int old = -1;
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const gdn_page_tables t, void *workspace) {
   __shared__ int sh[33];
   const Plan pl = plan_of(workspace, t.n_pages);
+  launch_dependents();
   int live = 0;
   for (int i = 4 * threadIdx.x; i < t.n_pages; i += 4 * kPlanThreads) {
     const int4 r = load_refs(t.refs, i, t.n_pages, 0);
@@ -308,6 +312,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
                                                             const int32_t *b, int n, const Pools pools, int n_pools,
                                                             int64_t page_bytes, int64_t page_stride, void *workspace) {
   constexpr int kPer = 8;  // vectors a thread moves in one go, all loads before the first store
+  if (KIND != kCopy) grid_dependency_wait();  // for the plan
   const Plan pl = plan_of(workspace, t.n_pages);
   const int32_t *src = KIND == kCopy ? a : pl.src, *dst = KIND == kCopy ? b : pl.dst;
   int moves = n;
@@ -384,21 +389,30 @@ gdn_status pools_ok(const gdn_page_pools *in, Pools *p) {
   return GDN_OK;
 }
 
+template <typename V, int KIND>
+void launch_move(const gdn_page_tables &t, const int32_t *a, const int32_t *b, int n, const gdn_page_pools &in,
+                 const Pools &pools, void *workspace, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(152 * 8);  // resident at once: 256 threads, eight vectors each in flight
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the plan
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = KIND == kCopy ? 0 : 1;
+  cudaLaunchKernelEx(&cfg, move_kernel<V, KIND>, t, a, b, n, pools, (int)in.n_pools, (int64_t)in.page_bytes,
+                     (int64_t)in.page_stride, workspace);
+}
+
 template <int KIND>
 gdn_status launch_moves(const gdn_page_tables &t, const int32_t *a, const int32_t *b, int n, const gdn_page_pools &in,
                         const Pools &pools, void *workspace, cudaStream_t st) {
   uintptr_t bits = (uintptr_t)in.page_bytes | (uintptr_t)in.page_stride;
   for (int i = 0; i < in.n_pools; ++i) bits |= (uintptr_t)pools.p[i];
-  const int blocks = 152 * 8;  // resident at once: 256 threads, eight vectors each in flight
-  if (bits % 16 == 0)
-    move_kernel<uint4, KIND><<<blocks, kMoveThreads, 0, st>>>(t, a, b, n, pools, in.n_pools, in.page_bytes,
-                                                             in.page_stride, workspace);
-  else if (bits % 4 == 0)
-    move_kernel<uint32_t, KIND><<<blocks, kMoveThreads, 0, st>>>(t, a, b, n, pools, in.n_pools, in.page_bytes,
-                                                                in.page_stride, workspace);
-  else
-    move_kernel<uint8_t, KIND><<<blocks, kMoveThreads, 0, st>>>(t, a, b, n, pools, in.n_pools, in.page_bytes,
-                                                               in.page_stride, workspace);
+  if (bits % 16 == 0) launch_move<uint4, KIND>(t, a, b, n, in, pools, workspace, st);
+  else if (bits % 4 == 0) launch_move<uint32_t, KIND>(t, a, b, n, in, pools, workspace, st);
+  else launch_move<uint8_t, KIND>(t, a, b, n, in, pools, workspace, st);
   return launch_status();
 }
 

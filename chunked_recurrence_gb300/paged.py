@@ -5,6 +5,7 @@ package's __init__; the functions are reached through the package.
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib.util
 import os
 
@@ -17,14 +18,14 @@ from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT,
 
 
 def _load_marshal():
-    """lays and like of the C++ module, or the same in Python where there is none for this torch."""
+    """The C++ module, or its lays and like in Python where there is none for this torch."""
     if os.path.exists(_build.MARSHAL):
         try:
             spec = importlib.util.spec_from_file_location("gdn_marshal", _build.MARSHAL)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             if module.torch_version == torch.__version__.split("+")[0]:
-                return module.lays, module.like
+                return module.lays, module.like, module
         except ImportError:
             pass
 
@@ -34,10 +35,10 @@ def _load_marshal():
     def like(t, dims, f32):
         return torch.empty(t.shape[:dims], dtype=torch.float32 if f32 else t.dtype, device=t.device)
 
-    return lays, like
+    return lays, like, None
 
 
-_lays, _like = _load_marshal()
+_lays, _like, _marshal = _load_marshal()
 
 # What a call's layouts come to (sizes, strides, flags, the workspace's size), worked out and
 # checked once for each combination of shapes, strides, dtypes and devices; addresses are never
@@ -55,17 +56,20 @@ def _plan(key, make):
     return plan
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+_entries = {}
 
 
-_fns = {}
-
-
-def _fn(name):
-    f = _fns.get(name)
+def _entry(name):
+    """The library's function of this name, taking tensors, addresses or None for pointers."""
+    f = _entries.get(name)
     if f is None:
-        f = _fns[name] = getattr(load(), name)
+        fn = getattr(load(), name)
+        if _marshal is not None:
+            f = functools.partial(getattr(_marshal, name), ctypes.cast(fn, ctypes.c_void_p).value)
+        else:
+            def f(*args):
+                return fn(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args])
+        _entries[name] = f
     return f
 
 
@@ -160,8 +164,7 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     if k_out is None and k is not None:
         k_out = _empty(k, 3, False, stream)
     flags = (GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0) | (GDN_FLAG_ROPE_BACKWARD if backward else 0)
-    st = _fn("gdn_rope")(_addr(q), _addr(k), positions.data_ptr(), _addr(freqs), *plan, scale, flags, _addr(q_out),
-                         _addr(k_out), _handle(x, stream))
+    st = _entry("gdn_rope")(q, k, positions, freqs, *plan, scale, flags, q_out, k_out, _handle(x, stream))
     if st:
         _check(st, "gdn_rope")
     return q_out, k_out
@@ -236,7 +239,7 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
         if q_out is not None and (q is None or q_out.shape != q.shape or q_out.dtype != q.dtype
                                   or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous with q's shape and dtype")
-        return sh, ctypes.byref(sh), _rotary(freqs, sh.D)
+        return sh, ctypes.addressof(sh), _rotary(freqs, sh.D)
 
     _, shape, rd = _plan(("append", _lays(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions,
                                           q_out)), make)
@@ -244,10 +247,9 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
         q_out = _empty(q, 3, False, stream)
     ws, handle = ((workspace, _handle(k, stream)) if workspace is not None
                   else _own_workspace("cache", 256, k, stream))
-    st = _fn("gdn_kv_append")(_addr(q), k.data_ptr(), v.data_ptr(), _addr(positions), _addr(freqs), rd, scale,
-                              GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0, page_table.data_ptr(),
-                              seq_lens.data_ptr(), _addr(cu_seqlens), shape, _addr(q_out), k_cache.data_ptr(),
-                              v_cache.data_ptr(), ws.buf.data_ptr(), ws.nbytes, handle)
+    st = _entry("gdn_kv_append")(q, k, v, positions, freqs, rd, scale, GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0,
+                                 page_table, seq_lens, cu_seqlens, shape, q_out, k_cache, v_cache, ws.buf, ws.nbytes,
+                                 handle)
     if st:
         _check(st, "gdn_kv_append")
     return q_out
@@ -272,7 +274,7 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
         if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
             raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
         new = max_new if max_new is not None else sh.n_tok if cu_seqlens is not None else 1
-        return sh, ctypes.byref(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5
+        return sh, ctypes.addressof(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5
 
     _, shape, new, nbytes, unit = _plan(
         ("attn", max_new, _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
@@ -283,9 +285,8 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
     ws, handle = ((workspace, _handle(q, stream)) if workspace is not None
                   else _own_workspace("attn", nbytes, q, stream))
     flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
-    st = _fn("gdn_paged_attn")(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                               seq_lens.data_ptr(), _addr(cu_seqlens), shape, new, unit if scale is None else scale,
-                               window, flags, o.data_ptr(), _addr(lse), ws.buf.data_ptr(), ws.nbytes, handle)
+    st = _entry("gdn_paged_attn")(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, shape, new,
+                                  unit if scale is None else scale, window, flags, o, lse, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_paged_attn")
     return o, lse
@@ -295,7 +296,15 @@ def gdn_pages_workspace_bytes(n_pages: int, n_rows: int) -> int:
     return int(load().gdn_pages_workspace_bytes(int(n_pages), int(n_rows)))
 
 
-def _page_tables(page_table, seq_lens, refs, page_size):
+def _page_list(name, t, n=None):
+    _need_cuda(t)
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise TypeError(f"{name} must be a contiguous int32 list" + ("" if n is None else f" of {n}"))
+    return t.shape[0]
+
+
+def _page_tables(page_table, seq_lens, refs, page_size, names=(), *lists):
+    """The tables as the library takes them, the length of the lists of rows, and a workspace's size."""
     def make():
         _need_cuda(page_table, seq_lens, refs)
         for name, t, dims in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("refs", refs, 1)):
@@ -304,19 +313,14 @@ def _page_tables(page_table, seq_lens, refs, page_size):
         n_rows, max_pages = page_table.shape
         if seq_lens.shape[0] != n_rows:
             raise ValueError("seq_lens must have one entry a row of page_table")
-        n_pages = refs.shape[0]
-        return (n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages, n_pages, page_size,
-                gdn_pages_workspace_bytes(n_pages, n_rows))
+        n_pages, n = refs.shape[0], None
+        for name, t in zip(names, lists):
+            n = _page_list(name, t, n)
+        rest = (n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages, n_pages, page_size)
+        return rest, n, gdn_pages_workspace_bytes(n_pages, n_rows)
 
-    *rest, nbytes = _plan(("tables", page_size, _lays(page_table, seq_lens, refs)), make)
-    return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), *rest), nbytes
-
-
-def _page_list(name, t, n=None):
-    _need_cuda(t)
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise TypeError(f"{name} must be a contiguous int32 list" + ("" if n is None else f" of {n}"))
-    return t.shape[0]
+    rest, n, nbytes = _plan(("tables", page_size, names, _lays(page_table, seq_lens, refs, *lists)), make)
+    return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), *rest), n, nbytes
 
 
 def _page_pools(pools, n_pages):
@@ -354,42 +358,42 @@ def _pages_workspace(nbytes, t, workspace, stream):
 def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, workspace=None, stream=None):
     """Sequences `seqs` grow to `new_lens` tokens (device int32 lists): missing pages come from the free
     ones in rising order.  Nothing changes (GDN_ERR_PAGES in the workspace's status) if they do not suffice."""
-    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
-    n = _page_list("seqs", seqs)
-    _page_list("new_lens", new_lens, n)
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs", "new_lens"), seqs, new_lens)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    _check(_fn("gdn_pages_grow")(ctypes.byref(t), seqs.data_ptr(), new_lens.data_ptr(), n, ws.buf.data_ptr(), ws.nbytes,
-                                 handle), "gdn_pages_grow")
+    st = _entry("gdn_pages_grow")(ctypes.addressof(t), seqs, new_lens, n, ws.buf, ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_pages_grow")
 
 
 def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, stream=None):
     """Sequences `seqs` give their pages back and become empty."""
-    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
-    n = _page_list("seqs", seqs)
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs",), seqs)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    _check(_fn("gdn_pages_free")(ctypes.byref(t), seqs.data_ptr(), n, ws.buf.data_ptr(), ws.nbytes, handle),
-           "gdn_pages_free")
+    st = _entry("gdn_pages_free")(ctypes.addressof(t), seqs, n, ws.buf, ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_pages_free")
 
 
 def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_size, workspace=None, stream=None):
     """The empty rows `children` become copies of the rows `parents`: full pages shared, a part-filled last
     page copied in every pool ([n_pages, ...] tensors: the k and v caches of every layer)."""
-    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
-    n = _page_list("parents", parents)
-    _page_list("children", children, n)
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("parents", "children"), parents, children)
     p = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    _check(_fn("gdn_pages_fork")(ctypes.byref(t), parents.data_ptr(), children.data_ptr(), n, ctypes.byref(p),
-                                 ws.buf.data_ptr(), ws.nbytes, handle), "gdn_pages_fork")
+    st = _entry("gdn_pages_fork")(ctypes.addressof(t), parents, children, n, ctypes.addressof(p), ws.buf, ws.nbytes,
+                                  handle)
+    if st:
+        _check(st, "gdn_pages_fork")
 
 
 def gdn_pages_compact(page_table, seq_lens, refs, pools, page_size, workspace=None, stream=None):
     """The live pages come together at the start of the pools; tables and refs follow."""
-    t, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
+    t, _, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
     p = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    _check(_fn("gdn_pages_compact")(ctypes.byref(t), ctypes.byref(p), ws.buf.data_ptr(), ws.nbytes, handle),
-           "gdn_pages_compact")
+    st = _entry("gdn_pages_compact")(ctypes.addressof(t), ctypes.addressof(p), ws.buf, ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_pages_compact")
 
 
 def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
@@ -401,5 +405,6 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     p = _page_pools(pools, n_pages)
     ws, handle = ((workspace, _handle(src, stream)) if workspace is not None
                   else _own_workspace("pages", 256, src, stream))
-    _check(_fn("gdn_pages_copy")(src.data_ptr(), dst.data_ptr(), n, n_pages, ctypes.byref(p), ws.buf.data_ptr(),
-                                 ws.nbytes, handle), "gdn_pages_copy")
+    st = _entry("gdn_pages_copy")(src, dst, n, n_pages, ctypes.addressof(p), ws.buf, ws.nbytes, handle)
+    if st:
+        _check(st, "gdn_pages_copy")
