@@ -7,6 +7,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <cstring>
 #include <tuple>
 #include <type_traits>
 
@@ -49,6 +50,58 @@ PyObject *lays(PyObject *, PyObject *const *args, Py_ssize_t n) try {
   return nullptr;
 }
 
+struct PyRaised {};  // a Python error has been set
+
+// One argument of a library call: a pointer is a tensor's data, a bytes object's, an address or None.
+template <typename P>
+P argument(PyObject *o) {
+  if constexpr (std::is_pointer_v<P>) {
+    if (o == Py_None) return nullptr;
+    if (THPVariable_Check(o)) return (P)THPVariable_Unpack(o).data_ptr();
+    if (PyBytes_Check(o)) return (P)PyBytes_AS_STRING(o);
+    void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw PyRaised{};
+    return (P)p;
+  } else if constexpr (std::is_floating_point_v<P>) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw PyRaised{};
+    return (P)x;
+  } else {
+    const long long x = PyLong_AsLongLong(o);
+    if (x == -1 && PyErr_Occurred()) throw PyRaised{};
+    if ((P)x != x) {
+      PyErr_SetString(PyExc_OverflowError, "an argument does not fit its type");
+      throw PyRaised{};
+    }
+    return (P)x;
+  }
+}
+
+// pack(tail, *pointers) -> bytes: the pointers (as in a call), then the bytes of tail: a struct of the library
+PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n < 1 || n > kMost + 1 || !PyBytes_Check(args[0])) {
+    PyErr_SetString(PyExc_TypeError, "pack(tail, *pointers)");
+    return nullptr;
+  }
+  const Py_ssize_t heads = (n - 1) * sizeof(void *), tail = PyBytes_GET_SIZE(args[0]);
+  PyObject *out = PyBytes_FromStringAndSize(nullptr, heads + tail);
+  if (!out) return nullptr;
+  char *p = PyBytes_AS_STRING(out);
+  memcpy(p + heads, PyBytes_AS_STRING(args[0]), tail);
+  try {
+    for (Py_ssize_t i = 1; i < n; ++i, p += sizeof(void *)) {
+      const void *x = argument<void *>(args[i]);
+      memcpy(p, &x, sizeof x);
+    }
+    return out;
+  } catch (const PyRaised &) {
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  Py_DECREF(out);
+  return nullptr;
+}
+
 // like(tensor, dims, f32) -> a new contiguous tensor of the sizes of its first `dims` dimensions
 PyObject *like(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n != 3 || !THPVariable_Check(args[0])) {
@@ -67,32 +120,6 @@ PyObject *like(PyObject *, PyObject *const *args, Py_ssize_t n) {
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
-  }
-}
-
-struct PyRaised {};  // a Python error has been set
-
-// One argument of a library call: a pointer is a tensor's data, an address or None.
-template <typename P>
-P argument(PyObject *o) {
-  if constexpr (std::is_pointer_v<P>) {
-    if (o == Py_None) return nullptr;
-    if (THPVariable_Check(o)) return (P)THPVariable_Unpack(o).data_ptr();
-    void *p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw PyRaised{};
-    return (P)p;
-  } else if constexpr (std::is_floating_point_v<P>) {
-    const double x = PyFloat_AsDouble(o);
-    if (x == -1.0 && PyErr_Occurred()) throw PyRaised{};
-    return (P)x;
-  } else {
-    const long long x = PyLong_AsLongLong(o);
-    if (x == -1 && PyErr_Occurred()) throw PyRaised{};
-    if ((P)x != x) {
-      PyErr_SetString(PyExc_OverflowError, "an argument does not fit its type");
-      throw PyRaised{};
-    }
-    return (P)x;
   }
 }
 
@@ -134,6 +161,7 @@ PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
 PyMethodDef methods[] = {
     {"lays", fast(lays), METH_FASTCALL, "key of layouts"},
     {"like", fast(like), METH_FASTCALL, "new tensor"},
+    {"pack", fast(pack), METH_FASTCALL, "struct of pointers and a tail"},
     GDN_ENTRY(gdn_rope),
     GDN_ENTRY(gdn_kv_append),
     GDN_ENTRY(gdn_paged_attn),

@@ -8,6 +8,7 @@ import ctypes
 import functools
 import importlib.util
 import os
+import struct
 
 import torch
 
@@ -18,15 +19,15 @@ from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT,
 
 
 def _load_marshal():
-    """The C++ module, or its lays and like in Python where there is none for this torch."""
+    """lays, like and pack of the C++ module, and itself; the three in Python where there is none for this torch."""
     if os.path.exists(_build.MARSHAL):
         try:
             spec = importlib.util.spec_from_file_location("gdn_marshal", _build.MARSHAL)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             if module.torch_version == torch.__version__.split("+")[0]:
-                return module.lays, module.like, module
-        except ImportError:
+                return module.lays, module.like, module.pack, module
+        except (ImportError, AttributeError):  # another torch's, or an older build's
             pass
 
     def lays(*tensors):
@@ -35,10 +36,14 @@ def _load_marshal():
     def like(t, dims, f32):
         return torch.empty(t.shape[:dims], dtype=torch.float32 if f32 else t.dtype, device=t.device)
 
-    return lays, like, None
+    def pack(tail, *pointers):
+        at = [p.data_ptr() if isinstance(p, torch.Tensor) else ctypes.cast(p, ctypes.c_void_p).value for p in pointers]
+        return struct.pack(f"{len(at)}P", *at) + tail
+
+    return lays, like, pack, None
 
 
-_lays, _like, _marshal = _load_marshal()
+_lays, _like, _pack, _marshal = _load_marshal()
 
 # What a call's layouts come to (sizes, strides, flags, the workspace's size), worked out and
 # checked once for each combination of shapes, strides, dtypes and devices; addresses are never
@@ -60,7 +65,7 @@ _entries = {}
 
 
 def _entry(name):
-    """The library's function of this name, taking tensors, addresses or None for pointers."""
+    """The library's function of this name, taking tensors, bytes, addresses or None for pointers."""
     f = _entries.get(name)
     if f is None:
         fn = getattr(load(), name)
@@ -316,15 +321,16 @@ def _page_tables(page_table, seq_lens, refs, page_size, names=(), *lists):
         n_pages, n = refs.shape[0], None
         for name, t in zip(names, lists):
             n = _page_list(name, t, n)
-        rest = (n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages, n_pages, page_size)
-        return rest, n, gdn_pages_workspace_bytes(n_pages, n_rows)
+        t = GdnPageTables(None, None, None, n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages,
+                          n_pages, page_size)
+        return bytes(t)[3 * ctypes.sizeof(ctypes.c_void_p):], n, gdn_pages_workspace_bytes(n_pages, n_rows)
 
-    rest, n, nbytes = _plan(("tables", page_size, names, _lays(page_table, seq_lens, refs, *lists)), make)
-    return GdnPageTables(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), *rest), n, nbytes
+    tail, n, nbytes = _plan(("tables", page_size, names, _lays(page_table, seq_lens, refs, *lists)), make)
+    return _pack(tail, page_table, seq_lens, refs), n, nbytes
 
 
 def _page_pools(pools, n_pages):
-    """The pools as the library takes them; each page must be one contiguous block of its pool."""
+    """The pools as the library takes them, and what that points to; a page must be one contiguous block of its pool."""
     pools = tuple(pools)
     if len(pools) > GDN_MAX_POOLS:
         raise ValueError(f"at most {GDN_MAX_POOLS} pools")
@@ -343,10 +349,11 @@ def _page_pools(pools, n_pages):
             if page_bytes and (b, s) != (page_bytes, stride):
                 raise ValueError("the pools' pages must have one size and stride")
             page_bytes, stride = b, s
-        return ctypes.c_void_p * max(1, len(pools)), len(pools), page_bytes, stride
+        return bytes(GdnPagePools(None, len(pools), page_bytes, stride))[ctypes.sizeof(ctypes.c_void_p):]
 
-    array, n, page_bytes, stride = _plan(("pools", n_pages, _lays(*pools)), make)
-    return GdnPagePools(array(*[t.data_ptr() for t in pools]), n, page_bytes, stride)
+    tail = _plan(("pools", n_pages, _lays(*pools)), make)
+    at = _pack(b"", *pools)
+    return _pack(tail, at), at
 
 
 def _pages_workspace(nbytes, t, workspace, stream):
@@ -360,7 +367,7 @@ def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, worksp
     ones in rising order.  Nothing changes (GDN_ERR_PAGES in the workspace's status) if they do not suffice."""
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs", "new_lens"), seqs, new_lens)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_grow")(ctypes.addressof(t), seqs, new_lens, n, ws.buf, ws.nbytes, handle)
+    st = _entry("gdn_pages_grow")(t, seqs, new_lens, n, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_pages_grow")
 
@@ -369,7 +376,7 @@ def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, 
     """Sequences `seqs` give their pages back and become empty."""
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs",), seqs)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_free")(ctypes.addressof(t), seqs, n, ws.buf, ws.nbytes, handle)
+    st = _entry("gdn_pages_free")(t, seqs, n, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_pages_free")
 
@@ -378,10 +385,9 @@ def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_si
     """The empty rows `children` become copies of the rows `parents`: full pages shared, a part-filled last
     page copied in every pool ([n_pages, ...] tensors: the k and v caches of every layer)."""
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("parents", "children"), parents, children)
-    p = _page_pools(pools, refs.shape[0])
+    p, _keep = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_fork")(ctypes.addressof(t), parents, children, n, ctypes.addressof(p), ws.buf, ws.nbytes,
-                                  handle)
+    st = _entry("gdn_pages_fork")(t, parents, children, n, p, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_pages_fork")
 
@@ -389,9 +395,9 @@ def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_si
 def gdn_pages_compact(page_table, seq_lens, refs, pools, page_size, workspace=None, stream=None):
     """The live pages come together at the start of the pools; tables and refs follow."""
     t, _, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
-    p = _page_pools(pools, refs.shape[0])
+    p, _keep = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_compact")(ctypes.addressof(t), ctypes.addressof(p), ws.buf, ws.nbytes, handle)
+    st = _entry("gdn_pages_compact")(t, p, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_pages_compact")
 
@@ -402,9 +408,9 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     n = _page_list("src", src)
     _page_list("dst", dst, n)
     n_pages = pools[0].shape[0] if pools else 0
-    p = _page_pools(pools, n_pages)
+    p, _keep = _page_pools(pools, n_pages)
     ws, handle = ((workspace, _handle(src, stream)) if workspace is not None
                   else _own_workspace("pages", 256, src, stream))
-    st = _entry("gdn_pages_copy")(src, dst, n, n_pages, ctypes.addressof(p), ws.buf, ws.nbytes, handle)
+    st = _entry("gdn_pages_copy")(src, dst, n, n_pages, p, ws.buf, ws.nbytes, handle)
     if st:
         _check(st, "gdn_pages_copy")
