@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "paged.cuh"
 #include "paged_attn.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 
@@ -58,7 +59,7 @@ PagedSeqs paged_seqs(const gdn_cache_shape &s, const int32_t *seq_lens, const in
 
 namespace {
 
-constexpr int kWarps = 4, kRows = 4;
+constexpr int kWarps = 4, kRows = 4, kJoin = 128;
 
 template <typename T, int NE>
 __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const SimtArgs a) {
@@ -155,26 +156,51 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const Simt
   }
 }
 
-// one warp per row: the parts' maxima, sums and weighted sums joined
+// A block per row: the parts' maxima, sums and weighted sums joined.  A lane has the maximum and sum of parts lane
+// and lane + 32 (there are at most 64); a warp adds up every fourth part.
 template <typename T>
-__global__ void __launch_bounds__(128) simt_join_kernel(const float *part, int splits, int64_t rows, int D, T *o,
-                                                        float *lse) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (r >= rows) return;
-  const int64_t step = rows * (D + 2);
+__global__ void __launch_bounds__(kJoin) simt_join_kernel(const float *part, int splits, int64_t rows, int D, T *o,
+                                                          float *lse) {
+  __shared__ float s_x[kJoin / 32][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sm100::grid_dependency_wait();
+  const int64_t r = blockIdx.x, step = rows * (D + 2);
   const float *p = part + r * (D + 2);
-  float top = -INFINITY, sum = 0.f;
-  for (int i = 0; i < splits; ++i) top = fmaxf(top, p[i * step]);
-  for (int i = 0; i < splits; ++i) sum += p[i * step + 1] == 0.f ? 0.f : exp2f(p[i * step] - top) * p[i * step + 1];
+  float m[2], l[2], w[2], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = lane + 32 * j;
+    m[j] = i < splits ? p[i * step] : -INFINITY, l[j] = i < splits ? p[i * step + 1] : 0.f;
+    top = fmaxf(top, m[j]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = l[j] == 0.f ? 0.f : exp2f(m[j] - top);
+    sum += w[j] * l[j];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int d = lane; d < D; d += 32) {
+  for (int d = lane; d < (D + 31) / 32 * 32; d += 32) {
     float x = 0.f;
-    for (int i = 0; i < splits; ++i)
-      if (p[i * step + 1] != 0.f) x += exp2f(p[i * step] - top) * p[i * step + 2 + d];
+#pragma unroll 4
+    for (int i = warp; i < splits; i += kJoin / 32) {
+      const float a = __shfl_sync(0xffffffffu, w[0], i & 31), b = __shfl_sync(0xffffffffu, w[1], i & 31);
+      const float wi = i < 32 ? a : b, u = d < D ? p[i * step + 2 + d] : 0.f;
+      if (wi != 0.f) x += wi * u;  // a part that saw nothing has no say
+    }
+    s_x[warp][d] = x;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kJoin) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoin / 32; ++i) x += s_x[i][d];
     o[r * D + d] = from_f32<T>(x * inv);
   }
-  if (lane == 0 && lse) lse[r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  if (threadIdx.x == 0 && lse) lse[r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // Parts a row group's positions are cut into: enough blocks for the GPU, at most 16.
@@ -208,7 +234,13 @@ gdn_status dispatch_simt(const SimtArgs &a, int64_t slots, cudaStream_t st) {
 template <typename T>
 gdn_status launch_join(const SimtArgs &a, cudaStream_t st) {
   const int64_t rows = (int64_t)a.seqs.n_tok * a.Hq;
-  simt_join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a.part, a.splits, rows, a.D, (T *)a.o, a.lse);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows), cfg.blockDim = dim3(kJoin), cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the parts' end
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, simt_join_kernel<T>, (const float *)a.part, (int)a.splits, rows, (int)a.D, (T *)a.o, a.lse);
   return launch_status();
 }
 
@@ -222,7 +254,7 @@ extern "C" size_t gdn_paged_attn_workspace_bytes(const gdn_cache_shape *shape, i
   // any non-null offsets: the number of tokens is checked by the call
   static const int32_t some = 0;
   if (max_new < 0 || normalise_cache_shape(shape, &some, &s) != GDN_OK) return 0;
-  return std::max({parts_bytes(s, simt_splits(s)), parts_bytes(s, paged_attn_f32_splits(s, max_new)),
+  return std::max({parts_bytes(s, simt_splits(s)), parts_bytes(s, paged_attn_f32_splits(s, max_new, 0)),
                    paged_attn_tc_workspace(s, max_new)});
 }
 
@@ -249,7 +281,7 @@ extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const v
   const bool simt = flags & GDN_FLAG_SIMT;
   SimtArgs a{seqs, q, k_cache, v_cache, o, lse, nullptr, page_table, s.table_stride, s.page_stride, s.slot_stride,
              s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages, s.n_pages, window,
-             simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new), scale_log2, (int32_t *)workspace};
+             simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new, window), scale_log2, (int32_t *)workspace};
   if (a.splits > 1) a.part = (float *)((char *)workspace + 256);
   gdn_status r;
   if (simt) {

@@ -30,7 +30,7 @@ struct SimtArgs {
   int32_t *status;
 };
 
-int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new);
+int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new, int32_t window);  // window 0: the most of any
 gdn_status paged_attn_f32(const SimtArgs &a, const gdn_cache_shape &s, int32_t max_new, cudaStream_t st);
 
 }  // namespace gdn

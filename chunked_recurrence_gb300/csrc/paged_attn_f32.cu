@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "paged.cuh"
 #include "paged_attn.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace {
@@ -49,18 +50,19 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
   const int G = a.Hq / a.Hkv, h = blockIdx.y, part = blockIdx.z;
   const Item it = item_at(a.seqs, blockIdx.x, G, C::R, 1, a.window);  // tiles of one position
   if (!it.ok && tid == 0) set_status(a.status, GDN_ERR_BOUNDS);
+  sm100::launch_dependents();
   if (it.rows <= 0) return;
   const int begin = it.lo + (int)share_begin(it.hi - it.lo, part, a.splits);
   const int end = it.lo + (int)share_begin(it.hi - it.lo, part + 1, a.splits);
-  const int tile0 = begin / C::BN, n_tiles = end > begin ? (end + C::BN - 1) / C::BN - tile0 : 0;
+  const int n_tiles = (max(end - begin, 0) + C::BN - 1) / C::BN;
   const int32_t *table = a.table + (int64_t)it.s * a.table_stride;
 
   // where a position's rows lie in the caches, -1: not read
   auto places = [&](int tile) {
     if (tid < C::BN) {
-      const int p = (tile0 + tile) * C::BN + tid;
+      const int p = begin + tile * C::BN + tid;
       int64_t at = -1;
-      if (tile < n_tiles && p >= begin && p < end) {
+      if (tile < n_tiles && p < end) {
         const int page = page_of(table, p, a.page_size, a.max_pages, a.n_pages);
         if (page < 0) set_status(a.status, GDN_ERR_BOUNDS);
         else at = (int64_t)page * a.page_stride + (int64_t)(p % a.page_size) * a.slot_stride + (int64_t)h * a.head_stride;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
     __syncthreads();  // this tile is there, the next one's places too, and the tile before is done with
     if (tile + 1 < n_tiles) load(tile + 1);
     const float *k = ks + (tile & 1) * C::kTile + n0 * C::kPitch, *v = vs + (tile & 1) * C::kTile + n0 * C::kPitch;
-    const int pos = (tile0 + tile) * C::BN + n0;
+    const int pos = begin + tile * C::BN + n0;
 
     float s[C::kMine / 8][4];
 #pragma unroll
@@ -292,14 +294,16 @@ bool few_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_n
 
 }  // namespace
 
-// Parts that a block's positions are cut into: enough blocks for the GPU, no part below two tiles of the longest
-// sequence that the table can hold, at most 64.
-int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new) {
+// Parts that a block's positions are cut into: two blocks an SM (three with few rows), no part below 64 positions of the longest span that the table and the window allow, at most 64.
+// Single tokens of 24 sequences over 1000, D 128: 78 us, 112 us with as many blocks as are resident at most; 5 chunks
+// of up to 37 over 700 with a window of 200, D 64: 13.9 us, 18.2 us with parts from 128 positions on.
+int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new, int32_t window) {
   const bool few = few_rows(s, max_new);
   const int64_t blocks = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, few ? 16 : 64) * s.Hkv;
   const int64_t want = (152 * (few ? 3 : 2) + blocks - 1) / std::max<int64_t>(blocks, 1);
-  const int64_t most = ((int64_t)s.max_pages * s.page_size + 127) / 128;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({64, want, most}));
+  int64_t span = (int64_t)s.max_pages * s.page_size;
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + std::min<int64_t>(max_new, 64));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({64, want, (span + 63) / 64}));
 }
 
 gdn_status paged_attn_f32(const SimtArgs &a, const gdn_cache_shape &s, int32_t max_new, cudaStream_t st) {
