@@ -24,7 +24,7 @@ using namespace gdn;
 
 namespace {
 
-// Two heads a lane in flight and three blocks an SM (80 registers): 29 us over the rows of 8192 tokens x 40 heads x
+// Two heads a lane in flight and three blocks an SM (80 registers): 29.5 us over the rows of 8192 tokens x 40 heads x
 // 128 bf16 (168 MB, 5.8 TB/s); four heads and two blocks 29.4 us, four blocks 31 us, without the rows' prefetch 31.4 us.
 constexpr int kThreads = 256, kHeads = 2;
 
@@ -144,7 +144,8 @@ __device__ __forceinline__ void prefetch_row(const void *p, int64_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes) : "memory");
 }
 
-// A warp takes a token, or one of `parts` parts of its heads.  In a rotary column place a lane holds VEC
+// A warp takes a token, or one of `parts` parts of its heads and vectors, dealt out in turn (134 MB appended, 5460 tokens
+// in two parts: 27.1 us; 29.3 us with the parts' heads and vectors in blocks of as many as a lane has in flight).  In a rotary column place a lane holds VEC
 // pairs of a head in the half layout (two vectors), VEC / 2 pairs interleaved (one vector; VEC = 1:
 // one pair as two vectors of one element); 32 / rot heads go side by side over the lanes.
 template <typename T, int VEC, bool APPEND, bool INTER>
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
     if (lane == 1 && a.Hk) prefetch_row(k, (int64_t)a.Hk * a.D * sizeof(T));
     if (lane == 2 && APPEND) prefetch_row((const T *)a.v + t * a.vs, (int64_t)a.Hv * a.D * sizeof(T));
   }
+  const uint64_t freq0 = lane < half ? a.freqs[lane] : 0;  // on its way while the token's place is looked up
   int64_t pos = 0, slot = 0;
   if (APPEND) {
     slot = append_slot(a, t, pos);
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   }
   if (half && a.positions) pos = a.positions[t];
   for (int i = lane; i < half; i += 32) {
-    const float2 f = cos_sin((uint32_t)(((uint64_t)pos * a.freqs[i]) >> 32));
+    const float2 f = cos_sin((uint32_t)(((uint64_t)pos * (i < 32 ? freq0 : a.freqs[i])) >> 32));
     cs[i] = make_float2(f.x * a.scale, f.y * a.scale * a.sign);
   }
   __syncwarp();
@@ -189,11 +191,11 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
       const float2 f = cs[c * kPairs + j];
       cn[j] = f.x, sn[j] = f.y;
     }
-    for (int h0 = part * side * kHeads; h0 < heads; h0 += parts * side * kHeads) {
+    for (int h0 = part * side + hl; h0 < heads; h0 += parts * side * kHeads) {
       Vec<T, VEC> x1[kHeads], x2[kHeads];
 #pragma unroll
       for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i * side + hl;
+        const int h = h0 + i * parts * side;
         const T *x = (h < a.Hq ? q : k - a.Hq * a.D) + h * a.D + e;
         if (h < heads && hl < side) {
           x1[i] = *reinterpret_cast<const Vec<T, VEC> *>(x);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
       }
 #pragma unroll
       for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i * side + hl;
+        const int h = h0 + i * parts * side;
         T *y = h < a.Hq ? qo + h * a.D + e : ko + (h - a.Hq) * k_head + e;
         if constexpr (two) turn_halves(x1[i], x2[i], cn, sn);
         else turn_neighbours(x1[i], cn, sn);
@@ -217,10 +219,10 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   // ---- what passes through: columns [rd, D) of q and k where they are not in place, all of v
   auto copy = [&](const T *x, T *y, int64_t y_head, int n_heads, int from) {
     const int cols = (a.D - from) / VEC, all = n_heads * cols;
-    constexpr int kAhead = 8;
-    // place i of a lane is (head h, column c); 32 places on, without a division
-    const int dh = 32 / cols, dc = 32 - dh * cols;
-    for (int i0 = part * 32 * kAhead + lane; i0 < all; i0 += parts * 32 * kAhead) {
+    constexpr int kAhead = 4;
+    // place i of a lane is (head h, column c); a step on, without a division
+    const int step = 32 * parts, dh = step / cols, dc = step - dh * cols;
+    for (int i0 = part * 32 + lane; i0 < all; i0 += step * kAhead) {
       Vec<T, VEC> v[kAhead];
       int h = i0 / cols, c = i0 - h * cols;
       const int h_first = h, c_first = c;
