@@ -144,10 +144,11 @@ __device__ __forceinline__ void prefetch_row(const void *p, int64_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes) : "memory");
 }
 
-// A warp takes a token, or one of `parts` parts of its heads and vectors, dealt out in turn (134 MB appended, 5460 tokens
-// in two parts: 27.1 us; 29.3 us with the parts' heads and vectors in blocks of as many as a lane has in flight).  In a rotary column place a lane holds VEC
-// pairs of a head in the half layout (two vectors), VEC / 2 pairs interleaved (one vector; VEC = 1:
-// one pair as two vectors of one element); 32 / rot heads go side by side over the lanes.
+// A warp takes a token, or one of `parts` parts of its heads and vectors, dealt out in turn (134 MB appended, 5460
+// tokens in two parts: 27.1 us; 29.3 us with the parts' heads and vectors in blocks of as many as a lane has in
+// flight).  In a rotary column place a lane holds VEC pairs of a head in the half layout (two vectors), VEC / 2 pairs
+// interleaved (one vector; VEC = 1: one pair as two vectors of one element); 32 / rot heads go side by side over the
+// lanes.
 template <typename T, int VEC, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int parts) {
   constexpr int kPairs = INTER ? (VEC + 1) / 2 : VEC;  // of a place
