@@ -48,9 +48,10 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
   int64_t *off = reinterpret_cast<int64_t *>(vs + 2 * C::kTile);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
   const int G = a.Hq / a.Hkv, h = blockIdx.y, part = blockIdx.z;
+  sm100::launch_dependents();
+  sm100::grid_dependency_wait();
   const Item it = item_at(a.seqs, blockIdx.x, G, C::R, 1, a.window);  // tiles of one position
   if (!it.ok && tid == 0) set_status(a.status, GDN_ERR_BOUNDS);
-  sm100::launch_dependents();
   if (it.rows <= 0) return;
   const int begin = it.lo + (int)share_begin(it.hi - it.lo, part, a.splits);
   const int end = it.lo + (int)share_begin(it.hi - it.lo, part + 1, a.splits);
@@ -291,7 +292,14 @@ gdn_status launch(const SimtArgs &a, bool wide, cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   const int64_t slots = item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.Hq / a.Hkv, C::R);
-  kernel<<<dim3((unsigned)slots, a.Hkv, a.splits), kThreads, C::kSmem, st>>>(a, wide);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)slots, a.Hkv, a.splits), cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem, cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the launch overlaps the end of the kernel before
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, a, wide);
   return launch_status();
 }
 

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_table
                                                             const int32_t *new_lens, int n, void *workspace) {
   __shared__ int sh[33];
   const Plan pl = plan_of(workspace, t.n_pages);
+  grid_dependency_wait();
   bool bad = false;
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int s = seqs[i];
@@ -168,6 +169,8 @@ __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_table
 __global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, const int32_t *seqs, void *workspace) {
   __shared__ int s_len;
   const Plan pl = plan_of(workspace, t.n_pages);
+  grid_dependency_wait();
+  launch_dependents();
   const int s = seqs[blockIdx.x];
   if (s < 0 || s >= t.n_rows) {
     if (threadIdx.x == 0) set_status(pl.status, GDN_ERR_PAGES);
@@ -197,6 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
   __shared__ int sh[33];
   const Plan pl = plan_of(workspace, t.n_pages);
   bool bad = false;
+  grid_dependency_wait();
   launch_dependents();  // the moves' blocks wait for this one's end where they read
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int c = children[i];
@@ -252,6 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const gdn_page_tables t, void *workspace) {
   __shared__ int sh[33];
   const Plan pl = plan_of(workspace, t.n_pages);
+  grid_dependency_wait();
   launch_dependents();
   int live = 0;
   for (int i = 4 * threadIdx.x; i < t.n_pages; i += 4 * kPlanThreads) {
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
                                                             const int32_t *b, int n, const Pools pools, int n_pools,
                                                             int64_t page_bytes, int64_t page_stride, void *workspace) {
   constexpr int kPer = 8;  // vectors a thread moves in one go, all loads before the first store
-  if (KIND != kCopy) grid_dependency_wait();  // for the plan
+  grid_dependency_wait();  // for the plan
   const Plan pl = plan_of(workspace, t.n_pages);
   const int32_t *src = KIND == kCopy ? a : pl.src, *dst = KIND == kCopy ? b : pl.dst;
   int moves = n;
@@ -389,20 +394,24 @@ gdn_status pools_ok(const gdn_page_pools *in, Pools *p) {
   return GDN_OK;
 }
 
+// A launch that overlaps the end of the kernel before on the stream, whose results the kernel waits for.
+template <typename... P, typename... A>
+void launch_early(void (*kernel)(P...), int blocks, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename V, int KIND>
 void launch_move(const gdn_page_tables &t, const int32_t *a, const int32_t *b, int n, const gdn_page_pools &in,
                  const Pools &pools, void *workspace, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(152 * 8);  // resident at once: 256 threads, eight vectors each in flight
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the plan
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = KIND == kCopy ? 0 : 1;
-  cudaLaunchKernelEx(&cfg, move_kernel<V, KIND>, t, a, b, n, pools, (int)in.n_pools, (int64_t)in.page_bytes,
-                     (int64_t)in.page_stride, workspace);
+  const int blocks = 152 * 8;  // resident at once: 256 threads, eight vectors each in flight
+  launch_early(move_kernel<V, KIND>, blocks, kMoveThreads, st, t, a, b, n, pools, (int)in.n_pools,
+               (int64_t)in.page_bytes, (int64_t)in.page_stride, workspace);
 }
 
 template <int KIND>
@@ -433,7 +442,7 @@ extern "C" gdn_status gdn_pages_grow(const gdn_page_tables *tables, const int32_
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs || !new_lens) return GDN_ERR_INVALID_ARG;
-  grow_kernel<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(t, seqs, new_lens, n, workspace);
+  launch_early(grow_kernel, 1, kPlanThreads, (cudaStream_t)stream, t, seqs, new_lens, (int)n, workspace);
   return launch_status();
 }
 
@@ -444,7 +453,7 @@ extern "C" gdn_status gdn_pages_free(const gdn_page_tables *tables, const int32_
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs) return GDN_ERR_INVALID_ARG;
-  free_kernel<<<n, 256, 0, (cudaStream_t)stream>>>(t, seqs, workspace);
+  launch_early(free_kernel, n, 256, (cudaStream_t)stream, t, seqs, workspace);
   return launch_status();
 }
 
@@ -460,7 +469,7 @@ extern "C" gdn_status gdn_pages_fork(const gdn_page_tables *tables, const int32_
   if (n == 0) return GDN_OK;
   if (!parents || !children) return GDN_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(t, parents, children, n, workspace);
+  launch_early(fork_plan_kernel, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   return launch_moves<kFork>(t, parents, children, n, *pools, p, workspace, st);
 }
@@ -475,7 +484,7 @@ extern "C" gdn_status gdn_pages_compact(const gdn_page_tables *tables, const gdn
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (t.n_pages == 0) return GDN_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(t, workspace);
+  launch_early(compact_plan_kernel, 1, kPlanThreads, st, t, workspace);
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   return launch_moves<kCompact>(t, nullptr, nullptr, 0, *pools, p, workspace, st);
 }

@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "conv_tap.cuh"
 #include "paged.cuh"
+#include "sm100.cuh"
 
 using namespace gdn;
 
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a, int
   const int lane = threadIdx.x & 31, half = a.rd >> 1;
   const int64_t job = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int t = (int)(job / parts), part = (int)(job - (int64_t)t * parts);
+  sm100::grid_dependency_wait();
   if (t >= a.n_tok) return;
   float2 *cs = s_cs[threadIdx.x >> 5];
   const T *q = (const T *)a.q + t * a.qs, *k = (const T *)a.k + t * a.ks;
@@ -252,8 +254,13 @@ gdn_status launch_vec(const RopeArgs &a, bool inter, cudaStream_t st) {
   // a token's heads over several warps where the tokens alone would not fill the GPU some three times over
   const int parts = std::max(1, std::min((a.Hq + a.Hk + a.Hv + 7) / 8, 152 * 80 / a.n_tok));
   const int64_t blocks = ((int64_t)a.n_tok * parts * 32 + kThreads - 1) / kThreads;
-  if (inter) rope_kernel<T, VEC, APPEND, true><<<(unsigned)blocks, kThreads, 0, st>>>(a, parts);
-  else rope_kernel<T, VEC, APPEND, false><<<(unsigned)blocks, kThreads, 0, st>>>(a, parts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = dim3(kThreads), cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the launch overlaps the end of the kernel before
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, inter ? rope_kernel<T, VEC, APPEND, true> : rope_kernel<T, VEC, APPEND, false>, a, parts);
   return launch_status();
 }
 
