@@ -444,11 +444,15 @@ gdn_status gdn_kv_append(const void *q, const void *k, const void *v, const int6
  *   flags: GDN_FLAG_SIMT (the CUDA-core kernel), GDN_FLAG_TEST_NO_WAIT
  *   workspace: gdn_paged_attn_workspace_bytes(shape, max_new), 256-byte aligned, not shared by
  *   calls that may overlap; nothing in it has to be kept or cleared between calls.
- * Scores, softmax and sums are fp32.  On the tensor-core path (bf16; D 64, 128 or 256; page_size
- * a multiple of 8; 16-byte aligned pointers and strides) the softmax weights are rounded to
- * bf16 before the product with v, and an infinity or NaN in v at a position of the
- * sequence may reach its tile's earlier queries too (0 * inf); slots at or past seq_lens
- * never do. */
+ * Scores, softmax and sums are fp32.  Three kernels:
+ *   bf16; D 64, 128 or 256; page_size a multiple of 8 up to 2^20; Hq / Hkv up to 128; a positive scale
+ *   (1e-20 to 1e20); 16-byte aligned pointers and strides: tcgen05, the softmax weights rounded to
+ *   bf16 before the product with v;
+ *   everything else: products of fp32's precision on the tensor cores (each operand in two TF32 parts);
+ *   GDN_FLAG_SIMT: fp32 on the CUDA cores.
+ * Slots at or past seq_lens, and positions that no query of a tile sees, reach nothing whatever they hold.
+ * On the first two an infinity or NaN in v at a position that some query of the tile sees may reach the
+ * tile's other queries (0 * inf); with GDN_FLAG_SIMT it reaches only those that see it. */
 size_t gdn_paged_attn_workspace_bytes(const gdn_cache_shape *shape, int32_t max_new);
 gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *page_table,
                           const int32_t *seq_lens, const int32_t *cu_seqlens, const gdn_cache_shape *shape,
