@@ -6,9 +6,9 @@
 // are (fp32) and are split in registers as fragments are loaded, x = hi + lo, both TF32, a product
 // taking hi*hi + hi*lo + lo*hi (the dropped term is 2^-22 of it).  bf16 values are exact in TF32 and need no lo.
 // The matrix instructions, three a product, and the splitting bound chunks: 24 of 200 tokens over 1000, 64/8 heads,
-// D 256: 3.95 ms, 72 TFLOP/s, 215 of TF32 products (the CUDA-core kernel 14.4 ms).
+// D 256: 4.4 ms, 64 TFLOP/s, 193 of TF32 products (the CUDA-core kernel 14.4 ms).
 // Single tokens wait on their own chain of products, eight of a warp's sixteen rows unused: 24 over 1000, 32/8 heads,
-// D 128: 78 us, 38% of HBM.  Small calls are a chain of latencies: 5 chunks with a window of 200: 13 us.
+// D 128: 81 us, 36% of HBM.  Small calls are a chain of latencies: 5 chunks with a window of 200: 13 us.
 //
 // A block of four warps takes query rows of one sequence and kv head (row = token * group + head in the
 // group) and one of `splits` parts of their positions, tile by tile of BN positions, the next tile's
@@ -136,37 +136,43 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
     const float *k = ks + (tile & 1) * C::kTile + n0 * C::kPitch, *v = vs + (tile & 1) * C::kTile + n0 * C::kPitch;
     const int pos = begin + tile * C::BN + n0;
 
-    // with few rows a warp has one product of 8 positions: its sum goes in four parts, whose MMAs do not wait for each
-    // other (60 single tokens over 1000, D 256: 528 us, 660 us in one part)
-    constexpr int kChains = FEW ? 4 : 1, kUnroll = FEW ? 8 : 2;
-    float s[C::kMine / 8][4], sx[kChains][C::kMine / 8][4];
+    // The MMAs' accumulation cuts off where an fp32 addition rounds, always towards zero, so a sum is made of parts of
+    // four steps (with few rows, where a warp has one product at a time, of one: four that do not wait for each
+    // other), added by fp32 additions: an error of 6.6e-7 for chunks of 40 over 6000, D 128, and of 3.1e-6 with one
+    // chain of MMAs (fp32 products and sums in a library's order: 1.4e-6).  It costs 4.4 ms for 3.95 at D 256.
+    constexpr int kParts = FEW ? 4 : 1;
+    float s[C::kMine / 8][4];
 #pragma unroll
-    for (int c = 0; c < kChains; ++c)
+    for (int i = 0; i < C::kMine / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < DP; k0 += 32) {
+      float x[kParts][C::kMine / 8][4];
 #pragma unroll
-      for (int i = 0; i < C::kMine / 8; ++i) sx[c][i][0] = sx[c][i][1] = sx[c][i][2] = sx[c][i][3] = 0.f;
-#pragma unroll kUnroll
-    for (int kk = 0; kk < DP; kk += 8) {
-      const float *q = qs + (m0 + g4) * C::kPitch + kk + t4;
-      tc::FragA fa;
-      if constexpr (C::kExact) tc::frag_a_exact(fa, q[0], q[8 * C::kPitch], q[4], q[8 * C::kPitch + 4]);
-      else tc::frag_a(fa, q[0], q[8 * C::kPitch], q[4], q[8 * C::kPitch + 4]);
+      for (int c = 0; c < kParts; ++c)
 #pragma unroll
-      for (int i = 0; i < C::kMine / 8; ++i) {
-        const float *b = k + (i * 8 + g4) * C::kPitch + kk + t4;
-        tc::FragB fb;
-        if constexpr (C::kExact) tc::frag_b_exact(fb, b[0], b[4]);
-        else tc::frag_b(fb, b[0], b[4]);
-        tc::mma_x<C::kExact, C::kExact>(sx[kk / 8 % kChains][i], fa, fb);
+        for (int i = 0; i < C::kMine / 8; ++i) x[c][i][0] = x[c][i][1] = x[c][i][2] = x[c][i][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < 32; kk += 8) {
+        const float *q = qs + (m0 + g4) * C::kPitch + k0 + kk + t4;
+        tc::FragA fa;
+        if constexpr (C::kExact) tc::frag_a_exact(fa, q[0], q[8 * C::kPitch], q[4], q[8 * C::kPitch + 4]);
+        else tc::frag_a(fa, q[0], q[8 * C::kPitch], q[4], q[8 * C::kPitch + 4]);
+#pragma unroll
+        for (int i = 0; i < C::kMine / 8; ++i) {
+          const float *b = k + (i * 8 + g4) * C::kPitch + k0 + kk + t4;
+          tc::FragB fb;
+          if constexpr (C::kExact) tc::frag_b_exact(fb, b[0], b[4]);
+          else tc::frag_b(fb, b[0], b[4]);
+          tc::mma_x<C::kExact, C::kExact>(x[kk / 8 % kParts][i], fa, fb);
+        }
       }
+#pragma unroll
+      for (int c = 0; c < kParts; ++c)
+#pragma unroll
+        for (int i = 0; i < C::kMine / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] += x[c][i][e];
     }
-#pragma unroll
-    for (int i = 0; i < C::kMine / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[i][e] = sx[0][i][e];
-#pragma unroll
-        for (int c = 1; c < kChains; ++c) s[i][e] += sx[c][i][e];
-      }
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < C::kMine / 8; ++i)
@@ -187,10 +193,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
       m[e] = top[e];
       l[e] *= keep[e];
     }
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] *= keep[e >> 1];
+    tc::FragA pa[C::kMine / 8];  // columns 2t, 2t + 1 of P as the operand's t, t + 4
 #pragma unroll
     for (int j = 0; j < C::kMine / 8; ++j) {
       float p[4];
@@ -199,16 +202,28 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
         p[e] = exp2f(s[j][e] - base[e >> 1]);
         l[e >> 1] += p[e];
       }
-      tc::FragA fa;  // columns 2t, 2t + 1 of P as the operand's t, t + 4
-      tc::frag_a(fa, p[0], p[2], p[1], p[3]);
+      tc::frag_a(pa[j], p[0], p[2], p[1], p[3]);
+    }
+    // four columns' products of the tile side by side, then onto the scaled sums
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        const float *b = v + (j * 8 + 2 * t4) * C::kPitch + i * 8 + g4;
-        tc::FragB fb;
-        if constexpr (C::kExact) tc::frag_b_exact(fb, b[0], b[C::kPitch]);
-        else tc::frag_b(fb, b[0], b[C::kPitch]);
-        tc::mma_x<false, C::kExact>(o[i], fa, fb);
-      }
+    for (int i0 = 0; i0 < DP / 8; i0 += 4) {
+      float x[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < C::kMine / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float *b = v + (j * 8 + 2 * t4) * C::kPitch + (i0 + i) * 8 + g4;
+          tc::FragB fb;
+          if constexpr (C::kExact) tc::frag_b_exact(fb, b[0], b[C::kPitch]);
+          else tc::frag_b(fb, b[0], b[C::kPitch]);
+          tc::mma_x<false, C::kExact>(x[i], pa[j], fb);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i0 + i][e] = fmaf(o[i0 + i][e], keep[e >> 1], x[i][e]);
     }
   }
 #pragma unroll
