@@ -37,7 +37,8 @@ def _load_marshal():
         return torch.empty(t.shape[:dims], dtype=torch.float32 if f32 else t.dtype, device=t.device)
 
     def pack(tail, *pointers):
-        at = [p.data_ptr() if isinstance(p, torch.Tensor) else ctypes.cast(p, ctypes.c_void_p).value for p in pointers]
+        at = [p.data_ptr() if isinstance(p, torch.Tensor) else ctypes.cast(p, ctypes.c_void_p).value or 0
+              for p in pointers]
         return struct.pack(f"{len(at)}P", *at) + tail
 
     return lays, like, pack, None
