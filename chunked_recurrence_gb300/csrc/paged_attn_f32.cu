@@ -333,9 +333,10 @@ bool few_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_n
 
 }  // namespace
 
-// Parts that a block's positions are cut into: two blocks an SM (three with few rows), no part below 64 positions of the longest span that the table and the window allow, at most 64.
-// Single tokens of 24 sequences over 1000, D 128: 78 us, 112 us with as many blocks as are resident at most; 5 chunks
-// of up to 37 over 700 with a window of 200, D 64: 13.9 us, 18.2 us with parts from 128 positions on.
+// Parts that a block's positions are cut into: two blocks an SM (three with few rows), no part below 64 positions of
+// the longest span that the table and the window allow, at most 64.  Single tokens of 24 sequences over 1000, D 128:
+// 78 us, 112 us with as many blocks as are resident at most; 5 chunks of up to 37 over 700 with a window of 200, D 64:
+// 13.9 us, 18.2 us with parts from 128 positions on.
 int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new, int32_t window) {
   const bool few = few_rows(s, max_new);
   const int64_t blocks = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, few ? 16 : 64) * s.Hkv;

@@ -7,11 +7,11 @@
 // 16-byte loads) and leaves lists in the workspace.  What is proportional to the data
 // (table rows, page contents) runs on the whole GPU (move_kernel), which reads the lists.
 //
-// Copying is bound by HBM: a moved byte is read once and written once (1.14 GB read and written to bring the pages of
-// a half-empty cache together: 181 us, 94% of a copy's rate).  Small calls are launches and the plan's chain of loads: freeing and forking 24 of 48 sequences
-// 13 us, 5 of them the plan.  No page is both read
-// and written by one call (compact moves pages at or past L into free ones below it; fork's new
-// pages were free), so the copies run in any order.
+// Copying is bound by HBM: a moved byte is read once and written once (1.14 GB read and written to bring the pages of a
+// half-empty cache together: 181 us, 94% of a copy's rate).  Small calls are launches and the plan's chain of loads:
+// freeing and forking 24 of 48 sequences 13 us, 5 of them the plan.  No page is both read and written by one call
+// (compact moves pages at or past L into free ones below it; fork's new pages were free), so the copies run in any
+// order.
 #include <algorithm>
 
 #include "common.cuh"
