@@ -125,7 +125,15 @@ def _heads(name, t, D=None):
         raise ValueError(f"{name}: heads and features must be contiguous within a token")
     if D is not None and d != D:
         raise ValueError(f"{name}: head width {d}, expected {D}")
-    return s[0] if n > 1 else h * d
+    return _row_stride(name, n, s[0], h * d)
+
+
+def _row_stride(name, n, stride, row):
+    """Stride of n rows of `row` elements as the library takes it, where 0 would mean dense: a broadcast
+    tensor (stride 0) or one whose rows overlap is refused."""
+    if n > 1 and stride < row:
+        raise ValueError(f"{name}: rows overlap (a broadcast tensor?): use .contiguous()")
+    return stride if n > 1 else row
 
 
 def _rotary(freqs, D):
@@ -186,6 +194,8 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
     n_pages, page_size, Hkv, D = k_cache.shape
     if D > 1 and k_cache.stride(3) != 1:
         raise ValueError("the caches' last dimension must be contiguous")
+    if any(n > 1 and s < D for n, s in zip(k_cache.shape[:3], k_cache.stride()[:3])):
+        raise ValueError("the caches' pages, slots and heads must not overlap")
     if any(t is not None and t.dtype != x.dtype for t in (k_cache, v_cache, k, v)):
         raise TypeError("q, k, v and the caches must have one dtype")
     for name, t in (("page_table", page_table), ("seq_lens", seq_lens), ("cu_seqlens", cu_seqlens)):
@@ -209,7 +219,7 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
         raise ValueError("Hq must be a multiple of Hkv")
     st = k_cache.stride()
     return GdnCacheShape(n_seqs, n_tok, Hq, Hkv, D, _dtype_code(x.dtype), page_size, n_pages, max_pages,
-                         page_table.stride(0) if n_seqs > 1 else max_pages, st[0], st[1], st[2],
+                         _row_stride("page_table", n_seqs, page_table.stride(0), max_pages), st[0], st[1], st[2],
                          0 if q is None else _heads("q", q, D), 0 if k is None else _heads("k", k, D),
                          0 if v is None else _heads("v", v, D))
 
@@ -322,8 +332,8 @@ def _page_tables(page_table, seq_lens, refs, page_size, names=(), *lists):
         n_pages, n = refs.shape[0], None
         for name, t in zip(names, lists):
             n = _page_list(name, t, n)
-        t = GdnPageTables(None, None, None, n_rows, max_pages, page_table.stride(0) if n_rows > 1 else max_pages,
-                          n_pages, page_size)
+        t = GdnPageTables(None, None, None, n_rows, max_pages,
+                          _row_stride("page_table", n_rows, page_table.stride(0), max_pages), n_pages, page_size)
         return bytes(t)[3 * ctypes.sizeof(ctypes.c_void_p):], n, gdn_pages_workspace_bytes(n_pages, n_rows)
 
     tail, n, nbytes = _plan(("tables", page_size, names, _lays(page_table, seq_lens, refs, *lists)), make)
