@@ -299,6 +299,8 @@ def make_shape(q, k, v, cu_seqlens=None, B=None, n_seqs=None) -> GdnShape:
     for n, t, inner in (("q", q, K), ("k", k, K), ("v", v, V)):
         if t.stride(2) != 1 or t.stride(1) != inner:
             raise ValueError(f"{n}: heads and features must be contiguous within a token")
+        if n_tok > 1 and t.stride(0) == 0:  # the library would read it as dense
+            raise ValueError(f"{n}: tokens overlap (a broadcast tensor?): use .contiguous()")
     if cu_seqlens is not None:
         Bv, T, ns = 1, n_tok, (cu_seqlens.numel() - 1 if n_seqs is None else n_seqs)
     else:

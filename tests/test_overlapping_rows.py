@@ -75,3 +75,15 @@ def test_page_tables(no_launch, name):
     with pytest.raises(ValueError, match="overlap"):
         getattr(crg, "gdn_pages_" + name)(i32(1, 4).expand(5, 4), i32(5), i32(8), *lists[name], 16)
     assert no_launch == []
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_recurrent_shapes(which):
+    qkv = [torch.zeros(6, 2, 64), torch.zeros(6, 2, 64), torch.zeros(6, 4, 32)]
+    assert crg.make_shape(*qkv).q_stride == 128
+    qkv[which] = qkv[which][:1].expand(6, -1, -1)
+    with pytest.raises(ValueError, match="overlap"):
+        crg.make_shape(*qkv)
+    one = [t[:1] for t in qkv]  # a single token has nothing to lie upon
+    one[which] = one[which].as_strided(one[which].shape, (0, one[which].shape[2], 1))
+    crg.make_shape(*one)
