@@ -56,13 +56,14 @@ class GdnCacheShape(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("n_seqs", "n_tok", "Hq", "Hkv", "D", "dtype", "page_size", "n_pages",
                                                "max_pages")]
                 + [(n, ctypes.c_int64) for n in ("table_stride", "page_stride", "slot_stride", "head_stride",
-                                                 "q_stride", "k_stride", "v_stride")])
+                                                 "q_stride", "k_stride", "v_stride")]
+                + [("status", ctypes.c_void_p)])
 
 
 class GdnPageTables(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
                 ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
-                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("status", ctypes.c_void_p)]
 
 
 class GdnPagePools(ctypes.Structure):
@@ -82,6 +83,7 @@ _SIGS = {
     "gdn_workspace_reset": ([_P, _SZ, _P], ctypes.c_int),
     "gdn_workspace_status": ([_P, ctypes.POINTER(_I32), _P], ctypes.c_int),
     "gdn_workspace_path": ([_P, ctypes.POINTER(_I32), _P], ctypes.c_int),
+    "gdn_status_words": ([ctypes.POINTER(_P)], ctypes.c_int),
     "gdn_gate_prep": ([_P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _P], ctypes.c_int),
     "gdn_conv1d_varlen": ([_P, _P, _P, _I32, _P, _I32, _I64, _I32, _I32, _I32, _P, _P],
                           ctypes.c_int),
@@ -592,4 +594,5 @@ def segment_parallel_fwd(q, k, v, g, beta, seg_bounds, h0=None, scale=None, l2no
 # full attention over a paged cache
 from .paged import (cache_shape, gdn_kv_append, gdn_paged_attn, gdn_paged_attn_workspace_bytes,  # noqa: E402,F401
                     gdn_pages_compact, gdn_pages_copy, gdn_pages_fork, gdn_pages_free, gdn_pages_grow,
-                    gdn_pages_workspace_bytes, gdn_rope, gdn_rope_freqs, gdn_rope_inv_freq)
+                    gdn_pages_workspace_bytes, gdn_paged_status, gdn_paged_status_reset, gdn_rope, gdn_rope_freqs,
+                    gdn_rope_inv_freq)

@@ -28,7 +28,7 @@ extern "C" const char *gdn_status_string(int status) {
   }
 }
 
-extern "C" int32_t gdn_version(void) { return (1 << 16) | 2; }
+extern "C" int32_t gdn_version(void) { return (1 << 16) | 3; }
 
 extern "C" gdn_status gdn_workspace_reset(void *workspace, size_t workspace_bytes, void *stream) {
   if (!workspace || workspace_bytes < sizeof(int32_t)) return GDN_ERR_WORKSPACE;
@@ -56,6 +56,16 @@ extern "C" gdn_status gdn_workspace_status(const void *workspace, int32_t *statu
     return GDN_ERR_CUDA;
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return GDN_ERR_CUDA;
   *status_out = v;
+  return GDN_OK;
+}
+
+namespace {
+__device__ __align__(256) int32_t g_status[64];
+}
+
+extern "C" gdn_status gdn_status_words(void **words) {
+  if (!words) return GDN_ERR_INVALID_ARG;
+  if (cudaGetSymbolAddress(words, g_status) != cudaSuccess) return (void)cudaGetLastError(), GDN_ERR_CUDA;
   return GDN_OK;
 }
 

@@ -45,6 +45,7 @@ gdn_status normalise_cache_shape(const gdn_cache_shape *in, const int32_t *cu_se
   if (s.v_stride == 0) s.v_stride = (int64_t)s.Hkv * s.D;
   if (s.q_stride < (int64_t)s.Hq * s.D || s.k_stride < (int64_t)s.Hkv * s.D || s.v_stride < (int64_t)s.Hkv * s.D)
     return GDN_ERR_INVALID_ARG;
+  if (!aligned(s.status, sizeof(int32_t))) return GDN_ERR_INVALID_ARG;
   if (s.D > 256 || s.Hq > 65535) return GDN_ERR_UNSUPPORTED;
   // rows of a kv head and slots of items fit 32 bits
   if ((int64_t)s.n_tok * (s.Hq / s.Hkv) + s.n_seqs > 2147483647LL / 2) return GDN_ERR_UNSUPPORTED;
@@ -281,7 +282,8 @@ extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const v
   const bool simt = flags & GDN_FLAG_SIMT;
   SimtArgs a{seqs, q, k_cache, v_cache, o, lse, nullptr, page_table, s.table_stride, s.page_stride, s.slot_stride,
              s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages, s.n_pages, window,
-             simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new, window), scale_log2, (int32_t *)workspace};
+             simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new, window), scale_log2,
+             s.status ? s.status : (int32_t *)workspace};
   if (a.splits > 1) a.part = (float *)((char *)workspace + 256);
   gdn_status r;
   if (simt) {

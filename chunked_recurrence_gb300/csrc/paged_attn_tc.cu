@@ -1083,7 +1083,7 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
 }
 
 template <int D, int NQ, bool PAIR>
-gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st) {
+gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, void *workspace, cudaStream_t st) {
   using C = Cfg<D, NQ, PAIR>;
   a.box = std::gcd(s.page_size, C::kRowsK);  // a power of two
   a.box_log2 = __builtin_ctz(a.box);
@@ -1091,7 +1091,7 @@ gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs
   if (!make_q_map(&mq, a.q, s, a.G, a.RT) || !make_map(&mk, k, s, a.box) || !make_map(&mv, v, s, a.box))
     return GDN_ERR_CUDA;
   constexpr int units = kSms / C::kPair;
-  char *w = (char *)a.status;
+  char *w = (char *)workspace;
   a.meta = (int4 *)(w + 256);
   a.part_ml = (float *)(w + 256 + sizeof(int4) * 512);
   a.part = a.part_ml + (size_t)units * 2 * C::R * 2;
@@ -1168,13 +1168,15 @@ gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int3
   a.page_size = s.page_size, a.page_mask = s.page_size & (s.page_size - 1) ? -1 : s.page_size - 1;
   a.max_pages = s.max_pages, a.n_pages = s.n_pages;
   a.window = window, a.c = scale_log2;
-  a.status = (int32_t *)workspace;
+  a.status = s.status ? s.status : (int32_t *)workspace;
   a.no_wait = flags & GDN_FLAG_TEST_NO_WAIT ? 1 : 0;
   const bool pair = pairs(s, max_new);
-  if (s.D == 256) return pair ? launch<256, 1, true>(k, v, s, a, st) : launch<256, 1, false>(k, v, s, a, st);
-  if (pair) return launch<128, 2, true>(k, v, s, a, st);
-  if (two_tiles(s, max_new)) return s.D == 128 ? launch<128, 2, false>(k, v, s, a, st) : launch<64, 2, false>(k, v, s, a, st);
-  return s.D == 128 ? launch<128, 1, false>(k, v, s, a, st) : launch<64, 1, false>(k, v, s, a, st);
+  if (s.D == 256)
+    return pair ? launch<256, 1, true>(k, v, s, a, workspace, st) : launch<256, 1, false>(k, v, s, a, workspace, st);
+  if (pair) return launch<128, 2, true>(k, v, s, a, workspace, st);
+  if (two_tiles(s, max_new))
+    return s.D == 128 ? launch<128, 2, false>(k, v, s, a, workspace, st) : launch<64, 2, false>(k, v, s, a, workspace, st);
+  return s.D == 128 ? launch<128, 1, false>(k, v, s, a, workspace, st) : launch<64, 1, false>(k, v, s, a, workspace, st);
 }
 
 }  // namespace gdn

@@ -39,10 +39,11 @@ struct Plan {
   int32_t *rows;            // [n_rows] lengths saved while a list is checked
 };
 
-__host__ __device__ Plan plan_of(void *workspace, int32_t n_pages) {
+__device__ Plan plan_of(void *workspace, const gdn_page_tables &t) {
   char *p = (char *)workspace;
+  const int32_t n_pages = t.n_pages;
   Plan r;
-  r.status = (int32_t *)p;
+  r.status = t.status ? t.status : (int32_t *)p;
   r.w = (PlanWords *)(p + 128);
   r.src = (int32_t *)(p + 256);
   r.dst = r.src + n_pages;
@@ -119,7 +120,7 @@ __device__ __forceinline__ int32_t *table_row(const gdn_page_tables &t, int s) {
 __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_tables t, const int32_t *seqs,
                                                             const int32_t *new_lens, int n, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t.n_pages);
+  const Plan pl = plan_of(workspace, t);
   grid_dependency_wait();
   bool bad = false;
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_table
 
 __global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, const int32_t *seqs, void *workspace) {
   __shared__ int s_len;
-  const Plan pl = plan_of(workspace, t.n_pages);
+  const Plan pl = plan_of(workspace, t);
   grid_dependency_wait();
   launch_dependents();
   const int s = seqs[blockIdx.x];
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, cons
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_tables t, const int32_t *parents,
                                                                  const int32_t *children, int n, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t.n_pages);
+  const Plan pl = plan_of(workspace, t);
   bool bad = false;
   grid_dependency_wait();
   launch_dependents();  // the moves' blocks wait for this one's end where they read
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const gdn_page_tables t, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t.n_pages);
+  const Plan pl = plan_of(workspace, t);
   grid_dependency_wait();
   launch_dependents();
   int live = 0;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
                                                             int64_t page_bytes, int64_t page_stride, void *workspace) {
   constexpr int kPer = 8;  // vectors a thread moves in one go, all loads before the first store
   grid_dependency_wait();  // for the plan
-  const Plan pl = plan_of(workspace, t.n_pages);
+  const Plan pl = plan_of(workspace, t);
   const int32_t *src = KIND == kCopy ? a : pl.src, *dst = KIND == kCopy ? b : pl.dst;
   int moves = n;
   if (KIND != kCopy) {
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
 bool tables_ok(const gdn_page_tables *in, gdn_page_tables *t) {
   if (!in) return false;
   *t = *in;
-  if (t->n_rows < 0 || t->max_pages < 0 || t->n_pages < 0 || t->page_size < 1) return false;
+  if (t->n_rows < 0 || t->max_pages < 0 || t->n_pages < 0 || t->page_size < 1 || !aligned(t->status, sizeof(int32_t)))
+    return false;
   if (t->table_stride == 0) t->table_stride = t->max_pages;
   if (t->table_stride < t->max_pages || t->n_pages >= 1 << 21) return false;  // sums of 1024 rows' pages: 32 bits
   return (t->n_rows == 0 || (t->page_table && t->seq_lens)) && (t->n_pages == 0 || t->refs);

@@ -372,7 +372,7 @@ extern "C" gdn_status gdn_kv_append(const void *q, const void *k, const void *v,
   a.table = page_table, a.table_stride = s.table_stride;
   a.page_stride = s.page_stride, a.slot_stride = s.slot_stride, a.head_stride = s.head_stride;
   a.page_size = s.page_size, a.max_pages = s.max_pages, a.n_pages = s.n_pages;
-  a.status = (int32_t *)workspace;
+  a.status = s.status ? s.status : (int32_t *)workspace;
   const bool inter = flags & GDN_FLAG_ROPE_INTERLEAVED;
   if (s.dtype == GDN_BF16) return launch_type<__nv_bfloat16, true>(a, inter, (cudaStream_t)stream);
   return launch_type<float, true>(a, inter, (cudaStream_t)stream);

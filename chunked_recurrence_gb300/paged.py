@@ -98,6 +98,45 @@ def _as_stream(like, stream):
     return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=like.device)
 
 
+_words = {}
+
+
+def _status_words(index):
+    """Address of the library's 256 bytes on a device: the status word of its calls without a workspace."""
+    at = _words.get(index)
+    if at is None:
+        out = ctypes.c_void_p()
+        with torch.cuda.device(index):
+            _check(load().gdn_status_words(ctypes.byref(out)), "gdn_status_words")
+        at = _words[index] = out.value
+    return at
+
+
+def _device_words(device, stream):
+    device = torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    return ctypes.c_void_p(_status_words(index)), ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
+
+
+def gdn_paged_status(device="cuda", stream=None) -> int:
+    """The status of a device's gdn_kv_append, gdn_paged_attn and gdn_pages_* calls without a workspace (those with
+    one leave theirs in it): GDN_OK, or the first error that one of them found on the GPU since the last
+    gdn_paged_status_reset: GDN_ERR_PAGES (a grow or fork was refused), GDN_ERR_BOUNDS, GDN_ERR_TIMEOUT.
+    Synchronises `stream` (default: the current one)."""
+    words, stream = _device_words(device, stream)
+    out = ctypes.c_int32(0)
+    _check(load().gdn_workspace_status(words, ctypes.byref(out), stream), "gdn_workspace_status")
+    return out.value
+
+
+def gdn_paged_status_reset(device="cuda", stream=None):
+    """gdn_paged_status is GDN_OK again once `stream` comes to here."""
+    words, stream = _device_words(device, stream)
+    _check(load().gdn_workspace_reset(words, 256, stream), "gdn_workspace_reset")
+
+
 def gdn_rope_inv_freq(rotary_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0, alpha=1.0, beta=32.0):
     """Frequencies of the rotary pairs, fp64 on the CPU [rotary_dim / 2]: base^(-2i / rotary_dim), with
     scaling "linear" (over factor), "base" (a larger base) or "parts" (by parts, over orig_len positions)."""
@@ -261,11 +300,10 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
                                           q_out)), make)
     if q is not None and q_out is None:
         q_out = _empty(q, 3, False, stream)
-    ws, handle = ((workspace, _handle(k, stream)) if workspace is not None
-                  else _own_workspace("cache", 256, k, stream))
+    buf, nbytes = (workspace.buf, workspace.nbytes) if workspace is not None else (_status_words(k.get_device()), 256)
     st = _entry("gdn_kv_append")(q, k, v, positions, freqs, rd, scale, GDN_FLAG_ROPE_INTERLEAVED if interleaved else 0,
-                                 page_table, seq_lens, cu_seqlens, shape, q_out, k_cache, v_cache, ws.buf, ws.nbytes,
-                                 handle)
+                                 page_table, seq_lens, cu_seqlens, shape, q_out, k_cache, v_cache, buf, nbytes,
+                                 _handle(k, stream))
     if st:
         _check(st, "gdn_kv_append")
     return q_out
@@ -290,10 +328,12 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
         if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
             raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
         new = max_new if max_new is not None else sh.n_tok if cu_seqlens is not None else 1
+        if workspace is None:
+            sh.status = _status_words(q.get_device())
         return sh, ctypes.addressof(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5
 
     _, shape, new, nbytes, unit = _plan(
-        ("attn", max_new, _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
+        ("attn", max_new, workspace is None, _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
     if o is None:
         o = _empty(q, 3, False, stream)
     if lse is None and want_lse:
@@ -319,7 +359,7 @@ def _page_list(name, t, n=None):
     return t.shape[0]
 
 
-def _page_tables(page_table, seq_lens, refs, page_size, names=(), *lists):
+def _page_tables(page_table, seq_lens, refs, page_size, workspace, names=(), *lists):
     """The tables as the library takes them, the length of the lists of rows, and a workspace's size."""
     def make():
         _need_cuda(page_table, seq_lens, refs)
@@ -333,10 +373,11 @@ def _page_tables(page_table, seq_lens, refs, page_size, names=(), *lists):
         for name, t in zip(names, lists):
             n = _page_list(name, t, n)
         t = GdnPageTables(None, None, None, n_rows, max_pages,
-                          _row_stride("page_table", n_rows, page_table.stride(0), max_pages), n_pages, page_size)
+                          _row_stride("page_table", n_rows, page_table.stride(0), max_pages), n_pages, page_size,
+                          None if workspace is not None else _status_words(page_table.get_device()))
         return bytes(t)[3 * ctypes.sizeof(ctypes.c_void_p):], n, gdn_pages_workspace_bytes(n_pages, n_rows)
 
-    tail, n, nbytes = _plan(("tables", page_size, names, _lays(page_table, seq_lens, refs, *lists)), make)
+    tail, n, nbytes = _plan(("tables", page_size, names, workspace is None, _lays(page_table, seq_lens, refs, *lists)), make)
     return _pack(tail, page_table, seq_lens, refs), n, nbytes
 
 
@@ -375,8 +416,9 @@ def _pages_workspace(nbytes, t, workspace, stream):
 
 def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, workspace=None, stream=None):
     """Sequences `seqs` grow to `new_lens` tokens (device int32 lists): missing pages come from the free
-    ones in rising order.  Nothing changes (GDN_ERR_PAGES in the workspace's status) if they do not suffice."""
-    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs", "new_lens"), seqs, new_lens)
+    ones in rising order.  Nothing changes, the lengths included, if they do not suffice: GDN_ERR_PAGES in
+    the status of the workspace, or of gdn_paged_status without one."""
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs", "new_lens"), seqs, new_lens)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
     st = _entry("gdn_pages_grow")(t, seqs, new_lens, n, ws.buf, ws.nbytes, handle)
     if st:
@@ -385,7 +427,7 @@ def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, worksp
 
 def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, stream=None):
     """Sequences `seqs` give their pages back and become empty."""
-    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("seqs",), seqs)
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs",), seqs)
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
     st = _entry("gdn_pages_free")(t, seqs, n, ws.buf, ws.nbytes, handle)
     if st:
@@ -394,8 +436,10 @@ def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, 
 
 def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_size, workspace=None, stream=None):
     """The empty rows `children` become copies of the rows `parents`: full pages shared, a part-filled last
-    page copied in every pool ([n_pages, ...] tensors: the k and v caches of every layer)."""
-    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, ("parents", "children"), parents, children)
+    page copied in every pool ([n_pages, ...] tensors: the k and v caches of every layer).  Nothing changes
+    if the lists cannot be carried out or the free pages do not suffice: GDN_ERR_PAGES, as for gdn_pages_grow."""
+    t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("parents", "children"), parents,
+                                children)
     p, _keep = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
     st = _entry("gdn_pages_fork")(t, parents, children, n, p, ws.buf, ws.nbytes, handle)
@@ -405,7 +449,7 @@ def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_si
 
 def gdn_pages_compact(page_table, seq_lens, refs, pools, page_size, workspace=None, stream=None):
     """The live pages come together at the start of the pools; tables and refs follow."""
-    t, _, nbytes = _page_tables(page_table, seq_lens, refs, page_size)
+    t, _, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace)
     p, _keep = _page_pools(pools, refs.shape[0])
     ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
     st = _entry("gdn_pages_compact")(t, p, ws.buf, ws.nbytes, handle)
@@ -420,8 +464,7 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     _page_list("dst", dst, n)
     n_pages = pools[0].shape[0] if pools else 0
     p, _keep = _page_pools(pools, n_pages)
-    ws, handle = ((workspace, _handle(src, stream)) if workspace is not None
-                  else _own_workspace("pages", 256, src, stream))
-    st = _entry("gdn_pages_copy")(src, dst, n, n_pages, p, ws.buf, ws.nbytes, handle)
+    buf, nbytes = (workspace.buf, workspace.nbytes) if workspace is not None else (_status_words(src.get_device()), 256)
+    st = _entry("gdn_pages_copy")(src, dst, n, n_pages, p, buf, nbytes, _handle(src, stream))
     if st:
         _check(st, "gdn_pages_copy")

@@ -100,8 +100,8 @@ class Hybrid:
         self._pages(crg.gdn_pages_compact, self.pools)
 
     def check(self):
-        """Synchronises; whether every page operation could be carried out."""
-        return self.pages_ws.status() == crg.GDN_OK
+        """Synchronises; whether every page operation could be carried out, and every other call found its pages."""
+        return self.pages_ws.status() == crg.GDN_OK == crg.gdn_paged_status(self.table.device)
 
     # ---------------------------------------------------------------- layers
 

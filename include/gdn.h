@@ -125,6 +125,12 @@ gdn_status gdn_workspace_path(const void *workspace, int32_t *path_out, void *st
  * check failed since the last reset. */
 gdn_status gdn_workspace_status(const void *workspace, int32_t *status_out, void *stream);
 
+/* 256 bytes of device memory that the library holds on the current device, 256-byte aligned, zero when
+ * it is loaded: a status word that outlives every workspace.  It serves as the `status` of a
+ * gdn_cache_shape or gdn_page_tables, and as the workspace of a call that needs 256 bytes; it is read and
+ * cleared like a workspace's. */
+gdn_status gdn_status_words(void **words);
+
 /* Gate prep of the Qwen3.5 GatedDeltaNet layer ("[v1] support GDN Ulysses
  * cp", What This PR Does: A_log and dt_bias are per-v-head parameters, a and
  * b per-token inputs):
@@ -360,8 +366,9 @@ gdn_status gdn_cu_seqlens_from_position_ids(const int64_t *position_ids, int64_t
  * never used, whatever it holds.
  *
  * Device-side checks: a length past max_pages * page_size, offsets that fall or leave
- * [0, n_tok], and a page outside [0, n_pages) set GDN_ERR_BOUNDS in the workspace's status
- * word and are not followed; the results of that sequence are then unspecified.
+ * [0, n_tok], and a page outside [0, n_pages) set GDN_ERR_BOUNDS in the status word (the
+ * workspace's first, or the one that the shape or tables name) and are not followed; the
+ * results of that sequence are then unspecified.
  * ------------------------------------------------------------------------------------ */
 
 typedef struct {
@@ -375,6 +382,7 @@ typedef struct {
   int64_t page_stride, slot_stride, head_stride; /* elements; all 0 = dense [n_pages, page_size, Hkv, D] */
   int64_t q_stride;     /* elements between consecutive tokens of q; 0 = dense (Hq * D) */
   int64_t k_stride, v_stride; /* of the new k and v (gdn_kv_append); 0 = dense (Hkv * D) */
+  int32_t *status;      /* device word for the status; NULL = the first of the workspace */
 } gdn_cache_shape;
 
 #define GDN_FLAG_ROPE_INTERLEAVED 128u /* pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2) */
@@ -464,13 +472,14 @@ gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cach
  * in rising order, so the results do not depend on scheduling.  The calls below check their
  * lists on the device: a row outside [0, n_rows), a list that cannot be carried out, or too
  * few free pages sets GDN_ERR_PAGES (a page outside the cache: GDN_ERR_BOUNDS) in the status
- * word of `workspace` (gdn_pages_workspace_bytes(n_pages, n_rows) bytes, 256-byte aligned), and
- * gdn_pages_grow and gdn_pages_fork then change nothing. */
+ * word, and gdn_pages_grow and gdn_pages_fork then change nothing.  workspace:
+ * gdn_pages_workspace_bytes(n_pages, n_rows) bytes, 256-byte aligned. */
 typedef struct {
   int32_t *page_table, *seq_lens, *refs; /* device */
   int32_t n_rows, max_pages;
   int64_t table_stride; /* elements between rows of page_table; 0 = max_pages */
   int32_t n_pages, page_size; /* n_pages < 2^21 */
+  int32_t *status;      /* device word for the status; NULL = the first of the workspace */
 } gdn_page_tables;
 
 /* The caches that the pages index: n_pools device arrays (a HOST array of their addresses, at
