@@ -40,6 +40,7 @@
 #include "conv_tap.cuh"
 #include "gates.cuh"
 #include "sm100.cuh"
+#include "tensor_map.cuh"
 
 using namespace gdn;
 using namespace gdn::sm100;
@@ -1180,19 +1181,6 @@ __global__ void __launch_bounds__(NTS, 1)
 }
 
 // ============================================================ host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
 
 }  // namespace
 

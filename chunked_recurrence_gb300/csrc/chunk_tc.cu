@@ -35,6 +35,7 @@
 
 #include "common.cuh"
 #include "sm100.cuh"
+#include "tensor_map.cuh"
 #include "chunk_common.cuh"
 
 using namespace gdn;
@@ -856,19 +857,6 @@ __global__ void __launch_bounds__(NT2, 1)
 }
 
 // ============================================================ host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
 
 // 3-D bf16 map over [n_tok][heads][width] with token stride `tok_stride` elements.
 bool make_map3(CUtensorMap *m, const void *base, int width, int heads, int64_t n_tok,

@@ -34,7 +34,6 @@
 // the first of these.  A few short sequences: some 13 us, the chain of launch, lengths, table, copies, S, P, O, then the
 // join's.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <numeric>
@@ -44,6 +43,7 @@
 #include "conv_tap.cuh"
 #include "paged_attn.cuh"
 #include "sm100.cuh"
+#include "tensor_map.cuh"
 
 namespace gdn {
 namespace {
@@ -1043,18 +1043,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blo
     if (to >= 0)
       for (int c = lane; c < D / 4; c += 32) *reinterpret_cast<uint2 *>(a.o + to * D + 4 * c) = rows[q][c];
   }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
 }
 
 // [page][head][slot][D] of a cache, boxes of 64 columns x `box` slots
