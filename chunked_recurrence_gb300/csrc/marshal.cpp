@@ -4,9 +4,11 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/Allocator.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <algorithm>
 #include <cstring>
 #include <tuple>
 #include <type_traits>
@@ -123,20 +125,32 @@ PyObject *like(PyObject *, PyObject *const *args, Py_ssize_t n) {
   }
 }
 
-template <typename... P, size_t... I>
+// Calls f.  SCRATCH: its workspace (the third last argument, its size the second last), where it is None, is memory of
+// the current stream for this call: given back as the call returns, for what the stream does next.
+template <bool SCRATCH, typename... P, size_t... I>
 gdn_status invoke(gdn_status (*f)(P...), PyObject *const *args, std::index_sequence<I...>) {
-  const std::tuple<P...> a{argument<P>(args[I])...};
+  std::tuple<P...> a{argument<P>(args[I])...};
+  at::DataPtr scratch;
+  if constexpr (SCRATCH) {
+    constexpr size_t kAt = sizeof...(P) - 3;
+    if (!std::get<kAt>(a)) {
+      size_t &bytes = std::get<kAt + 1>(a);
+      bytes = std::max<size_t>(bytes, 256);
+      scratch = c10::GetAllocator(c10::DeviceType::CUDA)->allocate(bytes);
+      std::get<kAt>(a) = scratch.get();
+    }
+  }
   PyThreadState *state = PyEval_SaveThread();
   const gdn_status st = f(std::get<I>(a)...);
   PyEval_RestoreThread(state);
   return st;
 }
 
-template <typename F>
+template <typename F, bool SCRATCH>
 struct Entry;
 // call(address of the library's function, its arguments) -> status
-template <typename... P>
-struct Entry<gdn_status(P...)> {
+template <typename... P, bool SCRATCH>
+struct Entry<gdn_status(P...), SCRATCH> {
   static PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 1 + (Py_ssize_t)sizeof...(P)) {
       PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
@@ -144,7 +158,7 @@ struct Entry<gdn_status(P...)> {
     }
     try {
       auto *f = (gdn_status(*)(P...))argument<void *>(args[0]);
-      return PyLong_FromLong(invoke(f, args + 1, std::index_sequence_for<P...>{}));
+      return PyLong_FromLong(invoke<SCRATCH>(f, args + 1, std::index_sequence_for<P...>{}));
     } catch (const PyRaised &) {
     } catch (const std::exception &e) {
       PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -157,18 +171,19 @@ PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f));
 }
 
-#define GDN_ENTRY(name) {#name, fast(Entry<decltype(name)>::call), METH_FASTCALL, "library call"}
+#define GDN_ENTRY(name) {#name, fast(Entry<decltype(name), false>::call), METH_FASTCALL, "library call"}
+#define GDN_ENTRY_SCRATCH(name) {#name, fast(Entry<decltype(name), true>::call), METH_FASTCALL, "library call"}
 PyMethodDef methods[] = {
     {"lays", fast(lays), METH_FASTCALL, "key of layouts"},
     {"like", fast(like), METH_FASTCALL, "new tensor"},
     {"pack", fast(pack), METH_FASTCALL, "struct of pointers and a tail"},
     GDN_ENTRY(gdn_rope),
     GDN_ENTRY(gdn_kv_append),
-    GDN_ENTRY(gdn_paged_attn),
-    GDN_ENTRY(gdn_pages_grow),
+    GDN_ENTRY_SCRATCH(gdn_paged_attn),
+    GDN_ENTRY_SCRATCH(gdn_pages_grow),
     GDN_ENTRY(gdn_pages_free),
-    GDN_ENTRY(gdn_pages_fork),
-    GDN_ENTRY(gdn_pages_compact),
+    GDN_ENTRY_SCRATCH(gdn_pages_fork),
+    GDN_ENTRY_SCRATCH(gdn_pages_compact),
     GDN_ENTRY(gdn_pages_copy),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_marshal", "paged operators' marshalling", -1, methods};

@@ -33,17 +33,14 @@ struct PlanWords {
 };
 
 struct Plan {
-  int32_t *status;
   PlanWords *w;
   int32_t *src, *dst, *to;  // [n_pages] each: moves, and compact's new page of each moved one
   int32_t *rows;            // [n_rows] lengths saved while a list is checked
 };
 
-__device__ Plan plan_of(void *workspace, const gdn_page_tables &t) {
+__device__ Plan plan_of(void *workspace, int32_t n_pages) {
   char *p = (char *)workspace;
-  const int32_t n_pages = t.n_pages;
   Plan r;
-  r.status = t.status ? t.status : (int32_t *)p;
   r.w = (PlanWords *)(p + 128);
   r.src = (int32_t *)(p + 256);
   r.dst = r.src + n_pages;
@@ -120,7 +117,7 @@ __device__ __forceinline__ int32_t *table_row(const gdn_page_tables &t, int s) {
 __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_tables t, const int32_t *seqs,
                                                             const int32_t *new_lens, int n, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t);
+  const Plan pl = plan_of(workspace, t.n_pages);
   grid_dependency_wait();
   bool bad = false;
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
@@ -166,33 +163,32 @@ __global__ void __launch_bounds__(kPlanThreads) grow_kernel(const gdn_page_table
     }
     taken += part;
   }
-  if (bad && threadIdx.x == 0) set_status(pl.status, GDN_ERR_PAGES);
+  if (bad && threadIdx.x == 0) set_status(t.status, GDN_ERR_PAGES);
 }
 
-__global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, const int32_t *seqs, void *workspace) {
+__global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, const int32_t *seqs) {
   __shared__ int s_len;
-  const Plan pl = plan_of(workspace, t);
   grid_dependency_wait();
   launch_dependents();
   const int s = seqs[blockIdx.x];
   if (s < 0 || s >= t.n_rows) {
-    if (threadIdx.x == 0) set_status(pl.status, GDN_ERR_PAGES);
+    if (threadIdx.x == 0) set_status(t.status, GDN_ERR_PAGES);
     return;
   }
   if (threadIdx.x == 0) s_len = atomicExch(&t.seq_lens[s], 0);  // a row named twice is empty the second time
   __syncthreads();
   const int64_t pages = ((int64_t)max(s_len, 0) + t.page_size - 1) / t.page_size;
-  if (pages > t.max_pages && threadIdx.x == 0) set_status(pl.status, GDN_ERR_BOUNDS);
+  if (pages > t.max_pages && threadIdx.x == 0) set_status(t.status, GDN_ERR_BOUNDS);
   int32_t *row = table_row(t, s);
   for (int i = threadIdx.x; i < min(pages, (int64_t)t.max_pages); i += blockDim.x) {
     const int page = row[i];
     row[i] = -1;
     if (page == -1) continue;
     if (page < 0 || page >= t.n_pages) {
-      set_status(pl.status, GDN_ERR_BOUNDS);
+      set_status(t.status, GDN_ERR_BOUNDS);
     } else if (atomicSub(&t.refs[page], 1) <= 0) {  // held by nobody: stays at 0
       atomicAdd(&t.refs[page], 1);
-      set_status(pl.status, GDN_ERR_PAGES);
+      set_status(t.status, GDN_ERR_PAGES);
     }
   }
 }
@@ -201,7 +197,7 @@ __global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, cons
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_tables t, const int32_t *parents,
                                                                  const int32_t *children, int n, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t);
+  const Plan pl = plan_of(workspace, t.n_pages);
   bool bad = false;
   grid_dependency_wait();
   launch_dependents();  // the moves' blocks wait for this one's end where they read
@@ -252,13 +248,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
   if (threadIdx.x == 0) {
     pl.w->ok = !bad;
     pl.w->n_moves = bad ? 0 : total;
-    if (bad) set_status(pl.status, GDN_ERR_PAGES);
+    if (bad) set_status(t.status, GDN_ERR_PAGES);
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const gdn_page_tables t, void *workspace) {
   __shared__ int sh[33];
-  const Plan pl = plan_of(workspace, t);
+  const Plan pl = plan_of(workspace, t.n_pages);
   grid_dependency_wait();
   launch_dependents();
   int live = 0;
@@ -321,7 +317,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
                                                             int64_t page_bytes, int64_t page_stride, void *workspace) {
   constexpr int kPer = 8;  // vectors a thread moves in one go, all loads before the first store
   grid_dependency_wait();  // for the plan
-  const Plan pl = plan_of(workspace, t);
+  const Plan pl = plan_of(workspace, t.n_pages);
   const int32_t *src = KIND == kCopy ? a : pl.src, *dst = KIND == kCopy ? b : pl.dst;
   int moves = n;
   if (KIND != kCopy) {
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
       const int page = table_row(t, a[j])[k];
       table_row(t, b[j])[k] = page;
       if (page >= 0 && page < t.n_pages) atomicAdd(&t.refs[page], 1);
-      else if (page != -1) set_status(pl.status, GDN_ERR_BOUNDS);
+      else if (page != -1) set_status(t.status, GDN_ERR_BOUNDS);
     }
   }
   if (KIND == kCompact) {
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
       const int page = *e;
       if (page < L) continue;  // stays, or -1
       if (page < t.n_pages) *e = pl.to[page];
-      else set_status(pl.status, GDN_ERR_BOUNDS);
+      else set_status(t.status, GDN_ERR_BOUNDS);
     }
   }
   const int64_t vecs = page_bytes / (int64_t)sizeof(V);
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
     const int m = (int)(mp / n_pools), pool = (int)(mp - (int64_t)m * n_pools);
     const int s = src[m], d = dst[m];
     if (KIND == kCopy && (s < 0 || d < 0 || s >= t.n_pages || d >= t.n_pages)) {
-      if (threadIdx.x == 0) set_status(pl.status, GDN_ERR_BOUNDS);
+      if (threadIdx.x == 0) set_status(t.status, GDN_ERR_BOUNDS);
       continue;
     }
     const V *from = (const V *)((const char *)pools.p[pool] + s * page_stride) + c * piece + threadIdx.x;
@@ -377,12 +373,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
   }
 }
 
-bool tables_ok(const gdn_page_tables *in, gdn_page_tables *t) {
+// The tables checked, strides and the status word filled in.
+bool tables_ok(const gdn_page_tables *in, void *workspace, gdn_page_tables *t) {
   if (!in) return false;
   *t = *in;
   if (t->n_rows < 0 || t->max_pages < 0 || t->n_pages < 0 || t->page_size < 1 || !aligned(t->status, sizeof(int32_t)))
     return false;
   if (t->table_stride == 0) t->table_stride = t->max_pages;
+  if (!t->status) t->status = (int32_t *)workspace;
   if (t->table_stride < t->max_pages || t->n_pages >= 1 << 21) return false;  // sums of 1024 rows' pages: 32 bits
   return (t->n_rows == 0 || (t->page_table && t->seq_lens)) && (t->n_pages == 0 || t->refs);
 }
@@ -442,7 +440,7 @@ extern "C" size_t gdn_pages_workspace_bytes(int32_t n_pages, int32_t n_rows) {
 extern "C" gdn_status gdn_pages_grow(const gdn_page_tables *tables, const int32_t *seqs, const int32_t *new_lens,
                                      int32_t n, void *workspace, size_t workspace_bytes, void *stream) {
   gdn_page_tables t;
-  if (!tables_ok(tables, &t) || n < 0 || n > t.n_rows) return GDN_ERR_INVALID_ARG;  // no row twice
+  if (!tables_ok(tables, workspace, &t) || n < 0 || n > t.n_rows) return GDN_ERR_INVALID_ARG;  // no row twice
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs || !new_lens) return GDN_ERR_INVALID_ARG;
@@ -453,11 +451,11 @@ extern "C" gdn_status gdn_pages_grow(const gdn_page_tables *tables, const int32_
 extern "C" gdn_status gdn_pages_free(const gdn_page_tables *tables, const int32_t *seqs, int32_t n, void *workspace,
                                      size_t workspace_bytes, void *stream) {
   gdn_page_tables t;
-  if (!tables_ok(tables, &t) || n < 0) return GDN_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
+  if (!tables_ok(tables, workspace, &t) || n < 0) return GDN_ERR_INVALID_ARG;
+  if (!tables->status && !ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs) return GDN_ERR_INVALID_ARG;
-  launch_early(free_kernel, n, 256, (cudaStream_t)stream, t, seqs, workspace);
+  launch_early(free_kernel, n, 256, (cudaStream_t)stream, t, seqs);
   return launch_status();
 }
 
@@ -466,7 +464,7 @@ extern "C" gdn_status gdn_pages_fork(const gdn_page_tables *tables, const int32_
                                      void *stream) {
   gdn_page_tables t;
   Pools p{};
-  if (!tables_ok(tables, &t) || n < 0 || n > t.n_rows) return GDN_ERR_INVALID_ARG;
+  if (!tables_ok(tables, workspace, &t) || n < 0 || n > t.n_rows) return GDN_ERR_INVALID_ARG;
   const gdn_status ok = pools_ok(pools, &p);
   if (ok != GDN_OK) return ok;
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
@@ -482,7 +480,7 @@ extern "C" gdn_status gdn_pages_compact(const gdn_page_tables *tables, const gdn
                                         size_t workspace_bytes, void *stream) {
   gdn_page_tables t;
   Pools p{};
-  if (!tables_ok(tables, &t)) return GDN_ERR_INVALID_ARG;
+  if (!tables_ok(tables, workspace, &t)) return GDN_ERR_INVALID_ARG;
   const gdn_status ok = pools_ok(pools, &p);
   if (ok != GDN_OK) return ok;
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
@@ -504,6 +502,6 @@ extern "C" gdn_status gdn_pages_copy(const int32_t *src, const int32_t *dst, int
   if (n == 0) return GDN_OK;
   if (!src || !dst) return GDN_ERR_INVALID_ARG;
   gdn_page_tables t{};
-  t.n_pages = n_pages;
+  t.n_pages = n_pages, t.status = (int32_t *)workspace;
   return launch_moves<kCopy>(t, src, dst, n, *pools, p, workspace, (cudaStream_t)stream);
 }

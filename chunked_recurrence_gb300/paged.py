@@ -14,8 +14,8 @@ import torch
 
 from . import build as _build
 from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT, GDN_FLAG_TEST_NO_WAIT,
-               GDN_MAX_POOLS, GDN_ROPE_SCALING, GdnCacheShape, GdnPagePools, GdnPageTables, Workspace, _check,
-               _dtype_code, _need_cuda, _ptr, _stream, _ws_cache, load)
+               GDN_MAX_POOLS, GDN_ROPE_SCALING, GdnCacheShape, GdnPagePools, GdnPageTables, _check, _dtype_code,
+               _need_cuda, _ptr, _stream, load)
 
 
 def _load_marshal():
@@ -63,10 +63,14 @@ def _plan(key, make):
 
 
 _entries = {}
+_TAKE_SCRATCH = ("gdn_paged_attn", "gdn_pages_grow", "gdn_pages_fork", "gdn_pages_compact")
 
 
 def _entry(name):
-    """The library's function of this name, taking tensors, bytes, addresses or None for pointers."""
+    """The library's function of this name, taking tensors, bytes, addresses or None for pointers.  Those that take
+    scratch get it from the allocator where their workspace is None: memory of the current stream for this call alone,
+    for calls of several threads enqueue their kernels between each other's, and a captured graph goes on using what it
+    was captured with."""
     f = _entries.get(name)
     if f is None:
         fn = getattr(load(), name)
@@ -74,6 +78,9 @@ def _entry(name):
             f = functools.partial(getattr(_marshal, name), ctypes.cast(fn, ctypes.c_void_p).value)
         else:
             def f(*args):
+                if args[-3] is None and name in _TAKE_SCRATCH:
+                    scratch = torch.empty(max(256, args[-2]), dtype=torch.uint8, device="cuda")
+                    args = (*args[:-3], scratch, scratch.numel(), args[-1])
                 return fn(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args])
         _entries[name] = f
     return f
@@ -263,19 +270,18 @@ def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=No
                          0 if v is None else _heads("v", v, D))
 
 
-def _own_workspace(kind, nbytes, t, stream):
-    """A workspace of this kind for calls on this device and stream, which run one after another."""
-    handle = _handle(t, stream)
-    key = (kind, t.get_device(), handle)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.nbytes < nbytes:
-        if stream is None:
-            ws = Workspace(nbytes, t.device)
-        else:  # cleared on the stream that uses it
-            with torch.cuda.stream(_as_stream(t, stream)):
-                ws = Workspace(nbytes, t.device)
-        _ws_cache[key] = ws
-    return ws, handle
+def _call(name, t, nbytes, workspace, stream, *args):
+    """A library call with a workspace or with scratch of its own: its arguments up to that."""
+    buf = None
+    if workspace is not None:
+        buf, nbytes = workspace.buf, workspace.nbytes
+    if stream is None:
+        st = _entry(name)(*args, buf, nbytes, _handle(t, None))
+    else:
+        with torch.cuda.stream(_as_stream(t, stream)):
+            st = _entry(name)(*args, buf, nbytes, _handle(t, stream))
+    if st:
+        _check(st, name)
 
 
 def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, q=None, freqs=None,
@@ -333,18 +339,15 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
         return sh, ctypes.addressof(sh), new, gdn_paged_attn_workspace_bytes(sh, new), sh.D ** -0.5
 
     _, shape, new, nbytes, unit = _plan(
-        ("attn", max_new, workspace is None, _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
+        ("attn", max_new, workspace is None,
+         _lays(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)), make)
     if o is None:
         o = _empty(q, 3, False, stream)
     if lse is None and want_lse:
         lse = _empty(q, 2, True, stream)
-    ws, handle = ((workspace, _handle(q, stream)) if workspace is not None
-                  else _own_workspace("attn", nbytes, q, stream))
     flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
-    st = _entry("gdn_paged_attn")(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, shape, new,
-                                  unit if scale is None else scale, window, flags, o, lse, ws.buf, ws.nbytes, handle)
-    if st:
-        _check(st, "gdn_paged_attn")
+    _call("gdn_paged_attn", q, nbytes, workspace, stream, q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, shape,
+          new, unit if scale is None else scale, window, flags, o, lse)
     return o, lse
 
 
@@ -377,7 +380,8 @@ def _page_tables(page_table, seq_lens, refs, page_size, workspace, names=(), *li
                           None if workspace is not None else _status_words(page_table.get_device()))
         return bytes(t)[3 * ctypes.sizeof(ctypes.c_void_p):], n, gdn_pages_workspace_bytes(n_pages, n_rows)
 
-    tail, n, nbytes = _plan(("tables", page_size, names, workspace is None, _lays(page_table, seq_lens, refs, *lists)), make)
+    tail, n, nbytes = _plan(
+        ("tables", page_size, names, workspace is None, _lays(page_table, seq_lens, refs, *lists)), make)
     return _pack(tail, page_table, seq_lens, refs), n, nbytes
 
 
@@ -408,30 +412,18 @@ def _page_pools(pools, n_pages):
     return _pack(tail, at), at
 
 
-def _pages_workspace(nbytes, t, workspace, stream):
-    if workspace is not None:
-        return workspace, _handle(t, stream)
-    return _own_workspace("pages", nbytes, t, stream)
-
-
 def gdn_pages_grow(page_table, seq_lens, refs, seqs, new_lens, page_size, workspace=None, stream=None):
     """Sequences `seqs` grow to `new_lens` tokens (device int32 lists): missing pages come from the free
     ones in rising order.  Nothing changes, the lengths included, if they do not suffice: GDN_ERR_PAGES in
     the status of the workspace, or of gdn_paged_status without one."""
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs", "new_lens"), seqs, new_lens)
-    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_grow")(t, seqs, new_lens, n, ws.buf, ws.nbytes, handle)
-    if st:
-        _check(st, "gdn_pages_grow")
+    _call("gdn_pages_grow", page_table, nbytes, workspace, stream, t, seqs, new_lens, n)
 
 
 def gdn_pages_free(page_table, seq_lens, refs, seqs, page_size, workspace=None, stream=None):
     """Sequences `seqs` give their pages back and become empty."""
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs",), seqs)
-    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_free")(t, seqs, n, ws.buf, ws.nbytes, handle)
-    if st:
-        _check(st, "gdn_pages_free")
+    _call("gdn_pages_free", page_table, nbytes, workspace, stream, t, seqs, n)
 
 
 def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_size, workspace=None, stream=None):
@@ -441,20 +433,14 @@ def gdn_pages_fork(page_table, seq_lens, refs, parents, children, pools, page_si
     t, n, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("parents", "children"), parents,
                                 children)
     p, _keep = _page_pools(pools, refs.shape[0])
-    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_fork")(t, parents, children, n, p, ws.buf, ws.nbytes, handle)
-    if st:
-        _check(st, "gdn_pages_fork")
+    _call("gdn_pages_fork", page_table, nbytes, workspace, stream, t, parents, children, n, p)
 
 
 def gdn_pages_compact(page_table, seq_lens, refs, pools, page_size, workspace=None, stream=None):
     """The live pages come together at the start of the pools; tables and refs follow."""
     t, _, nbytes = _page_tables(page_table, seq_lens, refs, page_size, workspace)
     p, _keep = _page_pools(pools, refs.shape[0])
-    ws, handle = _pages_workspace(nbytes, page_table, workspace, stream)
-    st = _entry("gdn_pages_compact")(t, p, ws.buf, ws.nbytes, handle)
-    if st:
-        _check(st, "gdn_pages_compact")
+    _call("gdn_pages_compact", page_table, nbytes, workspace, stream, t, p)
 
 
 def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):

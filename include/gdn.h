@@ -473,7 +473,8 @@ gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cach
  * lists on the device: a row outside [0, n_rows), a list that cannot be carried out, or too
  * few free pages sets GDN_ERR_PAGES (a page outside the cache: GDN_ERR_BOUNDS) in the status
  * word, and gdn_pages_grow and gdn_pages_fork then change nothing.  workspace:
- * gdn_pages_workspace_bytes(n_pages, n_rows) bytes, 256-byte aligned. */
+ * gdn_pages_workspace_bytes(n_pages, n_rows) bytes, 256-byte aligned (gdn_pages_free with a
+ * status word in its tables takes NULL). */
 typedef struct {
   int32_t *page_table, *seq_lens, *refs; /* device */
   int32_t n_rows, max_pages;
