@@ -9,7 +9,7 @@
 //
 // Copying is bound by HBM: a moved byte is read once and written once (1.14 GB read and written to bring the pages of a
 // half-empty cache together: 181 us, 94% of a copy's rate).  Small calls are launches and the plan's chain of loads:
-// freeing and forking 24 of 48 sequences 13 us, 5 of them the plan.  No page is both read and written by one call
+// freeing and forking 24 of 48 sequences 14 us, 6 of them the plan.  No page is both read and written by one call
 // (compact moves pages at or past L into free ones below it; fork's new pages were free), so the copies run in any
 // order.
 #include <algorithm>
@@ -26,6 +26,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
+// Entries of a fork's parents' rows that the plan looks through itself (1128: 8.6 us a fork, 8.9 and a launch more with a
+// kernel for it; 4096: 9.9 and 8.9; unchecked 7.4 and 7.6).
+constexpr int kPlanEntries = 2048;
 
 // Words of the workspace after the 256 bytes that hold the status.
 struct PlanWords {
@@ -193,7 +196,32 @@ __global__ void __launch_bounds__(256) free_kernel(const gdn_page_tables t, cons
   }
 }
 
-// fork: checks the pairs, takes the new pages and lists the copies; move_kernel writes the rows.
+// Whether a fork's parent cannot give entry k of its row: a page outside the cache, or none where it has a part-filled
+// one (a full page may have been given back, -1).  Rows and lengths that cannot be are found by the plan.
+__device__ __forceinline__ bool bad_entry(const gdn_page_tables &t, int parent, int k) {
+  const int len = parent >= 0 && parent < t.n_rows ? __ldcg(&t.seq_lens[parent]) : -1;
+  const int full = len / t.page_size, part = len % t.page_size;
+  if (len < 0 || k > full || (k == full && !part)) return false;
+  const int page = table_row(t, parent)[k];
+  if (page < -1 || page >= t.n_pages) return set_status(t.status, GDN_ERR_BOUNDS), true;
+  return page == -1 && k == full;
+}
+
+// A parent's entries, a block a parent: rows[i] says whether one is bad.
+__global__ void __launch_bounds__(256) fork_check_kernel(const gdn_page_tables t, const int32_t *parents, void *workspace) {
+  const Plan pl = plan_of(workspace, t.n_pages);
+  grid_dependency_wait();
+  launch_dependents();
+  const int p = parents[blockIdx.x];
+  bool bad = false;
+  for (int k = threadIdx.x; k < t.max_pages; k += blockDim.x) bad = bad_entry(t, p, k) || bad;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) pl.rows[blockIdx.x] = bad;
+}
+
+// fork: checks the pairs (and the parents' entries, unless fork_check_kernel has), takes the new pages and lists the
+// copies; move_kernel writes the rows.
+template <bool CHECKED>
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_tables t, const int32_t *parents,
                                                                  const int32_t *children, int n, void *workspace) {
   __shared__ int sh[33];
@@ -205,18 +233,19 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const gdn_page_
     const int c = children[i];
     int old = -1;
     if (c >= 0 && c < t.n_rows) old = atomicExch(&t.seq_lens[c], -1);
+    if (CHECKED) bad = bad || pl.rows[i];
     pl.rows[i] = old;
     bad = bad || old != 0;
   }
+  // no barrier before: a parent that is claimed by now is refused below
+#pragma unroll 2
+  for (int i = threadIdx.x; !CHECKED && i < n * t.max_pages; i += kPlanThreads)
+    bad = bad_entry(t, parents[i / t.max_pages], i % t.max_pages) || bad;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int p = parents[i];  // a parent that is a child too has been claimed
     const int len = p >= 0 && p < t.n_rows ? *(volatile int32_t *)&t.seq_lens[p] : -1;
     bad = bad || len < 0 || len > (int64_t)t.max_pages * t.page_size;
-    if (!bad && len % t.page_size) {
-      const int page = table_row(t, p)[len / t.page_size];
-      bad = page < 0 || page >= t.n_pages;
-    }
   }
   bad = __syncthreads_or(bad);
   int total = 0;
@@ -332,8 +361,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
       if (k >= len / t.page_size) continue;  // the new page of a part-filled one is in place
       const int page = table_row(t, a[j])[k];
       table_row(t, b[j])[k] = page;
-      if (page >= 0 && page < t.n_pages) atomicAdd(&t.refs[page], 1);
-      else if (page != -1) set_status(t.status, GDN_ERR_BOUNDS);
+      if (page >= 0) atomicAdd(&t.refs[page], 1);
     }
   }
   if (KIND == kCompact) {
@@ -471,7 +499,12 @@ extern "C" gdn_status gdn_pages_fork(const gdn_page_tables *tables, const int32_
   if (n == 0) return GDN_OK;
   if (!parents || !children) return GDN_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  launch_early(fork_plan_kernel, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
+  if ((int64_t)n * t.max_pages <= kPlanEntries) {
+    launch_early(fork_plan_kernel<false>, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
+  } else {
+    launch_early(fork_check_kernel, n, 256, st, t, parents, workspace);
+    launch_early(fork_plan_kernel<true>, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
+  }
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   return launch_moves<kFork>(t, parents, children, n, *pools, p, workspace, st);
 }
