@@ -17,6 +17,9 @@
 // instead and join at the end.  A running maximum and sum per row, in base 2.  P's accumulator layout serves as the
 // second product's operand by taking V's rows in the order 0 2 4 6 1 3 5 7 of each eight.
 // Positions that no row of the block sees are zeros in shared memory; a masked weight is an exact 0.
+// Infinities and NaN: an infinite operand's parts are (inf, NaN), a masked 0 times one is NaN, and a row keeps a NaN to the
+// end.  A block that ends with one (or with an infinity) works its rows out again in plain fp32, position by position of
+// those that a row sees.
 #include <algorithm>
 
 #include "chunk_bwd_mma.cuh"
@@ -42,6 +45,66 @@ struct Cfg {
   static constexpr int kTile = BN * kPitch;
   static constexpr size_t kSmem = sizeof(float) * (R * kPitch + 4 * kTile) + 2 * BN * sizeof(int64_t);
 };
+
+// A row's values out: o / l and lse, or the part for the join.
+__device__ __forceinline__ void put_stats(const SimtArgs &a, int64_t row, float top, float sum) {
+  if (a.part) {
+    float *pp = a.part + ((int64_t)blockIdx.z * a.seqs.n_tok * a.Hq + row) * (a.D + 2);
+    pp[0] = top, pp[1] = sum;
+  } else if (a.lse) {
+    a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put(const SimtArgs &a, int64_t row, int col, float x, float inv) {
+  if (col >= a.D) return;
+  if (a.part) a.part[((int64_t)blockIdx.z * a.seqs.n_tok * a.Hq + row) * (a.D + 2) + 2 + col] = x;
+  else ((T *)a.o)[row * a.D + col] = from_f32<T>(x * inv);
+}
+
+// A block's R rows in plain fp32 on the CUDA cores, a warp a row, a lane holding the elements lane, lane + 32, ...  Apart
+// from the kernel, whose registers it would crowd (bf16 of D 96, 10 chunks of 150 over 600: 215 us, 272 in line), and
+// working out its item again, which the kernel then need not keep in memory.
+template <typename T, int DP>
+__device__ __noinline__ void plain_rows(const SimtArgs &a, int R) {
+  constexpr int kE = DP / 32;
+  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv, h = blockIdx.y;
+  const Item it = item_at(a.seqs, blockIdx.x, G, R, 1, a.window);
+  const int begin = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z, a.splits);
+  const int end = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z + 1, a.splits);
+  const int32_t *table = a.table + (int64_t)it.s * a.table_stride;
+  for (int r = threadIdx.x >> 5; r < it.rows; r += kThreads / 32) {
+    const int row = it.row0 + r, tok = row / G, p = it.first + tok;
+    const T *qp = (const T *)a.q + (int64_t)(it.t0 + tok) * a.q_stride + (int64_t)(h * G + row - tok * G) * a.D;
+    float q[kE], acc[kE], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) q[e] = lane + 32 * e < a.D ? to_f32<T>(qp[lane + 32 * e]) : 0.f, acc[e] = 0.f;
+    for (int j = a.window > 0 && p >= a.window ? max(p - a.window + 1, begin) : begin; j < min(p + 1, end); ++j) {
+      const int page = page_of(table, j, a.page_size, a.max_pages, a.n_pages);
+      if (page < 0) continue;
+      const int64_t at = (int64_t)page * a.page_stride + (int64_t)(j % a.page_size) * a.slot_stride +
+                         (int64_t)h * a.head_stride + lane;
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (lane + 32 * e < a.D) x = fmaf(q[e], to_f32<T>(((const T *)a.k)[at + 32 * e]), x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      x *= a.scale_log2;
+      const float up = fmaxf(top, x), keep = top == -INFINITY ? 0.f : exp2f(top - up);
+      const float w = x == -INFINITY ? 0.f : exp2f(x - up);
+      top = up, sum = sum * keep + w;
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (lane + 32 * e < a.D) acc[e] = fmaf(acc[e], keep, w * to_f32<T>(((const T *)a.v)[at + 32 * e]));
+    }
+    const int64_t out = (int64_t)(it.t0 + tok) * a.Hq + h * G + row - tok * G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (lane == 0) put_stats(a, out, top, sum);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) put<T>(a, out, lane + 32 * e, acc[e], inv);
+  }
+}
 
 template <typename T, int DP, bool FEW>
 __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs a, bool wide) {
@@ -232,24 +295,19 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
   }
 
-  // a row's values out: o / l and lse, or the part for the join
   auto out_row = [&](int r) {
     const int row = it.row0 + r, tok = row / G;
     return (int64_t)(it.t0 + tok) * a.Hq + h * G + row - tok * G;
   };
-  auto put_stats = [&](int64_t row, float top, float sum) {
-    if (a.part) {
-      float *pp = a.part + ((int64_t)part * a.seqs.n_tok * a.Hq + row) * (a.D + 2);
-      pp[0] = top, pp[1] = sum;
-    } else if (a.lse) {
-      a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  float odd = 0.f;  // NaN where a row of the item's has a NaN or an infinity
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (m0 + g4 + 8 * e < it.rows) {
+      odd = fmaf(l[e], 0.f, odd);
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) odd = fmaf(o[i][2 * e], 0.f, fmaf(o[i][2 * e + 1], 0.f, odd));
     }
-  };
-  auto put = [&](int64_t row, int col, float x, float inv) {
-    if (col >= a.D) return;
-    if (a.part) a.part[((int64_t)part * a.seqs.n_tok * a.Hq + row) * (a.D + 2) + 2 + col] = x;
-    else ((T *)a.o)[row * a.D + col] = from_f32<T>(x * inv);
-  };
+  if (__syncthreads_or(isnan(odd))) return plain_rows<T, DP>(a, C::R);
   if constexpr (!FEW) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -257,11 +315,11 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
       if (r >= it.rows) continue;
       const int64_t row = out_row(r);
       const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-      if (t4 == 0) put_stats(row, m[e], l[e]);
+      if (t4 == 0) put_stats(a, row, m[e], l[e]);
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i) {
-        put(row, i * 8 + 2 * t4, o[i][2 * e], inv);
-        put(row, i * 8 + 2 * t4 + 1, o[i][2 * e + 1], inv);
+        put<T>(a, row, i * 8 + 2 * t4, o[i][2 * e], inv);
+        put<T>(a, row, i * 8 + 2 * t4 + 1, o[i][2 * e + 1], inv);
       }
     }
   } else {
@@ -292,12 +350,12 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
       }
       const int64_t row = out_row(r);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (lane == 0) put_stats(row, top, sum);
+      if (lane == 0) put_stats(a, row, top, sum);
       for (int col = lane; col < a.D; col += 32) {
         float x = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x += w[i] == 0.f ? 0.f : w[i] * acc[(i * 16 + r) * C::kPitch + col];
-        put(row, col, x, inv);
+        put<T>(a, row, col, x, inv);
       }
     }
   }

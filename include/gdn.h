@@ -459,8 +459,8 @@ gdn_status gdn_kv_append(const void *q, const void *k, const void *v, const int6
  *   everything else: products of fp32's precision on the tensor cores (each operand in two TF32 parts);
  *   GDN_FLAG_SIMT: fp32 on the CUDA cores.
  * Slots at or past seq_lens, and positions that no query of a tile sees, reach nothing whatever they hold.
- * On the first two an infinity or NaN in v at a position that some query of the tile sees may reach the
- * tile's other queries (0 * inf); with GDN_FLAG_SIMT it reaches only those that see it. */
+ * Infinities and NaN in q, k and v reach the queries that see them, as the sums say.  On the first kernel one in v
+ * at a position that some query of a tile sees may also reach that tile's other queries (0 * inf), all of one sequence. */
 size_t gdn_paged_attn_workspace_bytes(const gdn_cache_shape *shape, int32_t max_new);
 gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *page_table,
                           const int32_t *seq_lens, const int32_t *cu_seqlens, const gdn_cache_shape *shape,
