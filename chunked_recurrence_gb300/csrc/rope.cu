@@ -5,9 +5,9 @@
 //     y1 = s (x1 cos a - x2 sin a),   y2 = s (x2 cos a + x1 sin a);
 // the gradient is the transposed rotation, the same with sin a negated.
 //
-// The angle is kept in turns as a 64-bit fraction: p * freq mod 2^64, one integer multiply,
-// exact for every 64-bit position, of which the top 32 bits are used.  A product in fp32 would be
-// off by p * 2^-25 rad.
+// The angle is kept in turns as a 64-bit fraction: p * freq mod 2^64, one integer multiply, exact for
+// every 64-bit position, of which the top 32 bits are used; freq itself is rounded, by 2^-65 turns at most
+// (p * 2^-65 in the angle).  A product in fp32 would be off by p * 2^-25 rad.
 //
 // Bound by HBM: every element is read and written once.  A warp takes a token: it works out
 // the token's cos and sin once for all heads (through its own piece of shared memory, no block
@@ -302,13 +302,34 @@ extern "C" gdn_status gdn_rope_inv_freq(int32_t rotary_dim, double base, int32_t
   return GDN_OK;
 }
 
+namespace {
+
+// 1 / 2 pi as a binary fraction, 192 bits in words from the lowest (pi by Machin's formula in whole numbers).
+constexpr uint64_t kTurn[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+
+// inv / 2 pi as a 64-bit fraction, rounded to nearest: inv = m 2^e with a whole m of 53 bits and e <= 0, and m / 2 pi to
+// 192 bits after the point (243 in all), so that what is cut off stays below 2^-75 of the result's last bit.
+uint64_t turns_word(double inv) {
+  int e;
+  const uint64_t m = (uint64_t)ldexp(frexp(fabs(inv), &e), 53);
+  uint64_t p[5] = {};
+  unsigned __int128 c = 0;
+  for (int i = 0; i < 3; ++i, c >>= 64) c += (unsigned __int128)m * kTurn[i], p[i] = (uint64_t)c;
+  p[3] = (uint64_t)c;
+  const int at = 128 - (e - 53), i = at / 64, b = at % 64;  // the result is bits [at, at + 64) of p
+  if (at > 255) return 0;
+  const uint64_t half = p[(at - 1) / 64] >> ((at - 1) % 64) & 1;
+  const uint64_t w = (p[i] >> b | (b ? p[i + 1] << (64 - b) : 0)) + half;
+  return inv < 0 ? 0 - w : w;
+}
+
+}  // namespace
+
 extern "C" gdn_status gdn_rope_freqs(const double *inv_freq, int32_t n, uint64_t *freqs) {
   if (n < 0 || (n > 0 && (!inv_freq || !freqs))) return GDN_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i) {
-    if (!isfinite(inv_freq[i])) return GDN_ERR_INVALID_ARG;
-    // the fraction of a turn, exact in double; +1/2 is the same angle as -1/2, which fits the word
-    const double turns = remainder(inv_freq[i] / (2 * M_PI), 1.0);
-    freqs[i] = turns >= 0.5 ? 1ull << 63 : (uint64_t)llrint(ldexp(turns, 64));
+    if (!(fabs(inv_freq[i]) < 0x1p53)) return GDN_ERR_INVALID_ARG;  // nor NaN
+    freqs[i] = turns_word(inv_freq[i]);
   }
   return GDN_OK;
 }

@@ -405,9 +405,10 @@ gdn_status gdn_rope_inv_freq(int32_t rotary_dim, double base, int32_t scaling, d
                              double alpha, double beta, double *inv_freq);
 
 /* The table that gdn_rope and gdn_kv_append read, on the HOST: each frequency in turns a
- * position as a 64-bit fixed-point fraction, round(inv / 2 pi * 2^64) mod 2^64.  A position
- * times it, mod 2^64, is the angle to 2^-64 turns a position whatever the position, which a
- * product in fp32 loses (0.06 rad at position 10^6).  Copy the n words to the device once. */
+ * position as a 64-bit fixed-point fraction, round(inv / 2 pi * 2^64) mod 2^64 with the 2 pi of
+ * mathematics (|inv| < 2^53).  A position times it, mod 2^64, is the angle to 2^-65 turns a position
+ * (2 * 10^-13 rad at position 10^6, where a product in fp32 is 0.06 off).  Copy the n words to the
+ * device once. */
 gdn_status gdn_rope_freqs(const double *inv_freq, int32_t n, uint64_t *freqs);
 
 /* Rotary positions of q and k: for each token t, head and pair i < rotary_dim / 2, with
