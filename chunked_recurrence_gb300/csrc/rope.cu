@@ -341,6 +341,7 @@ extern "C" gdn_status gdn_rope(const void *q, const void *k, const int64_t *posi
   if ((dtype != GDN_F32 && dtype != GDN_BF16) || n_tok < 0 || Hq < 0 || Hk < 0 || !rotary_ok(D, rotary_dim))
     return GDN_ERR_INVALID_ARG;
   if (flags & ~(uint32_t)(GDN_FLAG_ROPE_INTERLEAVED | GDN_FLAG_ROPE_BACKWARD)) return GDN_ERR_INVALID_ARG;
+  if (((int64_t)Hq + Hk) * D >= 1 << 29) return GDN_ERR_UNSUPPORTED;  // places and bytes within a token: 32 bits
   RopeArgs a{};
   a.qs = q_stride ? q_stride : (int64_t)Hq * D;
   a.ks = k_stride ? k_stride : (int64_t)Hk * D;

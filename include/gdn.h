@@ -420,7 +420,7 @@ gdn_status gdn_rope_freqs(const double *inv_freq, int32_t n, uint64_t *freqs);
  *   q: [n_tok, Hq, D], k: [n_tok, Hk, D] of dtype (Hq or Hk may be 0), token strides in
  *   elements, 0 = dense, the same for the outputs;  positions: [n_tok] int64;
  *   freqs: [rotary_dim / 2] device words of gdn_rope_freqs.  q_out may be q and k_out may be
- *   k (with equal strides); otherwise nothing overlaps.  Arithmetic in fp32. */
+ *   k (with equal strides); otherwise nothing overlaps.  (Hq + Hk) D < 2^29.  Arithmetic in fp32. */
 gdn_status gdn_rope(const void *q, const void *k, const int64_t *positions, const uint64_t *freqs, int32_t dtype,
                     int32_t n_tok, int32_t Hq, int32_t Hk, int32_t D, int32_t rotary_dim, int64_t q_stride,
                     int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, float scale, uint32_t flags,

@@ -82,3 +82,14 @@ def test_turns_at_far_positions(inter):
             y1, y2 = (out[t, 0, 2 * i], out[t, 0, 2 * i + 1]) if inter else (out[t, 0, i], out[t, 0, 32 + i])
             assert abs(y1.item() - (math.cos(a) - math.sin(a))) <= 2.0 ** -21 + 2 * angle_off, (p, i)
             assert abs(y2.item() - (math.cos(a) + math.sin(a))) <= 2.0 ** -21 + 2 * angle_off, (p, i)
+
+
+def test_tokens_too_wide_are_refused():
+    """Places within a token are 32-bit numbers in the kernel."""
+    fake = ctypes.c_void_p(0x10000)  # never dereferenced
+    crg.load()
+
+    def call(Hq, Hk, D):
+        return crg.load().gdn_rope(fake, fake, fake, fake, 1, 1, Hq, Hk, D, 2, 0, 0, 0, 0, 1.0, 0, fake, fake, None)
+    for Hq, Hk, D in ((1 << 24, 0, 128), (1 << 22, 1 << 22, 64), (0, 2 ** 31 - 1, 1), (2 ** 31 - 1, 2 ** 31 - 1, 256)):
+        assert call(Hq, Hk, max(D, 2)) == 2, (Hq, Hk, D)
