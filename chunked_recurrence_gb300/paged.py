@@ -197,8 +197,15 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     """Rotary positions of q [n_tok, Hq, D] and k [n_tok, Hk, D] (either may be None) over the first
     2 * len(freqs) elements of each head, times scale there; positions int64 [n_tok].  backward=True
     takes gradients of the outputs to those of the inputs.  q_out / k_out may be q / k.
-    Returns (q_out, k_out)."""
+    Returns (q_out, k_out), with gradients where q or k has them (then without q_out and k_out)."""
     x = q if q is not None else k
+    if ((q is not None and q.requires_grad) or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out take no gradients: leave them out, or call under torch.no_grad()")
+        if stream is None:
+            return _Rope.apply(q, k, positions, freqs, interleaved, scale, backward)
+        with torch.cuda.stream(_as_stream(x, stream)):  # the gradients then come on that stream too
+            return _Rope.apply(q, k, positions, freqs, interleaved, scale, backward)
 
     def make():
         _need_cuda(q, k, positions, freqs, q_out, k_out)
@@ -228,6 +235,24 @@ def gdn_rope(q, k, positions, freqs, interleaved=False, scale=1.0, backward=Fals
     if st:
         _check(st, "gdn_rope")
     return q_out, k_out
+
+
+class _Rope(torch.autograd.Function):
+    """gdn_rope with its gradient: the transposed rotation of the outputs' gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, interleaved, scale, backward):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions, freqs)
+        ctx.how = interleaved, scale, not backward
+        return gdn_rope(q, k, positions, freqs, interleaved, scale, backward)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        dq, dk = (t.contiguous() if t is not None and need else None for t, need in zip((dq, dk), ctx.needs_input_grad))
+        if dq is not None or dk is not None:
+            dq, dk = gdn_rope(dq, dk, *ctx.saved_tensors, *ctx.how)
+        return dq, dk, None, None, None, None, None
 
 
 def cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, k=None, v=None) -> GdnCacheShape:
@@ -289,7 +314,7 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     """The new tokens' k, v [n_tok, Hkv, D] into the cache at the end of their sequences (seq_lens counts
     them already), k rotated on the way with freqs, and q [n_tok, Hq, D] rotated into q_out (a new
     tensor, or q itself).  positions int64 [n_tok] replaces the places in the sequences as rotary
-    positions.  Returns q_out (None without q)."""
+    positions.  Returns q_out (None without q), without gradients."""
 
     def make():
         _need_cuda(q, k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens, freqs, positions, q_out)
@@ -324,7 +349,7 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
     """Attention of the new tokens q [n_tok, Hq, D] over the paged cache, which holds their k and v already:
     the token at position p of its sequence sees the last `window` positions up to p (0: all).
     max_new: a bound on the new tokens of one sequence (default: all of them).  Returns
-    (o [n_tok, Hq, D], lse [n_tok, Hq] fp32 or None)."""
+    (o [n_tok, Hq, D], lse [n_tok, Hq] fp32 or None), without gradients."""
 
     def make():
         _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
