@@ -15,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libgdn.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
-MARSHAL = os.path.join(OUT_DIR, "gdn_marshal.so")
+MARSHAL = os.path.join(OUT_DIR, "gdn_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))  # this interpreter's
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -56,8 +57,6 @@ def flags(extra=()):
 
 def _build_marshal(verbose: bool = False):
     """The binding's C++ module; without torch's headers or a C++ compiler it is left out."""
-    import sysconfig
-
     try:
         import torch
     except ImportError:
@@ -87,6 +86,8 @@ def _build_marshal(verbose: bool = False):
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile every csrc/*.cu for sm_103a and link libgdn.so; returns its path."""
     if not force and not _stale():
+        if not os.path.exists(MARSHAL):
+            _build_marshal(verbose)
         return LIB
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)

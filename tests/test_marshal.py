@@ -57,3 +57,11 @@ def test_entry_converts_like_the_library():
         crg.load().gdn_pages_copy(None, None, 1, 4, None, None, 0, 0) != 0
     with pytest.raises(OverflowError):
         paged._entry("gdn_pages_copy")(None, None, 1 << 40, 4, None, None, 0, 0)
+
+
+def test_the_module_is_this_interpreters():
+    """Its name carries the interpreter's tag, so that another Python does not load it."""
+    import sysconfig
+    from chunked_recurrence_gb300 import build
+    assert build.MARSHAL.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and "cpython" in build.MARSHAL
+    assert paged._marshal is None or paged._marshal.__file__ == build.MARSHAL
