@@ -344,11 +344,21 @@ class Workspace:
 _ws_cache = {}
 
 
-def _workspace_for(nbytes, device):
-    key = (str(device), nbytes)
+def _workspace_for(nbytes, t, stream=None):
+    """The workspace of calls without one: of this size, kept, one for each thread and stream, whose calls run one
+    after another.  Captured calls have one of their own; graphs that are replayed at once need a workspace each."""
+    who = ("graph" if torch.cuda.is_current_stream_capturing()
+           else (threading.get_ident(), _stream(t, stream).value or 0))
+    key = (str(t.device), nbytes, who)
     ws = _ws_cache.get(key)
     if ws is None:
-        ws = _ws_cache[key] = Workspace(nbytes, device)
+        if stream is None:
+            ws = Workspace(nbytes, t.device)
+        else:  # cleared on the stream that uses it
+            own = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=t.device)
+            with torch.cuda.stream(own):
+                ws = Workspace(nbytes, t.device)
+        _ws_cache[key] = ws
     return ws
 
 
@@ -390,7 +400,7 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, scale=None, l2norm
     if h0 is not None:
         assert h0.dtype == torch.float32 and tuple(h0.shape) == (sh.n_seqs, sh.Hv, sh.V, sh.K)
     if workspace is None:
-        workspace = _workspace_for(gdn_chunk_fwd_workspace_bytes(sh), v.device)
+        workspace = _workspace_for(gdn_chunk_fwd_workspace_bytes(sh), v, stream)
     ws = workspace
     _check(load().gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
                                 _ptr(cu_seqlens), ctypes.byref(sh), float(scale), flags, _ptr(o),
@@ -429,7 +439,7 @@ def gdn_chunk_bwd(q, k, v, g, beta, d_o, dh_T=None, h0=None, cu_seqlens=None, sc
     nbytes = gdn_chunk_bwd_workspace_bytes(sh)
     if nbytes == 0:
         raise GdnError("gdn_chunk_bwd: shape not supported (K 32/64/128, V a multiple of 16 up to 256)")
-    ws = workspace or _workspace_for(nbytes, dev)
+    ws = workspace or _workspace_for(nbytes, v, stream)
     flags = GDN_FLAG_QK_L2NORM if l2norm_qk else 0
     _check(load().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
                                 ctypes.byref(sh), float(scale), flags, _ptr(d_o), _ptr(dh_T), _ptr(dq), _ptr(dk),
@@ -471,7 +481,7 @@ def gdn_segment_summary(k, v, g, beta, seg_bounds, l2norm_qk=True, simt=False, M
     if S_local is None:
         S_local = torch.empty((n_seg, sh.Hv, sh.V, sh.K), device=v.device, dtype=torch.float32)
     nbytes = int(load().gdn_segment_summary_workspace_bytes(ctypes.byref(sh), n_seg))
-    ws = workspace or _workspace_for(nbytes, v.device)
+    ws = workspace or _workspace_for(nbytes, v, stream)
     _check(load().gdn_segment_summary(_ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(seg_bounds),
                                       n_seg, ctypes.byref(sh), flags, _ptr(M), _ptr(S_local),
                                       ws.ptr(), ws.nbytes, _stream(v, stream)),
@@ -570,7 +580,7 @@ def gdn_layer_fwd(x, conv_w, a, b, A_log, dt_bias, Hqk, Hv, K, V, h0=None, cu_se
     if z is not None:
         assert z.dtype == x.dtype and tuple(z.shape) == (n_tok, Hv, V)
     if workspace is None:
-        workspace = _workspace_for(gdn_layer_fwd_workspace_bytes(sh, width, flags), x.device)
+        workspace = _workspace_for(gdn_layer_fwd_workspace_bytes(sh, width, flags), x, stream)
     ws = workspace
     _check(load().gdn_layer_fwd(_ptr(x), _ptr(conv_w), _ptr(conv_bias), int(width), _ptr(a), _ptr(b),
                                 _ptr(A_log), _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), ctypes.byref(sh),
