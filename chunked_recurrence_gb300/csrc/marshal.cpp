@@ -5,6 +5,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/Allocator.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -54,6 +55,23 @@ PyObject *lays(PyObject *, PyObject *const *args, Py_ssize_t n) try {
 
 struct PyRaised {};  // a Python error has been set
 
+// The exception being handled as Python's; nullptr.
+PyObject *raised() {
+  try {
+    throw;
+  } catch (const PyRaised &) {
+  } catch (const c10::OutOfMemoryError &e) {  // what torch's own allocations raise
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
 // One argument of a library call: a pointer is a tensor's data, a bytes object's, an address or None.
 template <typename P>
 P argument(PyObject *o) {
@@ -96,12 +114,10 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
       memcpy(p, &x, sizeof x);
     }
     return out;
-  } catch (const PyRaised &) {
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    Py_DECREF(out);
+    return raised();
   }
-  Py_DECREF(out);
-  return nullptr;
 }
 
 // like(tensor, dims, f32) -> a new contiguous tensor of the sizes of its first `dims` dimensions
@@ -119,9 +135,8 @@ PyObject *like(PyObject *, PyObject *const *args, Py_ssize_t n) {
   try {
     const auto options = args[2] == Py_True ? t.options().dtype(at::kFloat) : t.options();
     return THPVariable_Wrap(at::empty(t.sizes().slice(0, dims), options.requires_grad(false)));
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
+  } catch (...) {
+    return raised();
   }
 }
 
@@ -159,11 +174,9 @@ struct Entry<gdn_status(P...), SCRATCH> {
     try {
       auto *f = (gdn_status(*)(P...))argument<void *>(args[0]);
       return PyLong_FromLong(invoke<SCRATCH>(f, args + 1, std::index_sequence_for<P...>{}));
-    } catch (const PyRaised &) {
-    } catch (const std::exception &e) {
-      PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+      return raised();
     }
-    return nullptr;
   }
 };
 

@@ -65,3 +65,11 @@ def test_the_module_is_this_interpreters():
     from chunked_recurrence_gb300 import build
     assert build.MARSHAL.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and "cpython" in build.MARSHAL
     assert paged._marshal is None or paged._marshal.__file__ == build.MARSHAL
+
+
+def test_a_module_that_was_built_loads():
+    import os
+    from chunked_recurrence_gb300 import build
+    if not os.path.exists(build.MARSHAL):
+        pytest.skip("gdn_marshal is not built")
+    assert paged._marshal is not None

@@ -177,3 +177,36 @@ def test_first_call_of_a_process_is_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL_IS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-3000:]
+
+
+OUT_OF_MEMORY = """
+import torch
+import chunked_recurrence_gb300 as crg
+cache = torch.zeros(64, 16, 8, 128, device="cuda").bfloat16()
+q = torch.zeros(1, 64, 128, device="cuda").bfloat16()
+table, lens = torch.zeros(1, 64, device="cuda", dtype=torch.int32), torch.ones(1, device="cuda", dtype=torch.int32)
+free = 24 << 20
+torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + free) / torch.cuda.mem_get_info()[1])
+hold = [torch.empty(8 << 20, device="cuda", dtype=torch.uint8) for _ in range(2)]
+for call in (lambda: crg.gdn_paged_attn(q, cache, cache, table, lens),
+             lambda: paged._like(torch.zeros(1, device="cuda").expand(1 << 27), 1, True)):
+    from chunked_recurrence_gb300 import paged
+    try:
+        call()
+    except torch.OutOfMemoryError:
+        print("out of memory")
+del hold
+crg.gdn_paged_attn(q, cache, cache, table, lens)
+torch.cuda.synchronize()
+print("done")
+"""
+
+
+def test_memory_that_runs_out_is_torchs_error():
+    """Outputs and scratch that the allocator refuses (a limit of this process's own) raise what torch's do."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", OUT_OF_MEMORY], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split("\n")[:3] == ["out of memory"] * 2 + ["done"], r.stdout + r.stderr[-3000:]
