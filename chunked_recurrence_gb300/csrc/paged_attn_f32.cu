@@ -5,8 +5,8 @@
 // tcgen05 would need an fp32 operand's parts staged in shared memory; here K, V and Q lie there as they
 // are (fp32) and are split in registers as fragments are loaded, x = hi + lo, both TF32, a product
 // taking hi*hi + hi*lo + lo*hi (the dropped term is 2^-22 of it).  bf16 values are exact in TF32 and need no lo.
-// The matrix instructions, three a product, and the splitting bound chunks: 24 of 200 tokens over 1000, 64/8 heads,
-// D 256: 4.4 ms, 64 TFLOP/s, 193 of TF32 products (the CUDA-core kernel 14.4 ms).
+// The matrix instructions, three a product, and the splitting bound chunks: 24 ragged ones of up to 200 tokens (1957 in
+// all) over 1000, 64/8 heads, D 256: 4.4 ms, 27 TFLOP/s, 81 of TF32 products (the CUDA-core kernel 14.4 ms).
 // Single tokens wait on their own chain of products, eight of a warp's sixteen rows unused: 24 over 1000, 32/8 heads,
 // D 128: 81 us, 36% of HBM.  Small calls are a chain of latencies: 5 chunks with a window of 200: 13 us.
 //
@@ -38,7 +38,7 @@ template <typename T, int DP, bool FEW>
 struct Cfg {
   static constexpr bool kExact = sizeof(T) == 2;   // values exact in TF32
   static constexpr int R = FEW ? 16 : 64;
-  // positions a tile (FEW: two blocks an SM; 24 single tokens over 1000, D 128: 92 us, 128 us with 64)
+  // positions a tile (FEW: two blocks an SM; 24 single tokens over 1000, D 128: 81 us, 109 us with 64)
   static constexpr int BN = DP == 256 || FEW ? 32 : 64;
   static constexpr int kMine = FEW ? BN / 4 : BN;  // of them a warp's
   static constexpr int kPitch = DP + 4;            // floats a row: the fragments' loads meet no bank conflict
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
     // The MMAs' accumulation cuts off where an fp32 addition rounds, always towards zero, so a sum is made of parts of
     // four steps (with few rows, where a warp has one product at a time, of one: four that do not wait for each
     // other), added by fp32 additions: an error of 6.6e-7 for chunks of 40 over 6000, D 128, and of 3.1e-6 with one
-    // chain of MMAs (fp32 products and sums in a library's order: 1.4e-6).  It costs 4.4 ms for 3.95 at D 256.
+    // chain of MMAs (fp32 products and sums in a library's order: 1.4e-6; with a window of 200 5.9e-7 to its
+    // 3.5e-7).  It costs 4.4 ms for 3.95 at D 256.
     constexpr int kParts = FEW ? 4 : 1;
     float s[C::kMine / 8][4];
 #pragma unroll
@@ -393,8 +394,8 @@ bool few_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_n
 
 // Parts that a block's positions are cut into: two blocks an SM (three with few rows), no part below 64 positions of
 // the longest span that the table and the window allow, at most 64.  Single tokens of 24 sequences over 1000, D 128:
-// 78 us, 112 us with as many blocks as are resident at most; 5 chunks of up to 37 over 700 with a window of 200, D 64:
-// 13.9 us, 18.2 us with parts from 128 positions on.
+// 81 us, 143 us with two blocks an SM (of 4 over 8000: 105 and 136); 5 chunks of up to 37 over 700 with a window of 200,
+// D 64: 12.8 us, 17.6 us with parts from 128 positions on.
 int paged_attn_f32_splits(const gdn_cache_shape &s, int32_t max_new, int32_t window) {
   const bool few = few_rows(s, max_new);
   const int64_t blocks = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, few ? 16 : 64) * s.Hkv;

@@ -27,10 +27,10 @@
 // and half of each K and V tile, so K and V come from L2 once for both and the ring holds twice the tiles.
 //
 // What bounds it, and what it measured (a copy 6694 GB/s, a cuBLAS product 1885 TFLOP/s in a burst, 1707 sustained).
-// Single tokens, HBM: 64 x 8192 positions, 8 kv heads, D 128, pages of 16: 324 us, 99% of the copy's rate; ragged 500
-// to 16000, pages of 64: 355 us, 94%; D 64: 207 us, 77% (rows of 128 bytes).  Chunks, the matrix instructions and the
-// waits between them: 8192 over 16384, 32/8 heads, D 128: 1131 us, 1459 TFLOP/s; 4096 over 8192, 16/2 heads, D 256:
-// 254 us, 1620.  D 64 waits on the softmax, as many weights as at D 256 for a quarter of the products: 1015 us for
+// Single tokens, HBM: 64 x 8192 positions, 8 kv heads, D 128, pages of 16: 319 us, 101% of the copy's rate; ragged 500
+// to 16000, pages of 64: 344 us, 97%; D 64: 205 us, 78% (rows of 128 bytes).  Chunks, the matrix instructions and the
+// waits between them: 8192 over 16384, 32/8 heads, D 128: 1115 us, 1479 TFLOP/s; 4096 over 8192, 16/2 heads, D 256:
+// 251 us, 1644.  D 64 waits on the softmax, as many weights as at D 256 for a quarter of the products: 999 us for
 // the first of these.  A few short sequences: some 13 us, the chain of launch, lengths, table, copies, S, P, O, then the
 // join's.
 #include <cuda.h>
@@ -1113,8 +1113,8 @@ gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs
 
 // Rows of the longest chunk's kv head, and the row tiles that share K and V: one, two in a block (D <= 128: their O
 // and S fill the TMEM), or (D 128 and 256) twice as many in a pair of blocks, wherever a chunk's rows need more than
-// one of the smaller.  8192 over 16384, D 128: 1165 us in pairs, 1198 without; 4096 over 8192, D 256: 267 us and 403;
-// 16 ragged chunks of up to 509 over up to 6000, 8 heads a group, D 256: 184 us and 212.
+// one of the smaller.  8192 over 16384, D 128: 1115 us in pairs, 1162 without; 4096 over 8192, D 256: 251 us and 394;
+// 16 ragged chunks of up to 509 over up to 6000, 8 heads a group, D 256: 139 us and 200.
 int64_t chunk_rows(const gdn_cache_shape &s, int32_t max_new) { return (int64_t)max_new * (s.Hq / s.Hkv); }
 bool two_tiles(const gdn_cache_shape &s, int32_t max_new) { return s.D <= 128 && chunk_rows(s, max_new) > 128; }
 bool pairs(const gdn_cache_shape &s, int32_t max_new) {

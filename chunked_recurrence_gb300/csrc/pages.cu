@@ -9,7 +9,7 @@
 //
 // Copying is bound by HBM: a moved byte is read once and written once (1.14 GB read and written to bring the pages of a
 // half-empty cache together: 181 us, 94% of a copy's rate).  Small calls are launches and the plan's chain of loads:
-// freeing and forking 24 of 48 sequences 14 us, 6 of them the plan.  No page is both read and written by one call
+// freeing and forking 24 of 48 sequences 14 us, some 6 of them the plan.  No page is both read and written by one call
 // (compact moves pages at or past L into free ones below it; fork's new pages were free), so the copies run in any
 // order.
 #include <algorithm>
