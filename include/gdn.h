@@ -14,13 +14,15 @@
  *  - Every pointer argument is a DEVICE pointer, allocated and owned by the
  *    caller, unless stated otherwise.  The library never allocates device
  *    memory, never synchronises the stream, and keeps no per-call state
- *    between calls beyond a cache of driver entry points.
+ *    between calls beyond a cache of driver entry points and the words of
+ *    gdn_status_words.
  *  - Calls are asynchronous and ordered on `stream` (a cudaStream_t passed as
  *    void*; NULL is the legacy default stream).
  *  - Argument errors return GDN_ERR_INVALID_ARG / GDN_ERR_UNSUPPORTED before
  *    anything is launched.  A failed launch returns GDN_ERR_CUDA.  Errors that
  *    only the GPU can see (a bounded wait that gave up, a bad index) are
- *    written to the status word at the start of the workspace; read it with
+ *    written to the status word at the start of the workspace (or to the one
+ *    that a paged call's shape or tables name); read it with
  *    gdn_workspace_status() after the stream has been synchronised.
  *  - Layouts are token-major and row-major: a token's heads are contiguous,
  *    and a head's features are contiguous.  "Dense" strides mean the natural
