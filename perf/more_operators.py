@@ -446,8 +446,7 @@ def _own(st):
     case, op = st["case"], st["case"]["op"]
     if op == "shared":
         return crg.gdn_paged_attn_shared(st["q"], st["k_cache"], st["v_cache"], st["table"], st["lens"], st["groups"],
-                                         st["prefix"], st["cu"], max_new=case["max_new"], max_group_new=st["most"],
-                                         want_lse=True)
+                                         st["prefix"], st["cu"], max_group_new=st["most"], want_lse=True)
     if op == "mass":
         if case["add"]:
             st["mass"].copy_(st["begin"])
