@@ -71,6 +71,12 @@ class GdnPagePools(ctypes.Structure):
                 ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
 
 
+class GdnPageHeads(ctypes.Structure):
+    _fields_ = ([("mass", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in ("n_layers", "heads", "mass_len")]
+                + [(n, ctypes.c_int64) for n in ("layer_stride", "row_stride", "head_stride", "row_bytes", "slot_stride",
+                                                 "slot_head_stride")])
+
+
 _P, _I32, _I64, _U32, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t)
 _F64 = ctypes.c_double
@@ -118,6 +124,11 @@ _SIGS = {
     "gdn_pages_fork": ([_P, _P, _P, _I32, _P, _P, _SZ, _P], ctypes.c_int),
     "gdn_pages_compact": ([_P, _P, _P, _SZ, _P], ctypes.c_int),
     "gdn_pages_copy": ([_P, _P, _I32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
+    "gdn_paged_attn_shared_workspace_bytes": ([_P, _I32, _I32], _SZ),
+    "gdn_paged_attn_shared": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I32, _F32, _U32, _P, _P, _P, _SZ, _P],
+                              ctypes.c_int),
+    "gdn_pages_evict_workspace_bytes": ([_P, _I32, _I32, _I32, _I32], _SZ),
+    "gdn_pages_evict": ([_P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
 }
 
 
@@ -602,7 +613,9 @@ def segment_parallel_fwd(q, k, v, g, beta, seg_bounds, h0=None, scale=None, l2no
 
 
 # full attention over a paged cache
-from .paged import (cache_shape, gdn_kv_append, gdn_paged_attn, gdn_paged_attn_workspace_bytes,  # noqa: E402,F401
-                    gdn_pages_compact, gdn_pages_copy, gdn_pages_fork, gdn_pages_free, gdn_pages_grow,
+from .paged import (cache_shape, gdn_kv_append, gdn_paged_attn, gdn_paged_attn_shared,  # noqa: E402,F401
+                    gdn_paged_attn_shared_workspace_bytes, gdn_paged_attn_workspace_bytes, gdn_pages_compact,
+                    gdn_pages_copy, gdn_pages_evict, gdn_pages_evict_workspace_bytes, gdn_pages_fork, gdn_pages_free,
+                    gdn_pages_grow,
                     gdn_pages_workspace_bytes, gdn_paged_status, gdn_paged_status_reset, gdn_rope, gdn_rope_freqs,
                     gdn_rope_inv_freq)

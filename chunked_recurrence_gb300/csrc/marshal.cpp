@@ -193,11 +193,13 @@ PyMethodDef methods[] = {
     GDN_ENTRY(gdn_rope),
     GDN_ENTRY(gdn_kv_append),
     GDN_ENTRY_SCRATCH(gdn_paged_attn),
+    GDN_ENTRY_SCRATCH(gdn_paged_attn_shared),
     GDN_ENTRY_SCRATCH(gdn_pages_grow),
     GDN_ENTRY(gdn_pages_free),
     GDN_ENTRY_SCRATCH(gdn_pages_fork),
     GDN_ENTRY_SCRATCH(gdn_pages_compact),
     GDN_ENTRY(gdn_pages_copy),
+    GDN_ENTRY_SCRATCH(gdn_pages_evict),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_marshal", "paged operators' marshalling", -1, methods};
 

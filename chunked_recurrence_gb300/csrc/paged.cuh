@@ -24,6 +24,9 @@ struct PagedSeqs {
   int32_t n_seqs;
   int32_t n_tok;
   int32_t max_tokens;       // max_pages * page_size, clamped to int32: no sequence can hold more
+  // sequences that share a prefix: [n_groups + 1] offsets of the groups' sequences, [n_groups] tokens shared; null: none
+  const int32_t *groups, *prefix;
+  int32_t n_groups;
 };
 
 struct SeqSpan {
@@ -114,6 +117,124 @@ GDN_HD int32_t unit_tile(int32_t u, int32_t over) { return u > over ? u - over :
 
 // Block b's share [begin, end) of `total` units over `blocks` blocks.
 GDN_HD int64_t share_begin(int64_t total, int32_t b, int32_t blocks) { return total / blocks * b + total % blocks * b / blocks; }
+
+// ---- groups of sequences that share a prefix.  The rows of a group's tokens make one run of rows against the prefix (its
+// pages read from the group's first row of the table), cut into items as a sequence's are; the sequences' own items then
+// begin at the prefix's end.  The groups' slots come first, then the sequences'.
+
+struct GroupSpan {
+  int32_t s0, s1, prefix;  // sequences [s0, s1), tokens that they share
+  bool ok;
+};
+GDN_HD int32_t group_at(const PagedSeqs &q, int32_t g) {
+  const int32_t s = q.groups[g];
+  return s < 0 ? 0 : s > q.n_seqs ? q.n_seqs : s;
+}
+GDN_HD GroupSpan group_span(const PagedSeqs &q, int32_t g) {
+  GroupSpan r;
+  r.s0 = group_at(q, g), r.s1 = group_at(q, g + 1);
+  const int32_t p = q.prefix[g];
+  r.prefix = p < 0 ? 0 : p > q.max_tokens ? q.max_tokens : p;
+  r.ok = q.groups[g] == r.s0 && q.groups[g + 1] == r.s1 && r.s0 <= r.s1 && r.prefix == p &&
+         (g > 0 || r.s0 == 0) && (g + 1 < q.n_groups || r.s1 == q.n_seqs);
+  return r;
+}
+// The group of a sequence, and the sequence of a token: the last whose offset is not past it.
+GDN_HD int32_t seq_group(const PagedSeqs &q, int32_t s) {
+  int32_t lo = 0, hi = q.n_groups - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (group_at(q, mid) <= s) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+GDN_HD int32_t token_seq(const PagedSeqs &q, int32_t t) {
+  if (!q.cu) return t;
+  int32_t lo = 0, hi = q.n_seqs - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (cu_at(q, mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+GDN_HD int32_t group_base(const PagedSeqs &q, int32_t g, int32_t G, int32_t R) { return cu_at(q, group_at(q, g)) * G / R + g; }
+GDN_HD int64_t shared_slots(int64_t n_tok, int32_t n_seqs, int32_t n_groups, int32_t G, int32_t R) {
+  return item_slots(n_tok, n_groups, G, R) + item_slots(n_tok, n_seqs, G, R);
+}
+
+struct SharedItem : Item {
+  int32_t g;  // the group
+  bool own;   // a sequence's own positions; else the group's prefix
+};
+
+// Rows of group g against its prefix; it.s is the group's first sequence.  A row sees less than all of the prefix where
+// its token lies in it (row_end).
+GDN_HD SharedItem prefix_item(const PagedSeqs &q, int32_t g, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+  SharedItem it;
+  const GroupSpan gs = group_span(q, g);
+  const int32_t a = cu_at(q, gs.s0), b = cu_at(q, gs.s1);
+  it.g = g, it.own = false;
+  it.s = gs.s0 < q.n_seqs ? gs.s0 : q.n_seqs - 1;
+  it.t0 = a, it.first = 0;
+  const int64_t row0 = (int64_t)(slot - group_base(q, g, G, R)) * R, all = b > a ? (int64_t)(b - a) * G : 0;
+  it.row0 = (int32_t)(row0 < all ? row0 : all);
+  it.rows = (int32_t)(row0 < 0 || row0 >= all ? 0 : all - row0 < R ? all - row0 : R);
+  const int32_t len = q.seq_lens[it.s];
+  it.ok = gs.ok && (it.rows == 0 || gs.prefix <= len);
+  it.lo = it.tile0 = 0;
+  it.hi = it.rows > 0 ? (gs.prefix < len ? gs.prefix : len < 0 ? 0 : len) : 0;
+  it.n_tiles = (it.hi + KT - 1) / KT;
+  return it;
+}
+// Rows of sequence s, of group g, against its positions behind the prefix.
+GDN_HD SharedItem own_item(const PagedSeqs &q, int32_t g, int32_t s, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+  SharedItem it;
+  static_cast<Item &>(it) = item_of(q, s, slot, G, R, KT, 0);
+  const GroupSpan gs = group_span(q, g);
+  it.g = g, it.own = true;
+  if (it.rows > 0) {
+    it.ok = it.ok && gs.ok && gs.prefix <= q.seq_lens[s];
+    it.lo = gs.prefix;
+    if (it.lo < it.hi) {
+      it.tile0 = it.lo / KT;
+      it.n_tiles = (it.hi + KT - 1) / KT - it.tile0;
+    } else {
+      it.lo = it.hi = it.tile0 = it.n_tiles = 0;
+    }
+  }
+  return it;
+}
+GDN_HD SharedItem shared_item_at(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+  const int32_t first = (int32_t)item_slots(q.n_tok, q.n_groups, G, R);
+  if (slot >= first) {
+    const int32_t s = slot_seq(q, slot - first, G, R);
+    return own_item(q, seq_group(q, s), s, slot - first, G, R, KT);
+  }
+  int32_t lo = 0, hi = q.n_groups - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (group_base(q, mid, G, R) <= slot) lo = mid; else hi = mid - 1;
+  }
+  return prefix_item(q, lo, slot, G, R, KT);
+}
+// The positions [0, row_end) of its prefix that row r (of the group) of a prefix item sees.
+GDN_HD int32_t row_end(const PagedSeqs &q, const SharedItem &it, int32_t r, int32_t G) {
+  const int32_t t = it.t0 + r / G;
+  const SeqSpan sp = seq_span(q, token_seq(q, t));
+  const int32_t end = sp.len - sp.n_new + (t - sp.t0) + 1;
+  return end < 0 ? 0 : end < it.hi ? end : it.hi;
+}
+// Units of an item as item_units, none where it has no tiles.
+GDN_HD int32_t shared_units(const Item &it, int32_t over) { return it.rows <= 0 || it.n_tiles <= 0 ? 0 : it.n_tiles + over; }
+
+// The block whose share (share_begin) holds unit u < total, with 1 <= blocks <= total.
+GDN_HD int32_t share_of(int64_t total, int64_t u, int32_t blocks) {
+  int32_t b = (int32_t)((u + 1) * blocks / total);  // u blocks fits: total is at most 2^40 or so
+  if (b >= blocks) b = blocks - 1;
+  while (b > 0 && share_begin(total, b, blocks) > u) --b;
+  while (b + 1 < blocks && share_begin(total, b + 1, blocks) <= u) ++b;
+  return b;
+}
 
 // Page of a position, or -1 where the table names none inside the cache.
 GDN_HD int32_t page_of(const int32_t *row, int32_t pos, int32_t page_size, int32_t max_pages, int32_t n_pages) {

@@ -1,6 +1,7 @@
-// paged_attn.cu -- attention of new tokens over a paged cache (gdn_paged_attn): argument
-// checks, dispatch and the CUDA-core kernel (GDN_FLAG_SIMT).  The kernels that run by default are in
-// paged_attn_tc.cu (bf16 on tcgen05) and paged_attn_f32.cu (fp32, and what the first does not take).
+// paged_attn.cu -- attention of new tokens over a paged cache (gdn_paged_attn, and gdn_paged_attn_shared where
+// sequences share a prefix): argument checks, dispatch and the CUDA-core kernel (GDN_FLAG_SIMT).  The kernels that
+// run by default are in paged_attn_tc.cuh (bf16 on tcgen05) and paged_attn_f32.cu (fp32, and what the first does not
+// take).
 //
 //     o[t, h] = sum_j softmax_j(scale <q[t, h], k_j>) v_j   over the positions that t sees
 //
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const Simt
   __shared__ float s_acc[kWarps][kRows][NE * 32], s_m[kWarps][kRows], s_l[kWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, h = blockIdx.y, part = blockIdx.z;
-  const Item it = item_at(a.seqs, blockIdx.x, G, kRows, 1, a.window);  // tiles of one position
+  const SharedItem it = simt_item(a, blockIdx.x, G, kRows);
   if (!it.ok && threadIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
   if (it.rows <= 0) return;
 
@@ -83,9 +84,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const Simt
       acc[r][e] = 0.f;
     }
     m[r] = -INFINITY, l[r] = 0.f;
-    const int p = it.first + i;
-    hi[r] = r < it.rows ? p + 1 : 0;
-    lo[r] = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+    hi[r] = r < it.rows ? simt_row_end(a, it, row, G) : 0;
+    lo[r] = simt_row_begin(a, it, row, G);
   }
   const int begin = it.lo + (int)share_begin(it.hi - it.lo, part, a.splits);
   const int end = it.lo + (int)share_begin(it.hi - it.lo, part + 1, a.splits);
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const Simt
     }
     const int rr = it.row0 + r, i = rr / G, g = rr - i * G;
     const int64_t out = (int64_t)(it.t0 + i) * a.Hq + h * G + g;
-    float *pp = a.part ? a.part + ((int64_t)part * a.seqs.n_tok * a.Hq + out) * (a.D + 2) : nullptr;
+    float *pp = a.part ? a.part + ((int64_t)simt_part(a, it) * a.seqs.n_tok * a.Hq + out) * (a.D + 2) : nullptr;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     for (int d = lane; d < a.D; d += 32) {
       float x = 0.f;
@@ -241,8 +241,22 @@ gdn_status launch_join(const SimtArgs &a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the parts' end
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, simt_join_kernel<T>, (const float *)a.part, (int)a.splits, rows, (int)a.D, (T *)a.o, a.lse);
+  const int parts = a.seqs.n_groups ? 2 * a.splits : a.splits;
+  cudaLaunchKernelEx(&cfg, simt_join_kernel<T>, (const float *)a.part, parts, rows, (int)a.D, (T *)a.o, a.lse);
   return launch_status();
+}
+
+// The kernels without tcgen05, and the join of their parts.
+gdn_status launch_parts(const SimtArgs &a, const gdn_cache_shape &s, bool simt, int32_t max_new, cudaStream_t st) {
+  gdn_status r;
+  if (simt) {
+    const int64_t slots = simt_slots(a, kRows);
+    r = s.dtype == GDN_BF16 ? dispatch_simt<__nv_bfloat16>(a, slots, st) : dispatch_simt<float>(a, slots, st);
+  } else {
+    r = paged_attn_f32(a, s, max_new, st);
+  }
+  if (r != GDN_OK || !a.part) return r;
+  return s.dtype == GDN_BF16 ? launch_join<__nv_bfloat16>(a, st) : launch_join<float>(a, st);
 }
 
 }  // namespace
@@ -285,13 +299,55 @@ extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const v
              simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new, window), scale_log2,
              s.status ? s.status : (int32_t *)workspace};
   if (a.splits > 1) a.part = (float *)((char *)workspace + 256);
-  gdn_status r;
-  if (simt) {
-    const int64_t slots = item_slots(s.n_tok, s.n_seqs, s.Hq / s.Hkv, kRows);
-    r = s.dtype == GDN_BF16 ? dispatch_simt<__nv_bfloat16>(a, slots, st) : dispatch_simt<float>(a, slots, st);
-  } else {
-    r = paged_attn_f32(a, s, max_new, st);
-  }
-  if (r != GDN_OK || !a.part) return r;
-  return s.dtype == GDN_BF16 ? launch_join<__nv_bfloat16>(a, st) : launch_join<float>(a, st);
+  return launch_parts(a, s, simt, max_new, st);
+}
+
+// With groups: the join takes at most 64 parts of both kinds together.
+static int shared_splits(const gdn_cache_shape &s, bool simt, int32_t max_group_new) {
+  return std::min(32, simt ? simt_splits(s) : paged_attn_f32_splits(s, max_group_new, 0));
+}
+
+extern "C" size_t gdn_paged_attn_shared_workspace_bytes(const gdn_cache_shape *shape, int32_t n_groups,
+                                                        int32_t max_group_new) {
+  gdn_cache_shape s;
+  static const int32_t some = 0;
+  if (max_group_new < 0 || normalise_cache_shape(shape, &some, &s) != GDN_OK) return 0;
+  if (n_groups < 0 || n_groups > 1 << 28) return 0;
+  return std::max({parts_bytes(s, 2 * shared_splits(s, true, max_group_new)),
+                   parts_bytes(s, 2 * shared_splits(s, false, max_group_new)),
+                   paged_shared_tc_workspace(s, n_groups, max_group_new)});
+}
+
+extern "C" gdn_status gdn_paged_attn_shared(const void *q, const void *k_cache, const void *v_cache,
+                                            const int32_t *page_table, const int32_t *seq_lens,
+                                            const int32_t *cu_seqlens, const int32_t *group_offsets,
+                                            const int32_t *prefix_lens, int32_t n_groups, const gdn_cache_shape *shape,
+                                            int32_t max_group_new, float scale, uint32_t flags, void *o, float *lse,
+                                            void *workspace, size_t workspace_bytes, void *stream) {
+  gdn_cache_shape s;
+  const gdn_status ok = normalise_cache_shape(shape, cu_seqlens, &s);
+  if (ok != GDN_OK) return ok;
+  if (max_group_new < 0 || n_groups < 0 || (n_groups == 0 && s.n_seqs > 0) ||
+      (flags & ~(uint32_t)(GDN_FLAG_SIMT | GDN_FLAG_TEST_NO_WAIT)))
+    return GDN_ERR_INVALID_ARG;
+  if (n_groups > 1 << 28) return GDN_ERR_UNSUPPORTED;  // slots of items fit 32 bits
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < gdn_paged_attn_shared_workspace_bytes(shape, n_groups, max_group_new))
+    return GDN_ERR_WORKSPACE;
+  if (s.n_tok == 0 || s.n_seqs == 0) return GDN_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !group_offsets || !prefix_lens || !o)
+    return GDN_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  PagedSeqs seqs = paged_seqs(s, seq_lens, cu_seqlens);
+  seqs.groups = group_offsets, seqs.prefix = prefix_lens, seqs.n_groups = n_groups;
+  const float scale_log2 = scale * 1.44269504088896340736f;
+  const bool simt = flags & GDN_FLAG_SIMT;
+  if (!simt && paged_attn_tc_supported(q, k_cache, v_cache, o, s, scale))
+    return paged_shared_tc(q, k_cache, v_cache, page_table, seqs, s, max_group_new, scale_log2, flags, o, lse,
+                           workspace, st);
+  SimtArgs a{seqs, q, k_cache, v_cache, o, lse, (float *)((char *)workspace + 256), page_table, s.table_stride,
+             s.page_stride, s.slot_stride, s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages,
+             s.n_pages, 0, shared_splits(s, simt, max_group_new), scale_log2,
+             s.status ? s.status : (int32_t *)workspace};
+  return launch_parts(a, s, simt, max_group_new, st);
 }

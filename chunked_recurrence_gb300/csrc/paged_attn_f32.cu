@@ -47,18 +47,18 @@ struct Cfg {
 };
 
 // A row's values out: o / l and lse, or the part for the join.
-__device__ __forceinline__ void put_stats(const SimtArgs &a, int64_t row, float top, float sum) {
+__device__ __forceinline__ void put_stats(const SimtArgs &a, int part, int64_t row, float top, float sum) {
   if (a.part) {
-    float *pp = a.part + ((int64_t)blockIdx.z * a.seqs.n_tok * a.Hq + row) * (a.D + 2);
+    float *pp = a.part + ((int64_t)part * a.seqs.n_tok * a.Hq + row) * (a.D + 2);
     pp[0] = top, pp[1] = sum;
   } else if (a.lse) {
     a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
   }
 }
 template <typename T>
-__device__ __forceinline__ void put(const SimtArgs &a, int64_t row, int col, float x, float inv) {
+__device__ __forceinline__ void put(const SimtArgs &a, int part, int64_t row, int col, float x, float inv) {
   if (col >= a.D) return;
-  if (a.part) a.part[((int64_t)blockIdx.z * a.seqs.n_tok * a.Hq + row) * (a.D + 2) + 2 + col] = x;
+  if (a.part) a.part[((int64_t)part * a.seqs.n_tok * a.Hq + row) * (a.D + 2) + 2 + col] = x;
   else ((T *)a.o)[row * a.D + col] = from_f32<T>(x * inv);
 }
 
@@ -69,17 +69,18 @@ template <typename T, int DP>
 __device__ __noinline__ void plain_rows(const SimtArgs &a, int R) {
   constexpr int kE = DP / 32;
   const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv, h = blockIdx.y;
-  const Item it = item_at(a.seqs, blockIdx.x, G, R, 1, a.window);
+  const SharedItem it = simt_item(a, blockIdx.x, G, R);
+  const int part = simt_part(a, it);
   const int begin = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z, a.splits);
   const int end = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z + 1, a.splits);
   const int32_t *table = a.table + (int64_t)it.s * a.table_stride;
   for (int r = threadIdx.x >> 5; r < it.rows; r += kThreads / 32) {
-    const int row = it.row0 + r, tok = row / G, p = it.first + tok;
+    const int row = it.row0 + r, tok = row / G;
     const T *qp = (const T *)a.q + (int64_t)(it.t0 + tok) * a.q_stride + (int64_t)(h * G + row - tok * G) * a.D;
     float q[kE], acc[kE], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) q[e] = lane + 32 * e < a.D ? to_f32<T>(qp[lane + 32 * e]) : 0.f, acc[e] = 0.f;
-    for (int j = a.window > 0 && p >= a.window ? max(p - a.window + 1, begin) : begin; j < min(p + 1, end); ++j) {
+    for (int j = max(simt_row_begin(a, it, row, G), begin), to = min(simt_row_end(a, it, row, G), end); j < to; ++j) {
       const int page = page_of(table, j, a.page_size, a.max_pages, a.n_pages);
       if (page < 0) continue;
       const int64_t at = (int64_t)page * a.page_stride + (int64_t)(j % a.page_size) * a.slot_stride +
@@ -100,9 +101,9 @@ __device__ __noinline__ void plain_rows(const SimtArgs &a, int R) {
     }
     const int64_t out = (int64_t)(it.t0 + tok) * a.Hq + h * G + row - tok * G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (lane == 0) put_stats(a, out, top, sum);
+    if (lane == 0) put_stats(a, part, out, top, sum);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) put<T>(a, out, lane + 32 * e, acc[e], inv);
+    for (int e = 0; e < kE; ++e) put<T>(a, part, out, lane + 32 * e, acc[e], inv);
   }
 }
 
@@ -113,14 +114,15 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
   float *qs = smem, *ks = qs + C::R * C::kPitch, *vs = ks + 2 * C::kTile;
   int64_t *off = reinterpret_cast<int64_t *>(vs + 2 * C::kTile);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-  const int G = a.Hq / a.Hkv, h = blockIdx.y, part = blockIdx.z;
+  const int G = a.Hq / a.Hkv, h = blockIdx.y;
   sm100::launch_dependents();
   sm100::grid_dependency_wait();
-  const Item it = item_at(a.seqs, blockIdx.x, G, C::R, 1, a.window);  // tiles of one position
+  const SharedItem it = simt_item(a, blockIdx.x, G, C::R);
+  const int part = simt_part(a, it);
   if (!it.ok && tid == 0) set_status(a.status, GDN_ERR_BOUNDS);
   if (it.rows <= 0) return;
-  const int begin = it.lo + (int)share_begin(it.hi - it.lo, part, a.splits);
-  const int end = it.lo + (int)share_begin(it.hi - it.lo, part + 1, a.splits);
+  const int begin = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z, a.splits);
+  const int end = it.lo + (int)share_begin(it.hi - it.lo, blockIdx.z + 1, a.splits);
   const int n_tiles = (max(end - begin, 0) + C::BN - 1) / C::BN;
   const int32_t *table = a.table + (int64_t)it.s * a.table_stride;
 
@@ -183,9 +185,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int r = m0 + g4 + 8 * e, p = it.first + (it.row0 + r) / G;
-    hi[e] = r < it.rows ? min(p + 1, end) : 0;
-    lo[e] = a.window > 0 && p >= a.window ? max(p - a.window + 1, begin) : begin;
+    const int r = m0 + g4 + 8 * e;
+    hi[e] = r < it.rows ? min(simt_row_end(a, it, it.row0 + r, G), end) : 0;
+    lo[e] = max(simt_row_begin(a, it, it.row0 + r, G), begin);
   }
   float o[DP / 8][4];
 #pragma unroll
@@ -316,11 +318,11 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
       if (r >= it.rows) continue;
       const int64_t row = out_row(r);
       const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-      if (t4 == 0) put_stats(a, row, m[e], l[e]);
+      if (t4 == 0) put_stats(a, part, row, m[e], l[e]);
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i) {
-        put<T>(a, row, i * 8 + 2 * t4, o[i][2 * e], inv);
-        put<T>(a, row, i * 8 + 2 * t4 + 1, o[i][2 * e + 1], inv);
+        put<T>(a, part, row, i * 8 + 2 * t4, o[i][2 * e], inv);
+        put<T>(a, part, row, i * 8 + 2 * t4 + 1, o[i][2 * e + 1], inv);
       }
     }
   } else {
@@ -351,12 +353,12 @@ __global__ void __launch_bounds__(kThreads) paged_attn_f32_kernel(const SimtArgs
       }
       const int64_t row = out_row(r);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (lane == 0) put_stats(a, row, top, sum);
+      if (lane == 0) put_stats(a, part, row, top, sum);
       for (int col = lane; col < a.D; col += 32) {
         float x = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x += w[i] == 0.f ? 0.f : w[i] * acc[(i * 16 + r) * C::kPitch + col];
-        put<T>(a, row, col, x, inv);
+        put<T>(a, part, row, col, x, inv);
       }
     }
   }
@@ -368,7 +370,7 @@ gdn_status launch(const SimtArgs &a, bool wide, cudaStream_t st) {
   const auto kernel = paged_attn_f32_kernel<T, DP, FEW>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
-  const int64_t slots = item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.Hq / a.Hkv, C::R);
+  const int64_t slots = simt_slots(a, C::R);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)slots, a.Hkv, a.splits), cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem, cfg.stream = st;

@@ -14,26 +14,19 @@
 // order.
 #include <algorithm>
 
-#include "common.cuh"
-#include "paged.cuh"
-#include "sm100.cuh"
+#include "pages.cuh"
 
 using namespace gdn;
+using namespace gdn::pages;
 using sm100::grid_dependency_wait;
 using sm100::launch_dependents;
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
 // Entries of a fork's parents' rows that the plan looks through itself (1128: 8.6 us a fork, 8.9 and a launch more with a
 // kernel for it; 4096: 9.9 and 8.9; unchecked 7.4 and 7.6).
 constexpr int kPlanEntries = 2048;
-
-// Words of the workspace after the 256 bytes that hold the status.
-struct PlanWords {
-  int32_t ok, n_moves, live, pad;
-};
 
 struct Plan {
   PlanWords *w;
@@ -50,67 +43,6 @@ __device__ Plan plan_of(void *workspace, int32_t n_pages) {
   r.to = r.dst + n_pages;
   r.rows = r.to + n_pages;
   return r;
-}
-
-struct Pools {
-  void *p[GDN_MAX_POOLS];
-};
-
-// Inclusive sum over the block's threads; *total gets the whole.  sh: 33 words.
-__device__ __forceinline__ int block_scan(int x, int *sh, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += u;
-  }
-  __syncthreads();  // sh is free
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int y = lane < warps ? sh[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += u;
-    }
-    sh[lane] = y;
-  }
-  __syncthreads();
-  *total = sh[warps - 1];
-  return x + (warp ? sh[warp - 1] : 0);
-}
-
-// Four consecutive refs of a thread, n past the end read as `past`.
-__device__ __forceinline__ int4 load_refs(const int32_t *refs, int i, int n, int past) {
-  if (i + 3 < n && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) return *reinterpret_cast<const int4 *>(refs + i);
-  return make_int4(i < n ? refs[i] : past, i + 1 < n ? refs[i + 1] : past, i + 2 < n ? refs[i + 2] : past,
-                   i + 3 < n ? refs[i + 3] : past);
-}
-
-// The first `want` free pages into list, in rising order; returns how many there are of them.
-__device__ int first_free(const int32_t *refs, int n_pages, int want, int32_t *list, int *sh) {
-  int found = 0;
-  for (int base = 0; base < n_pages && found < want; base += 4 * kPlanThreads) {
-    const int i = base + 4 * threadIdx.x;
-    const int4 r = load_refs(refs, i, n_pages, 1);
-    const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
-    int total;
-    int at = found + block_scan(f[0] + f[1] + f[2] + f[3], sh, &total) - (f[0] + f[1] + f[2] + f[3]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (f[k]) {
-        if (at < want) list[at] = i + k;
-        ++at;
-      }
-    found += total;
-  }
-  __syncthreads();
-  return min(found, want);
-}
-
-__device__ __forceinline__ int32_t *table_row(const gdn_page_tables &t, int s) {
-  return t.page_table + (int64_t)s * t.table_stride;
 }
 
 // ------------------------------------------------------------------- plans
@@ -401,46 +333,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const gdn_page_table
   }
 }
 
-// The tables checked, strides and the status word filled in.
-bool tables_ok(const gdn_page_tables *in, void *workspace, gdn_page_tables *t) {
-  if (!in) return false;
-  *t = *in;
-  if (t->n_rows < 0 || t->max_pages < 0 || t->n_pages < 0 || t->page_size < 1 || !aligned(t->status, sizeof(int32_t)))
-    return false;
-  if (t->table_stride == 0) t->table_stride = t->max_pages;
-  if (!t->status) t->status = (int32_t *)workspace;
-  if (t->table_stride < t->max_pages || t->n_pages >= 1 << 21) return false;  // sums of 1024 rows' pages: 32 bits
-  return (t->n_rows == 0 || (t->page_table && t->seq_lens)) && (t->n_pages == 0 || t->refs);
-}
-
-gdn_status pools_ok(const gdn_page_pools *in, Pools *p) {
-  if (!in || in->n_pools < 0 || in->page_bytes < 0 || in->page_stride < in->page_bytes || (in->n_pools && !in->pools))
-    return GDN_ERR_INVALID_ARG;
-  if (in->n_pools > GDN_MAX_POOLS) return GDN_ERR_UNSUPPORTED;
-  for (int i = 0; i < in->n_pools; ++i) {
-    if (!in->pools[i]) return GDN_ERR_INVALID_ARG;
-    p->p[i] = in->pools[i];
-  }
-  return GDN_OK;
-}
-
-// A launch that overlaps the end of the kernel before on the stream, whose results the kernel waits for.
-template <typename... P, typename... A>
-void launch_early(void (*kernel)(P...), int blocks, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.stream = st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr, cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename V, int KIND>
 void launch_move(const gdn_page_tables &t, const int32_t *a, const int32_t *b, int n, const gdn_page_pools &in,
                  const Pools &pools, void *workspace, cudaStream_t st) {
   const int blocks = 152 * 8;  // resident at once: 256 threads, eight vectors each in flight
-  launch_early(move_kernel<V, KIND>, blocks, kMoveThreads, st, t, a, b, n, pools, (int)in.n_pools,
+  launch_early(move_kernel<V, KIND>, blocks, kMoveThreads, st, 0, t, a, b, n, pools, (int)in.n_pools,
                (int64_t)in.page_bytes, (int64_t)in.page_stride, workspace);
 }
 
@@ -457,8 +354,6 @@ gdn_status launch_moves(const gdn_page_tables &t, const int32_t *a, const int32_
 
 size_t need(int32_t n_pages, int32_t n_rows) { return 256 + sizeof(int32_t) * (3 * (size_t)n_pages + n_rows); }
 
-bool ws_ok(const void *w, size_t bytes, size_t want) { return w && aligned(w, 256) && bytes >= want; }
-
 }  // namespace
 
 extern "C" size_t gdn_pages_workspace_bytes(int32_t n_pages, int32_t n_rows) {
@@ -472,7 +367,7 @@ extern "C" gdn_status gdn_pages_grow(const gdn_page_tables *tables, const int32_
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs || !new_lens) return GDN_ERR_INVALID_ARG;
-  launch_early(grow_kernel, 1, kPlanThreads, (cudaStream_t)stream, t, seqs, new_lens, (int)n, workspace);
+  launch_early(grow_kernel, 1, kPlanThreads, (cudaStream_t)stream, 0, t, seqs, new_lens, (int)n, workspace);
   return launch_status();
 }
 
@@ -483,7 +378,7 @@ extern "C" gdn_status gdn_pages_free(const gdn_page_tables *tables, const int32_
   if (!tables->status && !ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
   if (!seqs) return GDN_ERR_INVALID_ARG;
-  launch_early(free_kernel, n, 256, (cudaStream_t)stream, t, seqs);
+  launch_early(free_kernel, n, 256, (cudaStream_t)stream, 0, t, seqs);
   return launch_status();
 }
 
@@ -500,10 +395,10 @@ extern "C" gdn_status gdn_pages_fork(const gdn_page_tables *tables, const int32_
   if (!parents || !children) return GDN_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if ((int64_t)n * t.max_pages <= kPlanEntries) {
-    launch_early(fork_plan_kernel<false>, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
+    launch_early(fork_plan_kernel<false>, 1, kPlanThreads, st, 0, t, parents, children, (int)n, workspace);
   } else {
-    launch_early(fork_check_kernel, n, 256, st, t, parents, workspace);
-    launch_early(fork_plan_kernel<true>, 1, kPlanThreads, st, t, parents, children, (int)n, workspace);
+    launch_early(fork_check_kernel, n, 256, st, 0, t, parents, workspace);
+    launch_early(fork_plan_kernel<true>, 1, kPlanThreads, st, 0, t, parents, children, (int)n, workspace);
   }
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   return launch_moves<kFork>(t, parents, children, n, *pools, p, workspace, st);
@@ -519,7 +414,7 @@ extern "C" gdn_status gdn_pages_compact(const gdn_page_tables *tables, const gdn
   if (!ws_ok(workspace, workspace_bytes, need(t.n_pages, t.n_rows))) return GDN_ERR_WORKSPACE;
   if (t.n_pages == 0) return GDN_OK;
   cudaStream_t st = (cudaStream_t)stream;
-  launch_early(compact_plan_kernel, 1, kPlanThreads, st, t, workspace);
+  launch_early(compact_plan_kernel, 1, kPlanThreads, st, 0, t, workspace);
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   return launch_moves<kCompact>(t, nullptr, nullptr, 0, *pools, p, workspace, st);
 }

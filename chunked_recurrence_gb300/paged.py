@@ -14,8 +14,8 @@ import torch
 
 from . import build as _build
 from . import (GDN_FLAG_ROPE_BACKWARD, GDN_FLAG_ROPE_INTERLEAVED, GDN_FLAG_SIMT, GDN_FLAG_TEST_NO_WAIT,
-               GDN_MAX_POOLS, GDN_ROPE_SCALING, GdnCacheShape, GdnPagePools, GdnPageTables, _check, _dtype_code,
-               _need_cuda, _ptr, _stream, load)
+               GDN_MAX_POOLS, GDN_ROPE_SCALING, GdnCacheShape, GdnPageHeads, GdnPagePools, GdnPageTables, _check,
+               _dtype_code, _need_cuda, _ptr, _stream, load)
 
 
 def _load_marshal():
@@ -63,7 +63,8 @@ def _plan(key, make):
 
 
 _entries = {}
-_TAKE_SCRATCH = ("gdn_paged_attn", "gdn_pages_grow", "gdn_pages_fork", "gdn_pages_compact")
+_TAKE_SCRATCH = ("gdn_paged_attn", "gdn_paged_attn_shared", "gdn_pages_grow", "gdn_pages_fork", "gdn_pages_compact",
+                 "gdn_pages_evict")
 
 
 def _entry(name):
@@ -376,6 +377,54 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, m
     return o, lse
 
 
+def _groups(group_offsets, prefix_lens):
+    _need_cuda(group_offsets, prefix_lens)
+    for name, t in (("group_offsets", group_offsets), ("prefix_lens", prefix_lens)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            raise TypeError(f"{name} must be contiguous int32")
+    if group_offsets.shape[0] != prefix_lens.shape[0] + 1:
+        raise ValueError("group_offsets must have one entry more than prefix_lens")
+    return prefix_lens.shape[0]
+
+
+def gdn_paged_attn_shared_workspace_bytes(shape: GdnCacheShape, n_groups: int, max_group_new: int) -> int:
+    return int(load().gdn_paged_attn_shared_workspace_bytes(ctypes.byref(shape), int(n_groups), int(max_group_new)))
+
+
+def gdn_paged_attn_shared(q, k_cache, v_cache, page_table, seq_lens, group_offsets, prefix_lens, cu_seqlens=None,
+                          max_group_new=None, scale=None, want_lse=False, o=None, lse=None, simt=False, workspace=None,
+                          stream=None, _test_no_wait=False):
+    """gdn_paged_attn where groups of sequences share a prefix: sequences group_offsets[g] .. group_offsets[g + 1] - 1 hold
+    the same tokens in their first prefix_lens[g] positions (device int32 [n_groups + 1], from 0 to n_seqs, and
+    [n_groups]), which are read once for the group, from its first sequence's pages.  max_group_new: a bound on
+    the new tokens of one group (default: all of them).  Returns (o, lse or None) as gdn_paged_attn, without gradients."""
+
+    def make():
+        _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
+        n_groups = _groups(group_offsets, prefix_lens)
+        sh = cache_shape(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
+        if o is not None and (o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous()):
+            raise ValueError("o must be contiguous with q's shape and dtype")
+        if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+            raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
+        new = sh.n_tok if max_group_new is None else max_group_new
+        if workspace is None:
+            sh.status = _status_words(q.get_device())
+        return sh, ctypes.addressof(sh), n_groups, new, gdn_paged_attn_shared_workspace_bytes(sh, n_groups, new), sh.D ** -0.5
+
+    _, shape, n_groups, new, nbytes, unit = _plan(
+        ("shared", max_group_new, workspace is None,
+         _lays(q, k_cache, v_cache, page_table, seq_lens, group_offsets, prefix_lens, cu_seqlens, o, lse)), make)
+    if o is None:
+        o = _empty(q, 3, False, stream)
+    if lse is None and want_lse:
+        lse = _empty(q, 2, True, stream)
+    flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
+    _call("gdn_paged_attn_shared", q, nbytes, workspace, stream, q, k_cache, v_cache, page_table, seq_lens, cu_seqlens,
+          group_offsets, prefix_lens, n_groups, shape, new, unit if scale is None else scale, flags, o, lse)
+    return o, lse
+
+
 def gdn_pages_workspace_bytes(n_pages: int, n_rows: int) -> int:
     return int(load().gdn_pages_workspace_bytes(int(n_pages), int(n_rows)))
 
@@ -479,3 +528,60 @@ def gdn_pages_copy(pools, src, dst, workspace=None, stream=None):
     st = _entry("gdn_pages_copy")(src, dst, n, n_pages, p, buf, nbytes, _handle(src, stream))
     if st:
         _check(st, "gdn_pages_copy")
+
+
+def gdn_pages_evict_workspace_bytes(n_pages: int, n_rows: int, max_pages: int, n: int, max_keep: int, n_layers: int,
+                                    heads: int) -> int:
+    t = GdnPageTables(n_rows=int(n_rows), max_pages=int(max_pages), n_pages=int(n_pages))
+    return int(load().gdn_pages_evict_workspace_bytes(ctypes.byref(t), int(n), int(max_keep), int(n_layers), int(heads)))
+
+
+def gdn_pages_evict(page_table, seq_lens, refs, seqs, keep, mass, pools, page_size, max_keep, recent=0, want_kept=False,
+                    workspace=None, stream=None):
+    """Sequences `seqs` are cut to `keep` tokens (device int32 lists, at most max_keep) where they have more: in each layer
+    and for each kv head the last `recent` positions stay and those of the others with the largest mass (fp32
+    [n_layers, n_rows, heads, length]; ties to the lowest position), moved in their order to fresh pages.
+    pools: each layer's [n_pages, page_size, heads, D] caches in turn (k0, v0, k1, v1, ...).  Masses move along, the tables
+    follow.  Returns the positions that stayed, int32 [n_layers, n, heads, max_keep] filled up with -1, or None without
+    want_kept.  Nothing changes, and nothing is returned that means anything, if a list cannot be carried out or the free
+    pages do not suffice: GDN_ERR_PAGES, as for gdn_pages_grow."""
+    pools = tuple(pools)
+    t, n, _ = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs", "keep"), seqs, keep)
+    p, _keep = _page_pools(pools, refs.shape[0])
+
+    def make():
+        _need_cuda(mass)
+        if mass.dtype != torch.float32 or mass.dim() != 4 or (mass.shape[3] > 1 and mass.stride(3) != 1):
+            raise TypeError("mass must be fp32 [n_layers, n_rows, heads, length] with contiguous rows")
+        n_layers, n_rows, heads, length = mass.shape
+        if n_rows != page_table.shape[0]:
+            raise ValueError("mass must have one row a row of page_table")
+        if n_layers == 0 or len(pools) % n_layers:
+            raise ValueError("the pools must be as many for each of mass's layers")
+        st = [max(s, length) if k == 1 else s for s, k in zip(mass.stride()[:3], mass.shape[:3])]
+        if any(s < length for s in st):
+            raise ValueError("mass's rows overlap (a broadcast tensor?): use .contiguous()")
+        row_bytes = slot = head = 1
+        if pools:
+            x = pools[0]
+            if any(c.dim() != 4 or c.shape[1:3] != (page_size, heads) or c.shape[3] != x.shape[3] or c.dtype != x.dtype
+                   or (c.shape[3] > 1 and c.stride(3) != 1) or c.stride()[1:3] != x.stride()[1:3] for c in pools):
+                raise ValueError("the pools must be [n_pages, page_size, heads, D] with the same strides")
+            row_bytes = x.shape[3] * x.element_size()
+            slot, head = (s * x.element_size() for s in x.stride()[1:3])
+            slot, head = slot if page_size > 1 else row_bytes, head if heads > 1 else row_bytes
+        tail = bytes(GdnPageHeads(None, n_layers, heads, length, *st, row_bytes, slot, head))
+        nbytes = gdn_pages_evict_workspace_bytes(refs.shape[0], n_rows, page_table.shape[1], n, max_keep, n_layers, heads)
+        return tail[ctypes.sizeof(ctypes.c_void_p):], (n_layers, n, heads, max_keep), nbytes
+
+    tail, shape, nbytes = _plan(("evict", page_size, max_keep, _lays(page_table, refs, seqs, mass), _lays(*pools)), make)
+    kept = None
+    if want_kept:
+        if stream is None:
+            kept = torch.empty(shape, dtype=torch.int32, device=mass.device)
+        else:
+            with torch.cuda.stream(_as_stream(mass, stream)):
+                kept = torch.empty(shape, dtype=torch.int32, device=mass.device)
+    _call("gdn_pages_evict", page_table, nbytes, workspace, stream, t, seqs, keep, n, max_keep, recent,
+          _pack(tail, mass), p, kept)
+    return kept

@@ -470,6 +470,24 @@ gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cach
                           int32_t max_new, float scale, int32_t window, uint32_t flags, void *o, float *lse,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* gdn_paged_attn where groups of sequences share a prefix (many samples of one prompt, beams after a fork): the same o
+ * and lse, the prefix's K and V read once for all rows of its group.
+ *   group_offsets: [n_groups + 1] device int32, first 0, last n_seqs: group g is sequences [group_offsets[g],
+ *   group_offsets[g + 1]) of the call, possibly none;  prefix_lens: [n_groups] device int32 (0: nothing is shared): the
+ *   first prefix_lens[g] positions of each of the group's sequences hold the same tokens.  They are read from the
+ *   pages of the group's first sequence; the others' pages (shared or copies of their own) only behind them.
+ *   prefix_lens[g] is at most the length of each of the group's sequences that has new tokens, and of its first.
+ *   A new token may itself lie in the prefix; it sees it up to its own position.
+ *   max_group_new: the host's bound on the new tokens of one group (it picks the kernel; more are still right)
+ * Offsets or lengths that are none of this set GDN_ERR_BOUNDS; the results of those groups are then unspecified.
+ * The other arguments, types and kernels are gdn_paged_attn's without a window.  n_groups up to 2^28. */
+size_t gdn_paged_attn_shared_workspace_bytes(const gdn_cache_shape *shape, int32_t n_groups, int32_t max_group_new);
+gdn_status gdn_paged_attn_shared(const void *q, const void *k_cache, const void *v_cache, const int32_t *page_table,
+                                 const int32_t *seq_lens, const int32_t *cu_seqlens, const int32_t *group_offsets,
+                                 const int32_t *prefix_lens, int32_t n_groups, const gdn_cache_shape *shape,
+                                 int32_t max_group_new, float scale, uint32_t flags, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
 /* The bookkeeping of the pages, all on the device: page_table [n_rows, max_pages], seq_lens
  * [n_rows], refs [n_pages] (how many sequences hold a page; 0 = free).  Free pages are taken
  * in rising order, so the results do not depend on scheduling.  The calls below check their
@@ -524,6 +542,34 @@ gdn_status gdn_pages_compact(const gdn_page_tables *t, const gdn_page_pools *poo
  * in dst, none twice in dst; pairs with a page outside [0, n_pages) set GDN_ERR_BOUNDS and are skipped). */
 gdn_status gdn_pages_copy(const int32_t *src, const int32_t *dst, int32_t n, int32_t n_pages,
                           const gdn_page_pools *pools, void *workspace, size_t workspace_bytes, void *stream);
+
+/* What gdn_pages_evict has to know of the weights and of a page's rows. */
+typedef struct {
+  float *mass;  /* device: [n_layers][n_rows of the tables][heads][mass_len] accumulated weights */
+  int32_t n_layers, heads, mass_len;
+  int64_t layer_stride, row_stride, head_stride; /* elements of mass; all 0 = dense */
+  int64_t row_bytes;                     /* one head's row of one slot in a pool (D elements), at most 65536 */
+  int64_t slot_stride, slot_head_stride; /* bytes between a page's slots and between a slot's heads; both 0 = dense
+                                          * [page_size][heads][row_bytes] */
+} gdn_page_heads;
+
+/* Eviction by accumulated weight: sequence seqs[i] (i < n, no row twice) is cut to keep[i] tokens (0 .. max_keep) where
+ * it has more, in every layer and for every kv head on its own: its last min(recent, keep[i]) positions stay, and of
+ * those before them the ones with the largest mass, ties to the lowest position, NaN below every number.  In rising
+ * order they become its positions 0 .. keep[i] - 1.  They move, with their masses, into fresh pages (free ones, in rising
+ * order, sequence after sequence), so sequences that share the old pages keep theirs; the old pages' refs go down by
+ * one, and masses from keep[i] up to the old length become 0.  Rotary positions lie in the keys and stay what they were:
+ * append later tokens with explicit positions.
+ *   pools: n_pools a multiple of n_layers: pool j belongs to layer j / (n_pools / n_layers) (k and v caches: k0 v0 k1 v1 ...)
+ *   kept: [n_layers][n][heads][max_keep] int32 out or NULL: the positions that stay, then -1
+ * A list that cannot be carried out (a row outside the tables or twice, keep[i] outside [0, max_keep], an entry of -1 in
+ * use, too few free pages) sets GDN_ERR_PAGES, a page outside the cache or a length past mass_len GDN_ERR_BOUNDS; then
+ * nothing changes.  workspace: gdn_pages_evict_workspace_bytes(t, n, max_keep, n_layers, heads), 256-byte aligned. */
+size_t gdn_pages_evict_workspace_bytes(const gdn_page_tables *t, int32_t n, int32_t max_keep, int32_t n_layers,
+                                       int32_t heads);
+gdn_status gdn_pages_evict(const gdn_page_tables *t, const int32_t *seqs, const int32_t *keep, int32_t n,
+                           int32_t max_keep, int32_t recent, const gdn_page_heads *heads, const gdn_page_pools *pools,
+                           int32_t *kept, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
