@@ -127,6 +127,9 @@ _SIGS = {
     "gdn_paged_attn_shared_workspace_bytes": ([_P, _I32, _I32], _SZ),
     "gdn_paged_attn_shared": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I32, _F32, _U32, _P, _P, _P, _SZ, _P],
                               ctypes.c_int),
+    "gdn_paged_mass_workspace_bytes": ([_P], _SZ),
+    "gdn_paged_mass": ([_P, _P, _P, _P, _P, _P, _P, _I32, _F32, _I32, _I32, _U32, _P, _I64, _I64, _I32, _P, _SZ, _P],
+                       ctypes.c_int),
     "gdn_pages_evict_workspace_bytes": ([_P, _I32, _I32, _I32, _I32], _SZ),
     "gdn_pages_evict": ([_P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
 }
@@ -614,8 +617,7 @@ def segment_parallel_fwd(q, k, v, g, beta, seg_bounds, h0=None, scale=None, l2no
 
 # full attention over a paged cache
 from .paged import (cache_shape, gdn_kv_append, gdn_paged_attn, gdn_paged_attn_shared,  # noqa: E402,F401
-                    gdn_paged_attn_shared_workspace_bytes, gdn_paged_attn_workspace_bytes, gdn_pages_compact,
+                    gdn_paged_attn_shared_workspace_bytes, gdn_paged_attn_workspace_bytes, gdn_paged_mass,
+                    gdn_paged_mass_workspace_bytes, gdn_paged_status, gdn_paged_status_reset, gdn_pages_compact,
                     gdn_pages_copy, gdn_pages_evict, gdn_pages_evict_workspace_bytes, gdn_pages_fork, gdn_pages_free,
-                    gdn_pages_grow,
-                    gdn_pages_workspace_bytes, gdn_paged_status, gdn_paged_status_reset, gdn_rope, gdn_rope_freqs,
-                    gdn_rope_inv_freq)
+                    gdn_pages_grow, gdn_pages_workspace_bytes, gdn_rope, gdn_rope_freqs, gdn_rope_inv_freq)

@@ -194,6 +194,7 @@ PyMethodDef methods[] = {
     GDN_ENTRY(gdn_kv_append),
     GDN_ENTRY_SCRATCH(gdn_paged_attn),
     GDN_ENTRY_SCRATCH(gdn_paged_attn_shared),
+    GDN_ENTRY_SCRATCH(gdn_paged_mass),
     GDN_ENTRY_SCRATCH(gdn_pages_grow),
     GDN_ENTRY(gdn_pages_free),
     GDN_ENTRY_SCRATCH(gdn_pages_fork),

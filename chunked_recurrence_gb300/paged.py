@@ -63,8 +63,8 @@ def _plan(key, make):
 
 
 _entries = {}
-_TAKE_SCRATCH = ("gdn_paged_attn", "gdn_paged_attn_shared", "gdn_pages_grow", "gdn_pages_fork", "gdn_pages_compact",
-                 "gdn_pages_evict")
+_TAKE_SCRATCH = ("gdn_paged_attn", "gdn_paged_attn_shared", "gdn_paged_mass", "gdn_pages_grow", "gdn_pages_fork",
+                 "gdn_pages_compact", "gdn_pages_evict")
 
 
 def _entry(name):
@@ -423,6 +423,44 @@ def gdn_paged_attn_shared(q, k_cache, v_cache, page_table, seq_lens, group_offse
     _call("gdn_paged_attn_shared", q, nbytes, workspace, stream, q, k_cache, v_cache, page_table, seq_lens, cu_seqlens,
           group_offsets, prefix_lens, n_groups, shape, new, unit if scale is None else scale, flags, o, lse)
     return o, lse
+
+
+def gdn_paged_mass_workspace_bytes(shape: GdnCacheShape) -> int:
+    return int(load().gdn_paged_mass_workspace_bytes(ctypes.byref(shape)))
+
+
+def gdn_paged_mass(q, k_cache, page_table, seq_lens, lse, mass, cu_seqlens=None, max_new=None, scale=None, window=0,
+                   accumulate=True, simt=False, workspace=None, stream=None, _test_no_wait=False):
+    """The softmax weight that each cached position gets from the new tokens q [n_tok, Hq, D] whose attention left lse
+    [n_tok, Hq] (fp32), summed over them and the heads of a kv head's group: added to mass [n_seqs, Hkv, length] (fp32,
+    contiguous rows), or with accumulate=False written over it, up to each sequence's length.  Other arguments as for
+    gdn_paged_attn.  Returns mass, without gradients."""
+
+    def make():
+        _need_cuda(q, k_cache, page_table, seq_lens, cu_seqlens, lse, mass)
+        sh = cache_shape(q, k_cache, k_cache, page_table, seq_lens, cu_seqlens)
+        if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [n_tok, Hq]")
+        if mass.dtype != torch.float32 or mass.dim() != 3 or (mass.shape[2] > 1 and mass.stride(2) != 1):
+            raise TypeError("mass must be fp32 [n_seqs, Hkv, length] with contiguous rows")
+        if mass.shape[:2] != (sh.n_seqs, sh.Hkv):
+            raise ValueError("mass must have a row a sequence and kv head")
+        length = mass.shape[2]
+        st = [length if n == 1 else s for n, s in zip(mass.shape, mass.stride()[:2])]
+        if any(s < length for s in st):
+            raise ValueError("mass's rows overlap (a broadcast tensor?): use .contiguous()")
+        new = max_new if max_new is not None else sh.n_tok if cu_seqlens is not None else 1
+        if workspace is None:
+            sh.status = _status_words(q.get_device())
+        return sh, ctypes.addressof(sh), new, (*st, length), gdn_paged_mass_workspace_bytes(sh), sh.D ** -0.5
+
+    _, shape, new, rows, nbytes, unit = _plan(
+        ("mass", max_new, workspace is None,
+         _lays(q, k_cache, page_table, seq_lens, lse, mass, cu_seqlens)), make)
+    flags = (GDN_FLAG_SIMT if simt else 0) | (GDN_FLAG_TEST_NO_WAIT if _test_no_wait else 0)
+    _call("gdn_paged_mass", q, nbytes, workspace, stream, q, k_cache, page_table, seq_lens, cu_seqlens, lse, shape, new,
+          unit if scale is None else scale, window, 1 if accumulate else 0, flags, mass, *rows)
+    return mass
 
 
 def gdn_pages_workspace_bytes(n_pages: int, n_rows: int) -> int:

@@ -488,6 +488,28 @@ gdn_status gdn_paged_attn_shared(const void *q, const void *k_cache, const void 
                                  int32_t max_group_new, float scale, uint32_t flags, void *o, float *lse,
                                  void *workspace, size_t workspace_bytes, void *stream);
 
+/* The attention weight that cached positions get from new tokens, by kv head, as eviction goes by it: with the lse of
+ * gdn_paged_attn (or gdn_paged_attn_shared) of the same tokens and scale, new token i of sequence s at position
+ * p = seq_lens[s] - n_new + i,
+ *     mass[s, h, j] (+)= sum_{i: max(0, p - window + 1) <= j <= p} sum_{g in h's group} exp(scale <q[i, g], k_j> - lse[i, g])
+ * for j < seq_lens[s]: added to what is there with accumulate 1 (0: written, 0 where no token sees j).  Entries from
+ * seq_lens[s] on stay as they are.  Heads whose lse is -inf (they see nothing) weigh nothing.
+ *   q, page_table, seq_lens, cu_seqlens, shape, window: as for gdn_paged_attn (v is not read);  max_new: the
+ *   host's bound on the new tokens of one sequence (it picks the kernel; more are still right)
+ *   lse: [n_tok, Hq] fp32 dense;  mass: [n_seqs, Hkv, mass_len] fp32, row_stride and head_stride elements apart, both 0 =
+ *   dense.  A length past mass_len sets GDN_ERR_BOUNDS; what lies past it is then not written.
+ *   flags: GDN_FLAG_SIMT (the kernel without tcgen05), GDN_FLAG_TEST_NO_WAIT
+ *   workspace: gdn_paged_mass_workspace_bytes(shape), 256-byte aligned, not shared by calls that may overlap.
+ * Scores, weights and sums are fp32, added in a fixed order: the same call gives the same bits.  bf16, D 64, 128 or 256,
+ * page_size a multiple of 8 up to 2^20, Hq / Hkv up to 128, 16-byte aligned pointers and strides: tcgen05; everything else:
+ * products of fp32's precision on the tensor cores (each operand in two TF32 parts). */
+size_t gdn_paged_mass_workspace_bytes(const gdn_cache_shape *shape);
+gdn_status gdn_paged_mass(const void *q, const void *k_cache, const int32_t *page_table, const int32_t *seq_lens,
+                          const int32_t *cu_seqlens, const float *lse, const gdn_cache_shape *shape, int32_t max_new,
+                          float scale, int32_t window, int32_t accumulate, uint32_t flags, float *mass,
+                          int64_t row_stride, int64_t head_stride, int32_t mass_len, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
 /* The bookkeeping of the pages, all on the device: page_table [n_rows, max_pages], seq_lens
  * [n_rows], refs [n_pages] (how many sequences hold a page; 0 = free).  Free pages are taken
  * in rising order, so the results do not depend on scheduling.  The calls below check their
