@@ -29,14 +29,6 @@ struct Cfg {
   static constexpr int kBlocks = DP == 256 ? 1 : DP == 128 ? 3 : 6;  // of an SM, by their shared memory
 };
 
-// Rows of the piece's queries (counted from the tile's first) that see position pos.
-__device__ __forceinline__ void rows_of(const MassArgs &a, const MassWalk &w, int pos, int &lo, int &hi) {
-  const int i0 = max(pos - w.m.first, w.i0);
-  const int64_t i1 = a.window > 0 ? min((int64_t)w.m.sp.n_new, (int64_t)pos - w.m.first + a.window) : w.m.sp.n_new;
-  lo = (i0 - w.i0) * a.G;
-  hi = i1 > w.i0 ? (int)(min(i1, (int64_t)w.i1) - w.i0) * a.G : 0;
-}
-
 template <typename T>
 __device__ __forceinline__ int64_t place_of(const MassArgs &a, const MassWalk &w, int pos) {
   const int page = page_of(a.table + w.s * a.table_stride, pos, a.page_size, a.max_pages, a.n_pages);
@@ -61,8 +53,8 @@ __device__ __noinline__ void plain_sums(const MassArgs &a, const MassWalk &w, fl
   for (int p = threadIdx.x >> 5; p < kBP; p += kThreads / 32) {
     const int pos = (w.m.tile0 + w.j) * kBP + p;
     int lo, hi;
-    rows_of(a, w, pos, lo, hi);
-    const int64_t at = pos >= w.m.lo && pos < w.m.hi ? place_of<T>(a, w, pos) : -1;
+    mass_rows(a, w, pos, lo, hi);
+    const int64_t at = pos >= w.m.seen && pos < w.m.hi ? place_of<T>(a, w, pos) : -1;
     float sum = 0.f;
     for (int r = max(lo, w.q0 * kRQ); r < min(hi, (w.q0 + w.n) * kRQ) && at >= 0; ++r) {
       const T *q = query_of<T>(a, w, r), *k = (const T *)a.k + at;
@@ -127,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) paged_mass_kernel(const MassArgs a, 
         const int r = i / (DP / 4), col = (i - r * (DP / 4)) * 4, pos = pos0 + r;
         float *to = ks + r * C::kPitch + col;
         int64_t at = -1;
-        if (pos >= w.m.lo && pos < w.m.hi && col < a.D) {
+        if (pos >= w.m.seen && pos < w.m.hi && col < a.D) {
           at = place_of<T>(a, w, pos);
           if (at < 0) set_status(a.status, GDN_ERR_BOUNDS);
         }
@@ -139,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) paged_mass_kernel(const MassArgs a, 
     int lo[2], hi[2];
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) rows_of(a, w, pos0 + m0 + g4 + 8 * e, lo[e], hi[e]);
+    for (int e = 0; e < 2; ++e) mass_rows(a, w, pos0 + m0 + g4 + 8 * e, lo[e], hi[e]);
     for (int t = 0; t < w.n; ++t) {
       cp_async_wait_all();
       __syncthreads();  // this tile is there, the one before done with
@@ -210,7 +202,7 @@ gdn_status launch(MassArgs &a, bool wide, void *workspace, cudaStream_t st) {
   const int shares = 152 * Cfg<DP>::kBlocks;
   a.meta = (int4 *)((char *)workspace + 256);
   a.part = (float *)(a.meta + 2 * shares);
-  return mass_launch<kBP>(paged_mass_kernel<T, DP>, a, wide, shares, kThreads, Cfg<DP>::kSmem, st);
+  return mass_launch<kBP>(paged_mass_kernel<T, DP>, a, shares, kThreads, Cfg<DP>::kSmem, st, a, wide);
 }
 size_t plain_workspace() { return 256 + 152 * 6 * (2 * sizeof(int4) + 2 * kBP * sizeof(float)); }
 

@@ -14,6 +14,7 @@ struct MassSeq {
   SeqSpan sp;
   int32_t first;          // position of the first new token (may be negative)
   int32_t lo, hi;         // positions [lo, hi) that are written
+  int32_t seen;           // the first position that some query sees: none before it is read
   int32_t tile0, n_tiles; // tiles of BP that hold them
   bool ok;
 };
@@ -26,10 +27,10 @@ GDN_HD MassSeq mass_seq(const PagedSeqs &q, int32_t s, int32_t BP, int32_t windo
   m.first = m.sp.len - m.sp.n_new;
   m.hi = m.sp.len < room ? m.sp.len : room;
   m.lo = 0;
+  m.seen = window > 0 && m.first >= window ? m.first - window + 1 : 0;
   if (!all) {
     if (m.sp.n_new == 0) m.hi = 0;
-    if (window > 0 && m.first >= window) m.lo = m.first - window + 1;
-    if (m.lo > m.hi) m.lo = m.hi;
+    m.lo = m.seen < m.hi ? m.seen : m.hi;
   }
   m.tile0 = m.lo / BP;
   m.n_tiles = m.lo < m.hi ? (m.hi + BP - 1) / BP - m.tile0 : 0;
@@ -116,6 +117,15 @@ struct MassWalk {
 };
 GDN_HD bool mass_begins(const MassWalk &w) { return w.q0 == 0; }
 GDN_HD bool mass_ends(const MassWalk &w) { return w.q0 + w.n == w.nq; }
+
+// Rows [lo, hi) of the tile's queries, counted from its first, that see position pos.
+GDN_HD void mass_rows(const MassArgs &a, const MassWalk &w, int32_t pos, int32_t &lo, int32_t &hi) {
+  const int32_t i0 = pos - w.m.first > w.i0 ? pos - w.m.first : w.i0;
+  int64_t i1 = w.i1;
+  if (a.window > 0 && (int64_t)pos - w.m.first + a.window < i1) i1 = (int64_t)pos - w.m.first + a.window;
+  lo = (i0 - w.i0) * a.G;
+  hi = i1 > w.i0 ? (int32_t)(i1 - w.i0) * a.G : 0;
+}
 
 // cuts the next piece at unit u of the tile; false where it holds nothing to do
 template <int BP, int OVER>
@@ -269,9 +279,9 @@ __global__ void __launch_bounds__(BP) mass_join_kernel(const MassArgs a, int sha
 }
 
 // A launch that starts under the end of the kernel before on the stream, and the join behind it.
-template <int BP>
-gdn_status mass_launch(void (*kernel)(MassArgs, bool), const MassArgs &a, bool flag, int shares, int threads, size_t smem,
-                       cudaStream_t st) {
+template <int BP, typename... P, typename... A>
+gdn_status mass_launch(void (*kernel)(P...), const MassArgs &a, int shares, int threads, size_t smem, cudaStream_t st,
+                       A... args) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   cudaLaunchAttribute attr = {};
@@ -280,7 +290,7 @@ gdn_status mass_launch(void (*kernel)(MassArgs, bool), const MassArgs &a, bool f
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(shares), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, a, flag);
+  cudaLaunchKernelEx(&cfg, kernel, args...);
   cfg.blockDim = dim3(BP), cfg.dynamicSmemBytes = 0;
   cudaLaunchKernelEx(&cfg, mass_join_kernel<BP>, a, shares);
   return launch_status();

@@ -354,3 +354,41 @@ def test_two_threads(crg):
         t.join()
     torch.cuda.synchronize()
     assert not failed and wrong.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_never_reads_released_pages(crg, dtype, accumulate):
+    """Pages wholly before every query's window may be given back (-1 in the table)."""
+    cache = Cache(130, dtype, [1000, 600], 2, 128, 16)
+    q = randn(gen(131), (31, 4, 128), dtype)
+    new, cu = [30, 1], cu_of([30, 1])
+    _, lse = crg.gdn_paged_attn(q, cache.k, cache.v, cache.table, cache.lens, cu, window=200, want_lse=True)
+    table = cache.table.clone()
+    for s, (n, m) in enumerate(((30, 1000), (1, 600))):
+        table[s, : max(0, m - n - 200 + 1) // 16] = -1
+    ws = crg.Workspace(1 << 26, DEV)
+    mass = torch.rand((2, 2, 1000), generator=gen(132), device=DEV)
+    before = mass.clone()
+    crg.gdn_paged_mass(q, cache.k, table, cache.lens, lse, mass, cu, window=200, accumulate=accumulate, workspace=ws)
+    assert ws.status() == 0
+    ref, tol = reference(q, lse, cache, new, 200, 128 ** -0.5, before, accumulate)
+    assert np.all(np.abs(f64(mass) - ref) <= tol)
+
+
+@pytest.mark.parametrize("max_new", [1, 300])
+def test_wait_that_runs_out_is_reported(crg, max_new):
+    """The test mode gives up at the first wait: the status says so and the context stays usable."""
+    cache = Cache(133, "bf16", [300, 200], 2, 128, 16)
+    q, mass = randn(gen(134), (2, 8, 128), "bf16"), torch.zeros((2, 2, 300), device=DEV)
+    _, lse = crg.gdn_paged_attn(q, cache.k, cache.v, cache.table, cache.lens, want_lse=True)
+    ws = crg.Workspace(1 << 26, DEV)
+    call = lambda **kw: crg.gdn_paged_mass(q, cache.k, cache.table, cache.lens, lse, mass, max_new=max_new,  # noqa: E731
+                                           accumulate=False, workspace=ws, **kw)
+    call(_test_no_wait=True)
+    assert ws.status() == crg.GDN_ERR_TIMEOUT
+    ws.reset()
+    call()
+    assert ws.status() == 0
+    ref, tol = reference(q, lse, cache, [1, 1], 0, 128 ** -0.5, torch.zeros_like(mass), False)
+    assert np.all(np.abs(f64(mass) - ref) <= tol)
