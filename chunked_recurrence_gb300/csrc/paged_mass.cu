@@ -1,8 +1,8 @@
 // paged_mass.cu -- gdn_paged_mass: the softmax weight that each cached position gets from new tokens, by their attention's
 // log-sum-exp:
 //     mass[s, h, j] (+)= sum over new tokens i of s that see j, heads g of kv head h's group, of e^(scale <q[i, g], k_j> - lse[i, g])
-// Argument checks, dispatch, and the kernel for every type, width, page size, stride and alignment (paged_mass_tc.cu has the
-// one on tcgen05).
+// Argument checks, dispatch, and the kernel for every type, width, page size, stride and alignment (bf16 of D 64, 128 and 256:
+// paged_mass_tc.cu on tcgen05, paged_mass_few.cu for few query rows).
 //
 // A block takes equal parts of the line of work (paged_mass.cuh): 64 positions of a sequence and kv head, whose keys stay in
 // shared memory as fp32 while their queries come by, 32 rows a tile, the next tile's copies under this one's
@@ -202,7 +202,7 @@ gdn_status launch(MassArgs &a, bool wide, void *workspace, cudaStream_t st) {
   const int shares = 152 * Cfg<DP>::kBlocks;
   a.meta = (int4 *)((char *)workspace + 256);
   a.part = (float *)(a.meta + 2 * shares);
-  return mass_launch<kBP>(paged_mass_kernel<T, DP>, a, shares, kThreads, Cfg<DP>::kSmem, st, a, wide);
+  return mass_launch<kBP>(paged_mass_kernel<T, DP>, a, shares, shares, kThreads, Cfg<DP>::kSmem, st, a, wide);
 }
 size_t plain_workspace() { return 256 + 152 * 6 * (2 * sizeof(int4) + 2 * kBP * sizeof(float)); }
 
@@ -222,7 +222,7 @@ extern "C" size_t gdn_paged_mass_workspace_bytes(const gdn_cache_shape *shape) {
   gdn_cache_shape s;
   static const int32_t some = 0;
   if (normalise_cache_shape(shape, &some, &s) != GDN_OK) return 0;
-  return std::max(plain_workspace(), paged_mass_tc_workspace(s));
+  return std::max({plain_workspace(), paged_mass_tc_workspace(s), paged_mass_few_workspace()});
 }
 
 extern "C" gdn_status gdn_paged_mass(const void *q, const void *k_cache, const int32_t *page_table,
@@ -256,7 +256,9 @@ extern "C" gdn_status gdn_paged_mass(const void *q, const void *k_cache, const i
   a.RQ = kRQ, a.c = scale * 1.44269504088896340736f;
   a.status = s.status ? s.status : (int32_t *)workspace;
   if (!(flags & GDN_FLAG_SIMT) && s.n_tok > 0 && paged_mass_tc_supported(s, q, k_cache))
-    return paged_mass_tc(a, s, max_new, flags, workspace, st);
+    return paged_mass_few(a, max_new) && !(flags & GDN_FLAG_TEST_NO_WAIT)  // that kernel has no waits to test
+               ? paged_mass_few_run(a, max_new, workspace, st)
+               : paged_mass_tc(a, s, flags, workspace, st);
   bool wide = s.D % 4 == 0 && aligned(q, 16) && aligned(k_cache, 16);
   for (int64_t x : {s.q_stride, s.page_stride, s.slot_stride, s.head_stride}) wide = wide && x % 4 == 0;
   return s.dtype == GDN_BF16 ? dispatch<__nv_bfloat16>(a, wide, workspace, st) : dispatch<float>(a, wide, workspace, st);

@@ -51,7 +51,7 @@ GDN_HD void mass_tokens(const MassSeq &m, int32_t pos, int32_t BP, int32_t windo
 GDN_HD int32_t mass_tiles(const MassSeq &m, int32_t j, int32_t BP, int32_t window, int32_t G, int32_t RQ) {
   int32_t i0, i1;
   mass_tokens(m, (m.tile0 + j) * BP, BP, window, i0, i1);
-  return (int32_t)(((int64_t)(i1 - i0) * G + RQ - 1) / RQ);
+  return ((i1 - i0) * G + RQ - 1) / RQ;  // the call checked that n_tok * G is below 2^30
 }
 // How many tiles from the j-th on have as many query tiles as it (at least it): without a window all up to the first new
 // token's, with one all that end before the first that some query sees.
@@ -101,6 +101,7 @@ struct MassArgs {
   int64_t table_stride, page_stride, slot_stride, head_stride, q_stride;
   int64_t row_stride, mass_head_stride;  // of mass
   int32_t G, Hkv, D, page_size, max_pages, n_pages, window, room, all, RQ;
+  int32_t tokens, page_mask;             // RQ / G, where that is whole; page_size - 1, or -1 where that is no power of two
   float c;                               // scale log2 e
   float *part;                           // [shares][2][BP]: sums of tiles that a share does not hold whole
   int4 *meta;                            // [shares][2]: how the share's first piece goes on (1: beyond it, 2: to its tile's
@@ -130,8 +131,9 @@ GDN_HD void mass_rows(const MassArgs &a, const MassWalk &w, int32_t pos, int32_t
 // cuts the next piece at unit u of the tile; false where it holds nothing to do
 template <int BP, int OVER>
 GDN_HD bool mass_cut(const MassArgs &a, MassWalk &w, int32_t u) {
+  const int32_t before = w.i1 - w.i0;
   mass_tokens(w.m, (w.m.tile0 + w.j) * BP, BP, a.window, w.i0, w.i1);
-  w.nq = (int32_t)(((int64_t)(w.i1 - w.i0) * a.G + a.RQ - 1) / a.RQ);
+  if (w.i1 - w.i0 != before || w.nq < 0) w.nq = ((w.i1 - w.i0) * a.G + a.RQ - 1) / a.RQ;  // a division saved, mostly
   const int32_t units = w.nq + OVER;
   const int32_t end = (int32_t)(u + w.left < units ? u + w.left : units);
   w.left -= end - u;
@@ -229,6 +231,7 @@ template <int BP, int OVER>
 __device__ __forceinline__ bool mass_begin(const MassArgs &a, const MassStart &st, int64_t left, MassWalk &w) {
   w.m = st.m;
   w.s = st.s, w.h = st.h, w.j = st.j;
+  w.i0 = w.i1 = 0, w.nq = -1;
   w.left = left;
   return mass_cut<BP, OVER>(a, w, st.u) || mass_next<BP, OVER>(a, w);
 }
@@ -280,26 +283,30 @@ __global__ void __launch_bounds__(BP) mass_join_kernel(const MassArgs a, int sha
 
 // A launch that starts under the end of the kernel before on the stream, and the join behind it.
 template <int BP, typename... P, typename... A>
-gdn_status mass_launch(void (*kernel)(P...), const MassArgs &a, int shares, int threads, size_t smem, cudaStream_t st,
-                       A... args) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+gdn_status mass_launch(void (*kernel)(P...), const MassArgs &a, int blocks, int shares, int threads, size_t smem,
+                       cudaStream_t st, A... args) {
+  if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(shares), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cfg.attrs = &attr, cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, kernel, args...);
-  cfg.blockDim = dim3(BP), cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(shares), cfg.blockDim = dim3(BP), cfg.dynamicSmemBytes = 0;
   cudaLaunchKernelEx(&cfg, mass_join_kernel<BP>, a, shares);
   return launch_status();
 }
 
 bool paged_mass_tc_supported(const gdn_cache_shape &s, const void *q, const void *k);
 size_t paged_mass_tc_workspace(const gdn_cache_shape &s);
-gdn_status paged_mass_tc(MassArgs &a, const gdn_cache_shape &s, int32_t max_new, uint32_t flags, void *workspace,
-                         cudaStream_t st);
+gdn_status paged_mass_tc(MassArgs &a, const gdn_cache_shape &s, uint32_t flags, void *workspace, cudaStream_t st);
+
+// Of the calls that the one on tcgen05 takes, those of few query rows.
+bool paged_mass_few(const MassArgs &a, int32_t max_new);
+size_t paged_mass_few_workspace();
+gdn_status paged_mass_few_run(MassArgs &a, int32_t max_new, void *workspace, cudaStream_t st);
 
 }  // namespace gdn
 #endif

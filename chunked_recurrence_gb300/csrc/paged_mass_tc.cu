@@ -1,14 +1,13 @@
 // paged_mass_tc.cu -- gdn_paged_mass on the tensor cores (tcgen05, bf16; D = 64, 128 or 256).
 //
-// S^T = K Q^T: a tile of 128 positions is the product's rows and stays in shared memory, a tile of up to 128 query rows its
+// S^T = K Q^T: a tile of 128 positions is the product's rows and stays in shared memory, a tile of up to 256 query rows its
 // columns, so a thread owns a position and adds up 2^(c S - lse) over the columns, c = scale log2 e: no weight leaves
-// the registers, nothing is added between threads but the two warpgroups' sums.
+// the registers, nothing is added between threads but the warpgroups' sums.
 //
-// Warps: two softmax warpgroups, which take the query tiles in turn from four TMEM slots of 128 columns; a warp for K's copies
-// (pages by their table entries), one for Q's (whole tokens with the heads of the group), an MMA thread, and a warp that lays
-// the rows' lse out beside the slots.  K and Q each have a ring of granules of 128 columns of a tile.
-//
-// FEW: up to 64 query rows a sequence and head (single tokens): one query tile a position tile, so K's ring gets the room.
+// Warps: four softmax warpgroups, two for each of two TMEM slots of 256 columns, half of them each; the slots take the
+// steps (a query tile of a position tile) in turn.  A warp for K's copies (pages by their table entries), one for Q's
+// (whole tokens with the heads of the group), an MMA thread, and a warp that lays out beside each slot what its
+// warpgroups have to know of the step, the rows' lse among it.  K and Q each have a ring of panels of 64 columns of a tile.
 #include <cuda.h>
 
 #include <algorithm>
@@ -28,28 +27,40 @@ using namespace sm100;
 
 constexpr int kSms = 152;            // persistent blocks
 constexpr uint32_t kSpin = 1u << 22; // polls of a wait before it gives up
-constexpr int kData = 222 * 1024;    // the rings
-constexpr int kBP = 128, kOver = 1, kThreads = 384, kBufs = 4;
+constexpr int kData = 218 * 1024;    // the rings
+constexpr int kBP = 128, kNQ = 256, kOver = 1, kGroups = 4, kThreads = 128 * kGroups + 128;
 
-template <int D, bool FEW>
+template <int D>
 struct Cfg {
-  static constexpr int kHalves = D == 256 ? 2 : 1;       // granules of a tile
-  static constexpr int kPanels = D == 64 ? 1 : 2;        // 64 columns each, of a granule
-  static constexpr int kRowsQ = FEW ? 64 : 128;
-  static constexpr int kPanelK = kBP * 128, kPanelQ = kRowsQ * 128;  // bytes
-  static constexpr int kGranK = kPanels * kPanelK, kGranQ = kPanels * kPanelQ;
-  static constexpr int kSlotsQ = FEW ? 2 * kHalves : D == 64 ? 8 : D == 128 ? 4 : 3;
-  static constexpr int kSlotsK = (kData - kSlotsQ * kGranQ) / kGranK;
+  static constexpr int kPanels = D / 64;                  // of a tile
+  static constexpr int kPanelK = kBP * 128, kPanelQ = kNQ * 128;  // bytes
+  static constexpr int kSlotsQ = 4;
+  static constexpr int kSlotsK = (kData - kSlotsQ * kPanelQ) / kPanelK;
 };
 
+// A step as its warpgroups see it.
+struct Step {
+  int64_t mass;           // where the tile's first position lies in the masses
+  int pos, lo, hi;        // that position; positions that are written
+  int base, n, row0;      // position of the tile's first query token; query tokens; row (of those) of the step's first column
+  int cols, flags;        // columns in use
+  int swap, pad[3];       // number of the exchange of sums
+};
+constexpr int kFirst = 1, kLast = 2;      // of the slot's steps of its piece
+constexpr int kEnds = 4, kAlone = 8;      // the piece's last step; its only one
+constexpr int kWhole = 16, kBegins = 32;  // the piece has all of its tile's steps; the first of them
+
 struct Ctl {
-  uint64_t kfull[16], kempty[16], qfull[8], qempty[8], sfull[kBufs], sempty[kBufs], lready[kBufs], xfull[2], xempty[2], drain;
+  uint64_t kfull[8], kempty[8], qfull[4], qempty[4], sfull[2], sempty[2], lready[2], xfull[2], xempty[2], drain;
   uint32_t tmem;
   volatile int abort;
   MassStart start;
-  alignas(16) float lse[kBufs][128];  // minus the rows' lse in base 2
-  float x[2][128];        // a warpgroup's sums for the other
+  alignas(16) Step step[2];
+  alignas(16) float lse[2][kNQ];    // minus the rows' lse in base 2
+  float x[2][kGroups][128];             // the warpgroups' sums for the one that ends a piece
 };
+
+static_assert(kData + 1024 + sizeof(Ctl) <= 227 * 1024, "shared memory of a block");
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
                                             int c3) {
@@ -90,28 +101,50 @@ struct Ring {
   }
 };
 
-template <int D, bool FEW>
+// The weights 2^(c s + nl) of 32 columns added to the sums, with a mask those of columns [from, end).
+template <bool MASK>
+__device__ __forceinline__ void add_weights(const float (&s)[32], const float *nl, uint64_t c2, int from, int end,
+                                            uint64_t &sum0, uint64_t &sum1) {
+#pragma unroll
+  for (int y = 0; y < 32; y += 4) {
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(nl + y);
+#pragma unroll
+    for (int z = 0; z < 4; z += 2) {
+      const uint64_t x = f2_fma(f2_pack(s[y + z], s[y + z + 1]), c2, z ? l.y : l.x);
+      uint64_t &sum = z ? sum1 : sum0;
+      float e0, e1;
+      f2_unpack(x, e0, e1);
+      e0 = ex2(e0), e1 = ex2(e1);
+      if (MASK) {
+        e0 = y + z >= from && y + z < end ? e0 : 0.f;
+        e1 = y + z + 1 >= from && y + z + 1 < end ? e1 : 0.f;
+      }
+      sum = f2_add(sum, f2_pack(e0, e1));
+    }
+  }
+}
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const MassArgs a,
                          int box_log2, int no_wait) {
-  using C = Cfg<D, FEW>;
-  static_assert(C::kSlotsK >= C::kHalves + 1 && C::kSlotsK <= 16 && C::kSlotsQ <= 8, "rings");
-  static_assert(kBP / 8 * C::kPanels <= 32, "a granule has at most one box a lane");
+  using C = Cfg<D>;
+  static_assert(C::kSlotsK > C::kPanels && C::kSlotsK <= 8 && kBP / 8 <= 32, "rings; a panel has at most one box a lane");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t *ks = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *qs = ks + C::kSlotsK * C::kGranK;
+  uint8_t *qs = ks + C::kSlotsK * C::kPanelK;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, unit = blockIdx.x;
-  constexpr int kWarpK = 8, kWarpQ = 9, kWarpMma = 10, kWarpLse = 11;
+  constexpr int kWarpK = 4 * kGroups, kWarpQ = kWarpK + 1, kWarpMma = kWarpK + 2, kWarpLse = kWarpK + 3;
   launch_dependents();
   grid_dependency_wait();
   if (tid == 0) {
     a.meta[2 * unit] = make_int4(0, 0, 0, 0);
     ctl.abort = 0;
-    for (int i = 0; i < 16; ++i) mbar_init(&ctl.kfull[i], 1), mbar_init(&ctl.kempty[i], 1);
-    for (int i = 0; i < 8; ++i) mbar_init(&ctl.qfull[i], 1), mbar_init(&ctl.qempty[i], 1);
-    for (int i = 0; i < kBufs; ++i) mbar_init(&ctl.sfull[i], 1), mbar_init(&ctl.sempty[i], 4), mbar_init(&ctl.lready[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&ctl.xfull[i], 4), mbar_init(&ctl.xempty[i], 4);
+    for (int i = 0; i < 8; ++i) mbar_init(&ctl.kfull[i], 1), mbar_init(&ctl.kempty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl.qfull[i], 1), mbar_init(&ctl.qempty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl.sfull[i], 1), mbar_init(&ctl.sempty[i], 8), mbar_init(&ctl.lready[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl.xfull[i], 4 * (kGroups - 1)), mbar_init(&ctl.xempty[i], 4);
     mbar_init(&ctl.drain, 1);
     fence_mbar_init();
   }
@@ -147,59 +180,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================= K: page by page
     Ring<C::kSlotsK> ring;
     const int box = 1 << box_log2, nb = kBP >> box_log2;
-    // pages of a tile a lane each, the next piece's asked for before this one's copies
-    auto look_up = [&](const MassWalk &x, bool there) {
-      const int pos = (x.m.tile0 + x.j) * kBP + lane * box;
-      const bool used = there && x.n > 0 && lane < nb && pos < x.m.hi && pos + box > x.m.seen;  // then the table's row holds it
-      const int page = used ? a.table[x.s * a.table_stride + pos / a.page_size] : -1;
-      if (used && (page < 0 || page >= a.n_pages)) {
-        set_status(a.status, GDN_ERR_BOUNDS);
-        return -1;
-      }
-      return page;
+    // Pages ahead of their use: lane l holds the page of box 32 win + l of the sequence, and of box 32 (win + 1) + l, kNone
+    // where no position of the box is read.  The next window's entries are asked for when this one is entered.
+    constexpr int kNone = INT32_MIN;
+    int win = 0, page[2] = {kNone, kNone}, of_s = -1, of_h = -1;
+    auto look_up = [&](int window) {
+      const int64_t pos = (int64_t)(32 * window + lane) * box;
+      const bool used = pos < w.m.hi && pos + box > w.m.seen;  // then the table's row holds it
+      return used ? a.table[w.s * a.table_stride + (int)pos / a.page_size] : kNone;
     };
-    int page = look_up(w, more);
-    while (more && ok) {
-      MassWalk next = w;
-      const bool later = mass_next<kBP, kOver>(a, next);
-      const int ahead = look_up(next, later);
-      if (w.n > 0) {
-        const int i = lane / C::kPanels, p = lane % C::kPanels, at = (w.m.tile0 + w.j) * kBP + i * box;
-        int pg = __shfl_sync(0xffffffffu, page, i);
-        if (i >= nb) pg = -1;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * (uint32_t)box * 128u;
-        for (int half = 0; half < C::kHalves && ok; ++half, ring.step()) {
-          if (!warp_wait(&ctl.kempty[ring.slot], ring.turn ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.kfull[ring.slot], bytes);
-          __syncwarp();
-          if (pg >= 0)
-            tma_load_4d(ks + ring.slot * C::kGranK + p * C::kPanelK + i * box * 128, &tm_k, &ctl.kfull[ring.slot],
-                        64 * (half * C::kPanels + p), at % a.page_size, w.h, pg);
-          issued |= 1u << ring.slot, phase = (phase & ~(1u << ring.slot)) | ring.turn << ring.slot;
-        }
+    for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
+      if (w.n == 0) continue;
+      const int b0 = (w.m.tile0 + w.j) * nb;  // nb divides 32: a tile lies in one window
+      if (w.s != of_s || w.h != of_h || b0 >> 5 > win + 1) {
+        if (w.s != of_s || b0 >> 5 != win) page[0] = look_up(b0 >> 5), page[1] = look_up((b0 >> 5) + 1);
+        of_s = w.s, of_h = w.h, win = b0 >> 5;
+      } else if (b0 >> 5 > win) {
+        ++win;
+        page[0] = page[1], page[1] = look_up(win + 1);
       }
-      w = next, more = later, page = ahead;
+      const int at = (b0 + lane) * box, slot = a.page_mask >= 0 ? at & a.page_mask : at % a.page_size;
+      int pg = page[0];
+      if (pg != kNone && (pg < 0 || pg >= a.n_pages)) set_status(a.status, GDN_ERR_BOUNDS), pg = -1;
+      pg = __shfl_sync(0xffffffffu, pg, (b0 + lane) & 31);
+      if (lane >= nb) pg = -1;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * (uint32_t)box * 128u;
+      for (int p = 0; p < C::kPanels && ok; ++p, ring.step()) {
+        if (!warp_wait(&ctl.kempty[ring.slot], ring.turn ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ctl.kfull[ring.slot], bytes);
+        __syncwarp();
+        if (pg >= 0)
+          tma_load_4d(ks + ring.slot * C::kPanelK + lane * box * 128, &tm_k, &ctl.kfull[ring.slot], 64 * p, slot, w.h, pg);
+        issued |= 1u << ring.slot, phase = (phase & ~(1u << ring.slot)) | ring.turn << ring.slot;
+      }
     }
     if (!ok && lane == 0) fail();
   } else if (warp == kWarpQ) {
     // ================================================= Q: whole tokens with the heads of the group, a box each 64 columns
     if (lane == 0) {
       Ring<C::kSlotsQ> ring;
-      const int tokens = a.RQ / a.G;
-      for (; more && ok; more = mass_next<kBP, kOver>(a, w))
-        for (int t = 0; t < w.n && ok; ++t)
-          for (int half = 0; half < C::kHalves && ok; ++half, ring.step()) {
+      for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
+        int token = w.m.sp.t0 + w.i0 + w.q0 * a.tokens;
+        for (int t = 0; t < w.n && ok; ++t, token += a.tokens)
+          for (int p = 0; p < C::kPanels; ++p, ring.step()) {
             ok = mbar_wait_spin(&ctl.qempty[ring.slot], ring.turn ^ 1, kSpin, abort_flag);
             if (!ok) break;
-            mbar_arrive_expect_tx(&ctl.qfull[ring.slot], C::kPanels * a.RQ * 128);
-            for (int p = 0; p < C::kPanels; ++p)
-              tma_load_3d(qs + ring.slot * C::kGranQ + p * C::kPanelQ, &tm_q, &ctl.qfull[ring.slot],
-                          64 * (half * C::kPanels + p), w.h * a.G, w.m.sp.t0 + w.i0 + (w.q0 + t) * tokens);
+            mbar_arrive_expect_tx(&ctl.qfull[ring.slot], a.RQ * 128);
+            tma_load_3d(qs + ring.slot * C::kPanelQ, &tm_q, &ctl.qfull[ring.slot], 64 * p, w.h * a.G, token);
             issued |= 1u << ring.slot, phase = (phase & ~(1u << ring.slot)) | ring.turn << ring.slot;
           }
+      }
       if (!ok) fail();
     }
   } else if (warp == kWarpMma) {
@@ -207,33 +240,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring<C::kSlotsK> kr;
       Ring<C::kSlotsQ> qr;
-      Ring<kBufs> buf;
+      Ring<2> buf;
       const uint64_t d_k = smem_desc(smem_u32(ks), 16, 1024, 2), d_q = smem_desc(smem_u32(qs), 16, 1024, 2);
       ok = !no_wait;
       for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
-        Ring<C::kSlotsK> k0 = kr;
-        for (int t = 0; t < w.n && ok; ++t, buf.step()) {
+        const Ring<C::kSlotsK> k0 = kr;
+        int left_rows = (w.i1 - w.i0) * a.G - w.q0 * a.RQ;
+        for (int t = 0; t < w.n && ok; ++t, buf.step(), left_rows -= a.RQ) {
           ok = mbar_wait_spin(&ctl.sempty[buf.slot], buf.turn ^ 1, kSpin, abort_flag);
-          const int rows = min(a.RQ, (w.i1 - w.i0) * a.G - (w.q0 + t) * a.RQ);
-          const uint32_t id = idesc_bf16(kBP, (rows + 15) & ~15, false, false);
+          const uint32_t id = idesc_bf16(kBP, (min(a.RQ, left_rows) + 15) & ~15, false, false);
           kr = k0;
-          for (int half = 0; half < C::kHalves && ok; ++half, kr.step(), qr.step()) {
+#pragma unroll 1
+          for (int p = 0; p < C::kPanels && ok; ++p, kr.step(), qr.step()) {
             if (t == 0) ok = mbar_wait_spin(&ctl.kfull[kr.slot], kr.turn, kSpin, abort_flag);
             ok = ok && mbar_wait_spin(&ctl.qfull[qr.slot], qr.turn, kSpin, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dk = d_k + ((kr.slot * C::kGranK) >> 4), dq = d_q + ((qr.slot * C::kGranQ) >> 4);
+            const uint64_t dk = d_k + ((kr.slot * C::kPanelK) >> 4), dq = d_q + ((qr.slot * C::kPanelQ) >> 4);
 #pragma unroll
-            for (int x = 0; x < C::kPanels * 4; ++x)
-              umma_bf16(tm + buf.slot * 128, dk + (((x >> 2) * C::kPanelK + (x & 3) * 32) >> 4),
-                        dq + (((x >> 2) * C::kPanelQ + (x & 3) * 32) >> 4), id, half > 0 || x > 0);
+            for (int x = 0; x < 4; ++x)
+              umma_bf16(tm + buf.slot * kNQ, dk + (x * 32 >> 4), dq + (x * 32 >> 4), id, p > 0 || x > 0);
             umma_commit(&ctl.qempty[qr.slot]);
+            if (t + 1 == w.n) umma_commit(&ctl.kempty[kr.slot]);
           }
-          if (!ok) break;
-          umma_commit(&ctl.sfull[buf.slot]);
+          if (ok) umma_commit(&ctl.sfull[buf.slot]);
         }
-        if (w.n > 0 && ok)
-          for (int half = 0; half < C::kHalves; ++half, k0.step()) umma_commit(&ctl.kempty[k0.slot]);
       }
       if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
         if (!ok) fail();
@@ -242,109 +273,134 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kWarpLse) {
-    // ================================================= the rows' lse, four rows a lane
-    Ring<kBufs> buf;
-    for (; more && ok; more = mass_next<kBP, kOver>(a, w))
-      for (int t = 0; t < w.n && ok; ++t, buf.step()) {
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = (w.q0 + t) * a.RQ + 4 * lane + k, i = r / a.G, g = r - i * a.G;
-          const bool there = 4 * lane + k < a.RQ && r < (w.i1 - w.i0) * a.G;
-          const float x = there ? a.lse[(int64_t)(w.m.sp.t0 + w.i0 + i) * (a.G * a.Hkv) + w.h * a.G + g] : 0.f;
-          v[k] = x == -INFINITY ? x : -x * 1.44269504088896340736f;  // such a row weighs nothing
+    // ================================================= what the warpgroups have to know of the steps: the rows' lse, eight
+    // rows a lane, the next step's on their way, and the step itself
+    Ring<2> buf;
+    const int i8 = 8 * lane / a.G, g8 = 8 * lane - i8 * a.G;  // token and head of a lane's first row
+    float next[8];
+    int t = -1, swaps = 0;
+    auto advance = [&]() {  // to the next step, whose lse is asked for; false where there is none
+      for (++t; more && t >= w.n; t = 0) {
+        if (w.n == 0 && a.all) {  // a tile that no query sees
+          float *to = a.mass + w.s * a.row_stride + w.h * a.mass_head_stride;
+          const int pos = (w.m.tile0 + w.j) * kBP;
+          for (int x = max(pos, w.m.lo) + lane; x < min(pos + kBP, w.m.hi); x += 32) to[x] = 0.f;
         }
-        if (!warp_wait(&ctl.sempty[buf.slot], buf.turn ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        *reinterpret_cast<float4 *>(&ctl.lse[buf.slot][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.lready[buf.slot]);
+        more = mass_next<kBP, kOver>(a, w);
       }
+      if (!more) return false;
+      const int rows = min(a.RQ, (w.i1 - w.i0) * a.G - (w.q0 + t) * a.RQ);
+      const float *at = a.lse + (int64_t)(w.m.sp.t0 + w.i0 + (w.q0 + t) * a.tokens + i8) * (a.G * a.Hkv) + w.h * a.G;
+#pragma unroll
+      for (int k = 0, g = g8; k < 8; ++k) {
+        next[k] = 8 * lane + k < rows ? at[g] : 0.f;
+        if (++g == a.G) g = 0, at += a.G * a.Hkv;
+      }
+      return true;
+    };
+    for (bool there = advance(); there && ok; buf.step()) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = next[k];
+      const int row0 = (w.q0 + t) * a.RQ, n = w.i1 - w.i0;
+      const bool ends = t + 1 == w.n, alone = w.n == 1;
+      Step st;
+      st.pos = (w.m.tile0 + w.j) * kBP, st.lo = w.m.lo, st.hi = w.m.hi;
+      st.mass = w.s * a.row_stride + w.h * a.mass_head_stride + st.pos;
+      st.base = w.m.first + w.i0, st.n = n, st.row0 = row0, st.cols = min(a.RQ, n * a.G - row0);
+      st.flags = (t < 2 ? kFirst : 0) | (t + 2 >= w.n ? kLast : 0) | (ends ? kEnds : 0) | (alone ? kAlone : 0) |
+                 (mass_begins(w) && mass_ends(w) ? kWhole : 0) | (mass_begins(w) ? kBegins : 0);
+      st.swap = swaps;
+      if (ends && lane == 0) mass_note(a, w, unit);
+      const int slot = swaps & 1;
+      const uint32_t turn = swaps >> 1 & 1;
+      if (ends) ++swaps;
+      there = advance();
+      if (!warp_wait(&ctl.sempty[buf.slot], buf.turn ^ 1, abort_flag) ||
+          (alone && !warp_wait(&ctl.xempty[slot], turn ^ 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = v[k] == -INFINITY ? v[k] : v[k] * -1.44269504088896340736f;  // -inf: weighs nothing
+      float4 *to = reinterpret_cast<float4 *>(&ctl.lse[buf.slot][8 * lane]);
+      to[0] = make_float4(v[0], v[1], v[2], v[3]);
+      to[1] = make_float4(v[4], v[5], v[6], v[7]);
+      if (lane == 0) ctl.step[buf.slot] = st;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.lready[buf.slot]);
+      // for the two warpgroups of the other slot, which have no step of this piece
+      if (alone && lane < 8) mbar_arrive(&ctl.xfull[slot]);
+    }
+    // no step is left: the warpgroups are told so
+    for (int k = 0; k < 2 && ok; ++k, buf.step()) {
+      ok = warp_wait(&ctl.sempty[buf.slot], buf.turn ^ 1, abort_flag);
+      if (lane == 0 && ok) {
+        ctl.step[buf.slot].cols = 0;
+        mbar_arrive(&ctl.lready[buf.slot]);
+      }
+    }
     if (!ok && lane == 0) fail();
   } else {
-    // ================================================= softmax: a thread owns a position, a warpgroup every second query tile
-    const int group = warp >> 2, p = tid & 127;
-    const uint32_t lq = (uint32_t)((warp & 3) * 32) << 16;
+    // ================================================= softmax: a thread owns a position
+    const int group = warp >> 2, slot = group >> 1, x0 = (group & 1) * 128, p = tid & 127;
+    const uint32_t ts = tm + ((uint32_t)((warp & 3) * 32) << 16) + slot * kNQ;
     const uint64_t c2 = f2_pack(a.c, a.c);
-    Ring<kBufs> buf;
-    uint32_t step = 0, swaps = 0;
-    for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
-      const int pos = (w.m.tile0 + w.j) * kBP + p;
-      int lo, hi;  // rows of the tile that see the position
-      mass_rows(a, w, pos, lo, hi);
-      const bool last = (int)(step + w.n - 1 & 1) == group || w.n == 0;  // this warpgroup writes the sums
-      const bool whole = mass_begins(w) && mass_ends(w), mine = pos >= w.m.lo && pos < w.m.hi;
-      float old = 0.f;
-      float *to = a.mass + w.s * a.row_stride + w.h * a.mass_head_stride + pos;
-      if (last && whole && mine && !a.all) old = *to;
-      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
-      for (int t = 0; t < w.n; ++t, ++step, buf.step()) {
-        if ((int)(step & 1) != group) continue;
-        const int row0 = (w.q0 + t) * a.RQ, cols = min(a.RQ, (w.i1 - w.i0) * a.G - row0);
-        ok = ok && warp_wait(&ctl.lready[buf.slot], buf.turn, abort_flag) &&
-             warp_wait(&ctl.sfull[buf.slot], buf.turn, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const int from = lo - row0, end = min(hi - row0, cols);  // columns that count
-#pragma unroll 1
-        for (int x = 0; x < cols; x += 32) {
-          float s[32];
-          tmem_ld32(tm + lq + buf.slot * 128 + x, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int y = 0; y < 32; ++y) asm volatile("" : "+f"(s[y]));
-          const ulonglong2 *l = reinterpret_cast<const ulonglong2 *>(&ctl.lse[buf.slot][x]);
-          const bool all = __all_sync(0xffffffffu, from <= x && end >= x + 32);
-#pragma unroll
-          for (int y = 0; y < 32; y += 4) {
-            const ulonglong2 nl = l[y / 4];
-            float e0, e1, e2, e3;
-            f2_unpack(f2_fma(f2_pack(s[y], s[y + 1]), c2, nl.x), e0, e1);
-            f2_unpack(f2_fma(f2_pack(s[y + 2], s[y + 3]), c2, nl.y), e2, e3);
-            e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-            if (!all) {
-              e0 = x + y >= from && x + y < end ? e0 : 0.f;
-              e1 = x + y + 1 >= from && x + y + 1 < end ? e1 : 0.f;
-              e2 = x + y + 2 >= from && x + y + 2 < end ? e2 : 0.f;
-              e3 = x + y + 3 >= from && x + y + 3 < end ? e3 : 0.f;
-            }
-            sum0 = f2_add(sum0, f2_pack(e0, e1));
-            sum1 = f2_add(sum1, f2_pack(e2, e3));
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.sempty[buf.slot]);
-      }
+    const float *nl = ctl.lse[slot];
+    uint64_t sum0 = 0, sum1 = 0;
+    float old = 0.f;
+    for (uint32_t turn = 0; ok; turn ^= 1) {
+      ok = warp_wait(&ctl.lready[slot], turn, abort_flag);
       if (!ok) break;
+      const Step &st = ctl.step[slot];
+      const int cols = st.cols, flags = st.flags, pos = st.pos + p, swap = st.swap;
+      if (cols == 0) break;
+      const bool mine = pos >= st.lo && pos < st.hi, writes = (flags & kEnds) && x0 == 0;
+      float *to = a.mass + st.mass + p;
+      if (flags & kFirst) sum0 = sum1 = f2_pack(0.f, 0.f);
+      if (writes && (flags & kWhole) && mine && !a.all) old = *to;
+      // columns [from, end) see the position
+      const int d = pos - st.base, rows = a.window > 0 ? (int)min((int64_t)st.n, max((int64_t)d + a.window, (int64_t)0)) : st.n;
+      const int from = max(d, 0) * a.G - st.row0, end = min(rows * a.G - st.row0, cols);
+      ok = warp_wait(&ctl.sfull[slot], turn, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int x = x0; x < min(cols, x0 + 128); x += 32) {
+        float v[32];
+        tmem_ld32(ts + x, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) asm volatile("" : "+f"(v[y]));
+        if (__all_sync(0xffffffffu, from <= x && end >= x + 32)) add_weights<false>(v, nl + x, c2, 0, 0, sum0, sum1);
+        else add_weights<true>(v, nl + x, c2, from - x, end - x, sum0, sum1);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.sempty[slot]);
+      if (!(flags & kLast)) continue;
       float s0, s1, s2, s3;
       f2_unpack(sum0, s0, s1);
       f2_unpack(sum1, s2, s3);
       float sum = (s0 + s1) + (s2 + s3);
-      if (w.n >= 2) {  // both have a part: one gives it to the other
-        const int x = swaps & 1;
-        const uint32_t turn = swaps >> 1 & 1;
-        if (!last) {
-          ok = warp_wait(&ctl.xempty[x], turn ^ 1, abort_flag);
-          ctl.x[x][p] = sum;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.xfull[x]);
-        } else {
-          ok = warp_wait(&ctl.xfull[x], turn, abort_flag);
-          sum += ctl.x[x][p];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.xempty[x]);
-        }
-        ++swaps;
-        if (!ok) break;
+      // the four parts: three give theirs to the one that writes
+      const int x = swap & 1;
+      const uint32_t phase = swap >> 1 & 1;
+      if (!writes) {
+        ok = warp_wait(&ctl.xempty[x], phase ^ 1, abort_flag);
+        ctl.x[x][group][p] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.xfull[x]);
+        continue;
       }
-      if (last && (w.n > 0 || group == 0)) {
-        if (!whole) a.part[((int64_t)2 * unit + mass_begins(w)) * kBP + p] = sum;
-        else if (mine) *to = old + sum;
-        if (p == 0) mass_note(a, w, unit);
-      }
+      ok = warp_wait(&ctl.xfull[x], phase, abort_flag);
+      if (!ok) break;
+      sum += ctl.x[x][group ^ 1][p];
+      if (!(flags & kAlone)) sum += ctl.x[x][group ^ 2][p] + ctl.x[x][group ^ 3][p];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.xempty[x]);
+      if (!(flags & kWhole)) a.part[((int64_t)2 * unit + (flags & kBegins ? 1 : 0)) * kBP + p] = sum;
+      else if (mine) *to = old + sum;
     }
     if (!ok && lane == 0) fail();
   }
@@ -387,14 +443,14 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool FEW>
+template <int D>
 gdn_status launch(MassArgs &a, const gdn_cache_shape &s, uint32_t flags, void *workspace, cudaStream_t st) {
   const int box = std::gcd(s.page_size, kBP);  // a power of two
   CUtensorMap mq, mk;
   if (!make_q_map(&mq, a.q, s, a.G, a.RQ) || !make_k_map(&mk, a.k, s, box)) return GDN_ERR_CUDA;
   a.meta = (int4 *)((char *)workspace + 256);
   a.part = (float *)(a.meta + 2 * kSms);
-  return mass_launch<kBP>(paged_mass_tc_kernel<D, FEW>, a, kSms, kThreads, kData + 1024, st, mq, mk, a,
+  return mass_launch<kBP>(paged_mass_tc_kernel<D>, a, kSms, kSms, kThreads, kData + 1024, st, mq, mk, a,
                           __builtin_ctz(box), flags & GDN_FLAG_TEST_NO_WAIT ? 1 : 0);
 }
 
@@ -416,14 +472,12 @@ size_t paged_mass_tc_workspace(const gdn_cache_shape &s) {
   return tc_shape(s) ? 256 + kSms * (2 * sizeof(int4) + 2 * kBP * sizeof(float)) : 0;
 }
 
-gdn_status paged_mass_tc(MassArgs &a, const gdn_cache_shape &s, int32_t max_new, uint32_t flags, void *workspace,
-                         cudaStream_t st) {
-  const int64_t most = (int64_t)std::max(max_new, 1) * a.G;
-  const bool few = most <= 64;
-  a.RQ = few ? (int)most : 128 / a.G * a.G;  // whole tokens
-  if (s.D == 64) return few ? launch<64, true>(a, s, flags, workspace, st) : launch<64, false>(a, s, flags, workspace, st);
-  if (s.D == 128) return few ? launch<128, true>(a, s, flags, workspace, st) : launch<128, false>(a, s, flags, workspace, st);
-  return few ? launch<256, true>(a, s, flags, workspace, st) : launch<256, false>(a, s, flags, workspace, st);
+gdn_status paged_mass_tc(MassArgs &a, const gdn_cache_shape &s, uint32_t flags, void *workspace, cudaStream_t st) {
+  a.tokens = kNQ / a.G;  // whole tokens
+  a.RQ = a.tokens * a.G;
+  a.page_mask = s.page_size & (s.page_size - 1) ? -1 : s.page_size - 1;
+  if (s.D == 64) return launch<64>(a, s, flags, workspace, st);
+  return s.D == 128 ? launch<128>(a, s, flags, workspace, st) : launch<256>(a, s, flags, workspace, st);
 }
 
 }  // namespace gdn

@@ -46,6 +46,7 @@ int32_t host_mass_pieces(const int32_t *lens, const int32_t *cu, int32_t n_seqs,
         w.h = (int32_t)((begin - from) / each);
         w.j = mass_find(w.m, (begin - from) % each, BP, window, G, RQ, OVER, u);
         w.left = end - begin;
+        w.nq = -1;
         bool more = mass_cut<BP, OVER>(a, w, u) || mass_next<BP, OVER>(a, w);
         for (; more; more = mass_next<BP, OVER>(a, w)) {
           if (n == cap) return -1;
