@@ -1,11 +1,11 @@
 // paged_mass_few.cu -- gdn_paged_mass for few query rows a sequence and kv head (single tokens; bf16, D = 64, 128 or 256).
 //
-// HBM bounds it: the keys are read once and meet a handful of rows.  So they go from global memory straight into the registers
-// that mma.sync takes its first operand from, with no shared memory and no barrier on the way, and every warp has a
-// share of the work of its own (paged_mass.cuh, tiles of 64 positions).  A lane's fragment of a product of 16 positions is four
-// columns of a row, two pairs 8 columns apart; as the order of a sum's terms is free, the lane takes 16 bytes of
-// the row that lie together, for two products, and the queries' fragments, which stay in registers, are taken the same way.
-// The rows of 16 positions are asked for DEPTH - 1 products ahead, the pages of the next tile a tile ahead.
+// HBM bounds it: the keys are read once and meet a handful of rows.  Every warp has a share of the work of its own
+// (paged_mass.cuh, tiles of 64 positions) and no barrier on the way.  A lane's fragment of a product (mma.sync) of 16
+// positions is four columns of a row, two pairs 8 columns apart; as the order of a sum's terms is free, the lane takes
+// 16 bytes of the row that lie together, for two products, and the queries' fragments, which stay in registers, are taken
+// the same way.  So a lane reads back from shared memory only what it copied there itself: a queue of its own, in which the
+// rows of 16 positions are asked for three products ahead (asynchronous copies), the pages of the next tile a tile ahead.
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,15 +16,16 @@
 namespace gdn {
 namespace {
 
-constexpr int kSms = 152, kBP = 64, kOver = 1;
+constexpr int kSms = 152, kBP = 64, kOver = 1, kDepth = 4;
 
 // NT: tiles of 8 query rows that the registers hold
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kWarps = D == 256 || NT * D > 256 ? 8 : 12;  // by their registers
+  static constexpr int kWarps = D == 256 ? 6 : NT == 4 ? 8 : 12;  // by their queues, and the queries in registers
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kDepth = D == 64 ? 4 : 2;
-  static constexpr int kVecs = D / 32;  // 16-byte pieces of a row a lane
+  static constexpr int kVecs = D / 32;            // 16-byte pieces of a row a lane
+  static constexpr int kEntry = 2 * kVecs * 512;  // bytes of a warp's rows of 16 positions
+  static constexpr int kSmem = kWarps * kDepth * kEntry;
 };
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -37,6 +38,10 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {  // zeros where there is nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // The units before each thread's sequences (thread i has the i-th run of `per`), and of all.
@@ -72,7 +77,8 @@ __device__ int64_t count_units(const MassArgs &a, int per, int64_t *before) {
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel(const MassArgs a) {
   using C = Cfg<D, NT>;
-  constexpr int kVecs = C::kVecs, kDepth = C::kDepth;
+  constexpr int kVecs = C::kVecs;
+  extern __shared__ __align__(16) uint8_t queues[];
   __shared__ int64_t before[C::kThreads];
   const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
   const int unit = blockIdx.x * C::kWarps + (threadIdx.x >> 5), units = gridDim.x * C::kWarps;
@@ -118,15 +124,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
       }
     }
   };
-  // rows g4 and g4 + 8 of 16 positions: this lane's pieces
-  auto load = [&](const int64_t (&off)[2], int c, uint4 (&r)[2][kVecs]) {
+  // rows g4 and g4 + 8 of the c-th 16 positions, this lane's pieces, into entry c of its queue and out of it
+  const uint8_t *queue = queues + (threadIdx.x >> 5) * kDepth * C::kEntry + lane * 16;
+  auto load = [&](const int64_t (&off)[2], int c) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int64_t at = __shfl_sync(0xffffffffu, off[c / 2], (c & 1) * 16 + g4 + 8 * e);
-      const uint4 *p = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + at) + t4;
+      const uint4 *p = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (at >= 0 ? at : 0)) + t4;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) r[e][j] = at >= 0 ? __ldcs(p + 4 * j) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < kVecs; ++j)
+        copy16(sm100::smem_u32(queue + c * C::kEntry + (e * kVecs + j) * 512), p + 4 * j, at >= 0);
     }
+    cp_async_commit();
   };
   uint4 q[NT][kVecs];
   float nl[NT][2];  // minus lse in base 2 of this lane's columns
@@ -152,7 +161,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
     }
   };
   // adds to sum[0], sum[1] the weights of positions g4 and g4 + 8 of the c-th 16 of the tile
-  auto weigh = [&](const uint4 (&r)[2][kVecs], int c, int t, float (&sum)[2]) {
+  auto weigh = [&](int c, int t, float (&sum)[2]) {
+    const uint4 *r0 = reinterpret_cast<const uint4 *>(queue + c * C::kEntry), *r1 = r0 + kVecs * 32;
     const int row0 = (w.q0 + t) * a.RQ, pos = (w.m.tile0 + w.j) * kBP + 16 * c + g4;
     int lo[2], hi[2];
 #pragma unroll
@@ -166,12 +176,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[n][i / 4][i % 4] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
+    for (int j = 0; j < kVecs; ++j) {
+      const uint4 x = r0[j * 32], y = r1[j * 32];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma(s[n][0], r[0][j].x, r[1][j].x, r[0][j].y, r[1][j].y, q[n][j].x, q[n][j].y);
-        mma(s[n][1], r[0][j].z, r[1][j].z, r[0][j].w, r[1][j].w, q[n][j].z, q[n][j].w);
+        mma(s[n][0], x.x, y.x, x.y, y.y, q[n][j].x, q[n][j].y);
+        mma(s[n][1], x.z, y.z, x.w, y.w, q[n][j].z, q[n][j].w);
       }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -183,10 +195,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
   };
 
   int64_t off[2], ahead[2];
-  uint4 rows[kDepth][2][kVecs];
   places(w, true, off);
 #pragma unroll
-  for (int c = 0; c < kDepth - 1; ++c) load(off, c, rows[c]);
+  for (int c = 0; c < kDepth - 1; ++c) load(off, c);
   for (bool more = true; more;) {
     MassWalk next = w;
     more = mass_next<kBP, kOver>(a, next);
@@ -202,19 +213,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
     if (w.n > 0) queries(0);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (c + kDepth - 1 < 4) load(off, c + kDepth - 1, rows[(c + kDepth - 1) % kDepth]);
-      else load(ahead, c + kDepth - 5, rows[(c + kDepth - 1) % kDepth]);
+      // the entry's products came before this; it is free
+      if (c == 0) load(off, 3);
+      else load(ahead, c - 1);
+      asm volatile("cp.async.wait_group 3;" ::: "memory");
       sum[c][0] = sum[c][1] = 0.f;
-      if (w.n > 0) weigh(rows[c % kDepth], c, 0, sum[c]);
+      if (w.n > 0) weigh(c, 0, sum[c]);
     }
-    for (int t = 1; t < w.n; ++t) {  // more rows than the call said
-      queries(t);
+    if (w.n > 1) {  // more rows than the call said: the tile once more for each 8 NT of them, then the next tile's first rows
+      for (int t = 1; t < w.n; ++t) {
+        queries(t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint4 again[2][kVecs];
-        load(off, c, again);
-        weigh(again, c, t, sum[c]);
+        for (int c = 0; c < 4; ++c) {
+          load(off, c);
+          cp_async_wait_all();
+          weigh(c, t, sum[c]);
+        }
       }
+#pragma unroll
+      for (int c = 0; c < kDepth - 1; ++c) load(ahead, c);
     }
     float out[2] = {0.f, 0.f};
 #pragma unroll
@@ -242,7 +259,7 @@ gdn_status launch(MassArgs &a, void *workspace, cudaStream_t st) {
   const int shares = kSms * Cfg<D, NT>::kWarps;
   a.meta = (int4 *)((char *)workspace + 256);
   a.part = (float *)(a.meta + 2 * shares);
-  return mass_launch<kBP>(paged_mass_few_kernel<D, NT>, a, kSms, shares, Cfg<D, NT>::kThreads, 0, st, a);
+  return mass_launch<kBP>(paged_mass_few_kernel<D, NT>, a, kSms, shares, Cfg<D, NT>::kThreads, Cfg<D, NT>::kSmem, st, a);
 }
 template <int D>
 gdn_status dispatch(MassArgs &a, void *workspace, cudaStream_t st) {
