@@ -87,6 +87,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// one lane of the warp, always the same
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // a wait of all lanes, the same answer for all of them
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, kSpin, abort));
@@ -236,41 +242,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail();
     }
   } else if (warp == kWarpMma) {
-    // ================================================= MMAs
-    if (lane == 0) {
-      Ring<C::kSlotsK> kr;
-      Ring<C::kSlotsQ> qr;
-      Ring<2> buf;
-      const uint64_t d_k = smem_desc(smem_u32(ks), 16, 1024, 2), d_q = smem_desc(smem_u32(qs), 16, 1024, 2);
-      ok = !no_wait;
-      for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
-        const Ring<C::kSlotsK> k0 = kr;
-        int left_rows = (w.i1 - w.i0) * a.G - w.q0 * a.RQ;
-        for (int t = 0; t < w.n && ok; ++t, buf.step(), left_rows -= a.RQ) {
-          ok = mbar_wait_spin(&ctl.sempty[buf.slot], buf.turn ^ 1, kSpin, abort_flag);
-          const uint32_t id = idesc_bf16(kBP, (min(a.RQ, left_rows) + 15) & ~15, false, false);
-          kr = k0;
+    // ================================================= MMAs: the warp goes together, one lane issues (its operands are then
+    // known to be the warp's)
+    Ring<C::kSlotsK> kr;
+    Ring<C::kSlotsQ> qr;
+    Ring<2> buf;
+    const uint64_t d_k = smem_desc(smem_u32(ks), 16, 1024, 2), d_q = smem_desc(smem_u32(qs), 16, 1024, 2);
+    ok = !no_wait;
+    for (; more && ok; more = mass_next<kBP, kOver>(a, w)) {
+      const Ring<C::kSlotsK> k0 = kr;
+      const int n = __shfl_sync(0xffffffffu, w.n, 0);
+      int left_rows = __shfl_sync(0xffffffffu, (w.i1 - w.i0) * a.G - w.q0 * a.RQ, 0);
+      for (int t = 0; t < n && ok; ++t, buf.step(), left_rows -= a.RQ) {
+        ok = warp_wait(&ctl.sempty[buf.slot], buf.turn ^ 1, abort_flag);
+        const uint32_t id = idesc_bf16(kBP, (min(a.RQ, left_rows) + 15) & ~15, false, false);
+        kr = k0;
 #pragma unroll 1
-          for (int p = 0; p < C::kPanels && ok; ++p, kr.step(), qr.step()) {
-            if (t == 0) ok = mbar_wait_spin(&ctl.kfull[kr.slot], kr.turn, kSpin, abort_flag);
-            ok = ok && mbar_wait_spin(&ctl.qfull[qr.slot], qr.turn, kSpin, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dk = d_k + ((kr.slot * C::kPanelK) >> 4), dq = d_q + ((qr.slot * C::kPanelQ) >> 4);
+        for (int p = 0; p < C::kPanels && ok; ++p, kr.step(), qr.step()) {
+          if (t == 0) ok = warp_wait(&ctl.kfull[kr.slot], kr.turn, abort_flag);
+          ok = ok && warp_wait(&ctl.qfull[qr.slot], qr.turn, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = d_k + ((kr.slot * C::kPanelK) >> 4), dq = d_q + ((qr.slot * C::kPanelQ) >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               umma_bf16(tm + buf.slot * kNQ, dk + (x * 32 >> 4), dq + (x * 32 >> 4), id, p > 0 || x > 0);
             umma_commit(&ctl.qempty[qr.slot]);
-            if (t + 1 == w.n) umma_commit(&ctl.kempty[kr.slot]);
+            if (t + 1 == n) umma_commit(&ctl.kempty[kr.slot]);
+            if (p + 1 == C::kPanels) umma_commit(&ctl.sfull[buf.slot]);
           }
-          if (ok) umma_commit(&ctl.sfull[buf.slot]);
+          __syncwarp();
         }
       }
-      if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
-        if (!ok) fail();
+    }
+    if (!ok || *abort_flag) {  // MMAs in flight end before the block's memory goes
+      if (!ok && lane == 0) fail();
+      if (elect_one()) {
         umma_commit(&ctl.drain);
         mbar_wait(&ctl.drain, 0, kSpin);
       }
+      __syncwarp();
     }
   } else if (warp == kWarpLse) {
     // ================================================= what the warpgroups have to know of the steps: the rows' lse, eight
@@ -446,6 +458,8 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
 template <int D>
 gdn_status launch(MassArgs &a, const gdn_cache_shape &s, uint32_t flags, void *workspace, cudaStream_t st) {
   const int box = std::gcd(s.page_size, kBP);  // a power of two
+  a.tokens = kNQ / a.G;  // whole tokens
+  a.RQ = a.tokens * a.G;
   CUtensorMap mq, mk;
   if (!make_q_map(&mq, a.q, s, a.G, a.RQ) || !make_k_map(&mk, a.k, s, box)) return GDN_ERR_CUDA;
   a.meta = (int4 *)((char *)workspace + 256);
@@ -473,8 +487,6 @@ size_t paged_mass_tc_workspace(const gdn_cache_shape &s) {
 }
 
 gdn_status paged_mass_tc(MassArgs &a, const gdn_cache_shape &s, uint32_t flags, void *workspace, cudaStream_t st) {
-  a.tokens = kNQ / a.G;  // whole tokens
-  a.RQ = a.tokens * a.G;
   a.page_mask = s.page_size & (s.page_size - 1) ? -1 : s.page_size - 1;
   if (s.D == 64) return launch<64>(a, s, flags, workspace, st);
   return s.D == 128 ? launch<128>(a, s, flags, workspace, st) : launch<256>(a, s, flags, workspace, st);
