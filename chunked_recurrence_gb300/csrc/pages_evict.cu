@@ -8,11 +8,11 @@
 //
 // Two launches.  choose_kernel: one block checks the lists and takes the free pages, one a sequence saves and checks its row of
 // the table, and one a (layer, sequence, head) finds the weights' order: a radix selection over the weights as whole
-// numbers of the same order (digits of 11, 11 and 10 bits from the top, the counts in shared memory) ends with the m - r th
-// largest T; a second walk, a warp a piece of the positions, writes those above T and the first of those at T, in order,
-// to the workspace.  apply_kernel: nothing where a list or row was refused; else the rows move, 64 positions of a head a block
-// with its place in the old and new pages worked out once for all pools of the layer, the weights follow, and tables,
-// lengths and refs are written.
+// numbers of the same order (digits of 11, 11 and 10 bits from the top, the counts in shared memory; after the first digit
+// those that are left are few) ends with the m - r th largest T; those above T and the first of those at T are written in
+// order to the workspace.  apply_kernel: nothing where a list or row was refused; else the rows move, 64 positions of a
+// head a block with its place in the old and new pages worked out once for all pools of the layer, the weights follow, and
+// tables, lengths and refs are written.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -25,10 +25,10 @@ using sm100::launch_dependents;
 namespace {
 
 constexpr int kChooseThreads = 1024;
-constexpr int kHeld = 48 * 1024;   // weights that a block keeps in shared memory; more are read again each time
+constexpr int kInRegs = 8;         // fours of weights a thread keeps in registers; of longer sequences they are read again each time
 constexpr int kBins = 2048;
-constexpr int kApplyThreads = 256;
-constexpr int kRows = 64;          // positions of a head that a block moves at a time
+constexpr int kApplyThreads = 128;
+constexpr int kRows = 32;          // positions of a head that a block moves at a time
 
 struct Evict {
   gdn_page_tables t;
@@ -119,15 +119,207 @@ __device__ void row_block(const Evict &e, int i) {
   if (threadIdx.x == 0) e.ok[1 + i] = !bad;
 }
 
-__global__ void __launch_bounds__(kChooseThreads) choose_kernel(const Evict e, int held) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins], sh[33], s_digit, s_left, above[32], level[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+struct Shared {
+  int hist[kBins], sh[33], digit, left;
+  uint32_t list[2 * kChooseThreads];
+  uint64_t sums[32];
+};
+
+// How many of the keys that each thread gives have each digit.  At once, but for keys that are alike in a warp (zeros, say),
+// which would meet at one count, a lane after another.
+__device__ __forceinline__ void count_digit(int *hist, uint32_t digit, bool mine) {
+  const uint32_t all = __ballot_sync(0xffffffffu, mine);
+  if (all == 0) return;
+  if (__popc(all) > 8) {
+    const uint32_t some = __shfl_sync(0xffffffffu, digit, __ffs(all) - 1);
+    if (__all_sync(0xffffffffu, !mine || digit == some)) {
+      if ((threadIdx.x & 31) == 0) atomicAdd(&hist[some], __popc(all));
+      return;
+    }
+  }
+  if (mine) atomicAdd(&hist[digit], 1);
+}
+// The digit that holds the left-th largest, and which of those with it; `many`: how many they are.
+__device__ __forceinline__ uint32_t find_digit(Shared &sm, int &left, int &many) {
+  __syncthreads();
+  // from the largest digit down: a thread has two
+  const int b = kBins - 1 - 2 * threadIdx.x, x = sm.hist[b], y = sm.hist[b - 1];
+  int total;
+  const int upto = block_scan(x + y, sm.sh, &total), before = upto - x - y;
+  if (before < left && left <= upto) {
+    const bool first = left <= before + x;
+    sm.digit = first ? b : b - 1;
+    sm.left = left - (first ? before : before + x);
+  }
+  __syncthreads();
+  left = sm.left;
+  many = sm.hist[sm.digit];
+  return sm.digit;
+}
+__device__ __forceinline__ void clear_counts(Shared &sm) {
+  __syncthreads();  // the counts before, and what was found in them, have been read
+  for (int b = threadIdx.x; b < kBins; b += kChooseThreads) sm.hist[b] = 0;
+  __syncthreads();
+}
+
+// Four 16-bit sums over the block's threads at once: those before this thread, and all.
+__device__ __forceinline__ uint64_t sums_before(uint64_t x, Shared &sm, uint64_t &all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t mine = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  __syncthreads();
+  if (lane == 31) sm.sums[warp] = x;
+  __syncthreads();
+  uint64_t y = sm.sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += u;
+  }
+  all = __shfl_sync(0xffffffffu, y, 31);
+  const uint64_t others = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+  return x - mine + (warp ? others : 0);
+}
+
+// The `need` largest of the N weights: their positions, in rising order, and the weights.  In round r a thread has weights
+// 4096 r + 4 tid .. + 3: R rounds in registers, or with R = 0 all that there are, read again each time.
+template <int R>
+__device__ void choose(const float *mass, int N, int need, int32_t *index, float *weight, Shared &sm) {
+  const int tid = threadIdx.x, rounds = R ? R : (N + 4 * kChooseThreads - 1) / (4 * kChooseThreads);
+  const bool wide = (reinterpret_cast<uintptr_t>(mass) & 15) == 0;
+  auto place = [&](int r) { return 4 * (r * kChooseThreads + tid); };
+  auto read = [&](int r, uint32_t (&u)[4]) {
+    const int j = place(r);
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (wide && j + 3 < N) {
+      w = *reinterpret_cast<const float4 *>(mass + j);
+    } else {
+      if (j < N) w.x = mass[j];
+      if (j + 1 < N) w.y = mass[j + 1];
+      if (j + 2 < N) w.z = mass[j + 2];
+      if (j + 3 < N) w.w = mass[j + 3];
+    }
+    u[0] = order_of(w.x), u[1] = order_of(w.y), u[2] = order_of(w.z), u[3] = order_of(w.w);
+  };
+  uint32_t held[R ? R : 1][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) read(r, held[r]);
+  auto keys = [&](int r, uint32_t (&u)[4]) {
+    if (R) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = held[R ? r : 0][i];
+    } else {
+      read(r, u);
+    }
+  };
+  auto there = [&](int r, int i) { return place(r) + i < N; };
+
+  // the need-th largest, digit by digit: of the numbers that begin with `top`, how many have each next digit
+  int left = need, many;
+  auto count = [&](int shift, uint32_t mask, uint32_t top, bool all) {
+    clear_counts(sm);
+#pragma unroll
+    for (int r = 0; r < rounds; ++r) {
+      uint32_t u[4];
+      keys(r, u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        count_digit(sm.hist, u[i] >> shift & mask, there(r, i) && (all || u[i] >> shift >> (mask == 1023 ? 10 : 11) == top));
+    }
+  };
+  count(21, 2047, 0, true);
+  uint32_t top = find_digit(sm, left, many);
+  if (many <= 2 * kChooseThreads) {  // those that begin so, by themselves, in any order
+    if (tid == 0) sm.digit = 0;
+    clear_counts(sm);
+#pragma unroll
+    for (int r = 0; r < rounds; ++r) {
+      uint32_t u[4];
+      keys(r, u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (there(r, i) && u[i] >> 21 == top) sm.list[atomicAdd(&sm.digit, 1)] = u[i];
+    }
+    const int listed = many;
+    uint32_t u[2];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u[i] = tid + i * kChooseThreads < listed ? sm.list[tid + i * kChooseThreads] : 0;
+      count_digit(sm.hist, u[i] >> 10 & 2047, tid + i * kChooseThreads < listed);
+    }
+    top = top << 11 | find_digit(sm, left, many);
+    clear_counts(sm);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      count_digit(sm.hist, u[i] & 1023, tid + i * kChooseThreads < listed && u[i] >> 10 == top);
+    top = top << 10 | find_digit(sm, left, many);
+  } else {
+    count(10, 2047, top, false);
+    top = top << 11 | find_digit(sm, left, many);
+    count(0, 1023, top, false);
+    top = top << 10 | find_digit(sm, left, many);
+  }
+  // above `top` all stay, of those at it the first `left`: where each round's go, four rounds' counts in a word
+  int eq0 = 0, at0 = 0;  // of the rounds before
+#pragma unroll
+  for (int r0 = 0; r0 < rounds; r0 += 4) {
+    uint64_t gt = 0, eq = 0, all;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (r0 + k >= rounds) break;
+      uint32_t u[4];
+      keys(r0 + k, u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        gt += (uint64_t)(there(r0 + k, i) && u[i] > top) << 16 * k;
+        eq += (uint64_t)(there(r0 + k, i) && u[i] == top) << 16 * k;
+      }
+    }
+    const uint64_t eq_at = sums_before(eq, sm, all);
+    uint64_t in = 0;  // of the thread's that are at `top`
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int before = eq0 + (int)(eq_at >> 16 * k & 0xffff);
+      in += (uint64_t)min(max(left - before, 0), (int)(eq >> 16 * k & 0xffff)) << 16 * k;
+      eq0 += (int)(all >> 16 * k & 0xffff);
+    }
+    const uint64_t at_r = sums_before(gt + in, sm, all);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (r0 + k >= rounds) break;
+      int at = at0 + (int)(at_r >> 16 * k & 0xffff), level = (int)(in >> 16 * k & 0xffff);
+      at0 += (int)(all >> 16 * k & 0xffff);
+      if ((gt + in) >> 16 * k & 0xffff) {
+        uint32_t u[4];
+        keys(r0 + k, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (there(r0 + k, i) && (u[i] > top || (u[i] == top && level-- > 0))) {
+            const int j = place(r0 + k) + i;
+            index[at] = j;
+            // the weight itself; which NaN or zero it was is not in the key
+            weight[at++] = u[i] == 0 || u[i] == 0x80000000u ? mass[j]
+                                                          : __uint_as_float(u[i] >> 31 ? u[i] & 0x7fffffffu : ~u[i]);
+          }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kChooseThreads) choose_kernel(const Evict e) {
+  __shared__ Shared sm;
   grid_dependency_wait();
   launch_dependents();
-  if (blockIdx.x == 0) return plan_block(e, sh);
-  if (blockIdx.x <= e.n) return row_block(e, blockIdx.x - 1);
-  const int64_t lih = (int64_t)blockIdx.x - 1 - e.n;
+  // the lists of the largest index first: the plan and the rows are shorter
+  const int lists = gridDim.x - 1 - e.n;
+  if (blockIdx.x == lists) return plan_block(e, sm.sh);
+  if ((int)blockIdx.x > lists) return row_block(e, blockIdx.x - lists - 1);
+  const int64_t lih = blockIdx.x;
   const int h = (int)(lih % e.heads), i = (int)(lih / e.heads % e.n), l = (int)(lih / e.heads / e.n);
   const int s = e.seqs[i], m = e.keep[i];
   const int len = s >= 0 && s < e.t.n_rows ? e.t.seq_lens[s] : -1;
@@ -136,76 +328,16 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const Evict e, i
   int32_t *index = e.index + lih * e.max_keep;
   float *weight = e.weight + lih * e.max_keep;
   const int recent = min(e.recent, m), N = len - recent, need = m - recent;  // need < N
-  for (int j = tid; j < recent; j += kChooseThreads) {
+  for (int j = threadIdx.x; j < recent; j += kChooseThreads) {
     index[need + j] = N + j;
     weight[need + j] = mass[N + j];
   }
   if (need == 0) return;
-  const bool keep_keys = N <= held;
-  auto key = [&](int j) { return keep_keys ? keys[j] : order_of(mass[j]); };
-  for (int j = tid; j < N && keep_keys; j += kChooseThreads) keys[j] = order_of(mass[j]);
-
-  // the need-th largest, digit by digit: of the numbers that begin with `top`, how many have each next digit
-  uint32_t top = 0;
-  int left = need;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int b = tid; b < kBins; b += kChooseThreads) hist[b] = 0;
-    __syncthreads();
-    for (int j0 = 0; j0 < N; j0 += kChooseThreads) {
-      const int j = j0 + tid;
-      const uint32_t u = j < N ? key(j) : 0;
-      const bool mine = j < N && (pass == 0 || u >> (shift + bits) == top);
-      const uint32_t digit = u >> shift & ((1u << bits) - 1), all = __ballot_sync(0xffffffffu, mine);
-      if (all == 0) continue;
-      // equal weights (zeros, say) would meet at one count, a lane after another
-      const uint32_t some = __shfl_sync(0xffffffffu, digit, __ffs(all) - 1);
-      if (__all_sync(0xffffffffu, !mine || digit == some)) {
-        if (lane == 0) atomicAdd(&hist[some], __popc(all));
-      } else if (mine) {
-        atomicAdd(&hist[digit], 1);
-      }
-    }
-    __syncthreads();
-    // from the largest digit down: a thread has two
-    const int b = kBins - 1 - 2 * tid, x = hist[b], y = hist[b - 1];
-    int total;
-    const int upto = block_scan(x + y, sh, &total), before = upto - x - y;
-    if (before < left && left <= upto) {
-      const bool first = left <= before + x;
-      s_digit = first ? b : b - 1;
-      s_left = left - (first ? before : before + x);
-    }
-    __syncthreads();
-    top = top << bits | s_digit;
-    left = s_left;
-    __syncthreads();
-  }
-  // above `top` all stay, of those at it the first `left`: a warp's piece of the positions, counted, then written
-  const int piece = (N + kChooseThreads - 1) / kChooseThreads * 32, begin = min(warp * piece, N), end = min(begin + piece, N);
-  int gt = 0, eq = 0;
-  for (int j0 = begin; j0 < end; j0 += 32) {
-    const uint32_t u = j0 + lane < end ? key(j0 + lane) : 0;
-    gt += __popc(__ballot_sync(0xffffffffu, j0 + lane < end && u > top));
-    eq += __popc(__ballot_sync(0xffffffffu, j0 + lane < end && u == top));
-  }
-  if (lane == 0) above[warp] = gt, level[warp] = eq;
-  __syncthreads();
-  gt = eq = 0;
-  for (int w = 0; w < warp; ++w) gt += above[w], eq += level[w];
-  for (int j0 = begin; j0 < end; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t u = j < end ? key(j) : 0, under = (1u << lane) - 1;
-    const uint32_t g = __ballot_sync(0xffffffffu, j < end && u > top), q = __ballot_sync(0xffffffffu, j < end && u == top);
-    const bool level_in = (q >> lane & 1) && eq + __popc(q & under) < left;
-    if ((g >> lane & 1) || level_in) {
-      const int at = gt + __popc(g & under) + min(eq + __popc(q & under), left);
-      index[at] = j;
-      weight[at] = mass[j];
-    }
-    gt += __popc(g), eq += __popc(q);
-  }
+  constexpr int kRound = 4 * kChooseThreads;
+  if (N <= kRound) choose<1>(mass, N, need, index, weight, sm);
+  else if (N <= 4 * kRound) choose<4>(mass, N, need, index, weight, sm);
+  else if (N <= kInRegs * kRound) choose<kInRegs>(mass, N, need, index, weight, sm);
+  else choose<0>(mass, N, need, index, weight, sm);
 }
 
 template <typename V>
@@ -219,25 +351,32 @@ __global__ void __launch_bounds__(kApplyThreads) apply_kernel(const Evict e, con
   grid_dependency_wait();
   bool ok = e.ok[0];
   for (int i = tid; i < e.n; i += kApplyThreads) ok = ok && e.ok[1 + i];
-  if (__syncthreads_or(!ok)) return;
+  bool asked = false;  // whether the lists can be carried out: after the first loads, which wait as long
 
   const int chunks = (e.max_keep + kRows - 1) / kRows;
   const int64_t blocks = (int64_t)e.n_layers * e.n * e.heads * chunks;
   for (int64_t x = blockIdx.x; x < blocks; x += gridDim.x) {
-    const int64_t lih = x / chunks;
-    const int j0 = (int)(x - lih * chunks) * kRows, h = (int)(lih % e.heads), i = (int)(lih / e.heads % e.n);
-    const int l = (int)(lih / e.heads / e.n), page0 = e.page0[i], m = page0 < 0 ? 0 : e.keep[i], s = e.seqs[i], len = e.len[i];
-    float *mass = e.mass + l * e.layer_stride + s * e.row_stride + h * e.head_stride;
+    // the heads of the same positions one after another: their rows lie side by side in the pages
+    const int64_t li_c = x / e.heads, li = li_c / chunks;
+    const int h = (int)(x - li_c * e.heads), j0 = (int)(li_c - li * chunks) * kRows, i = (int)(li % e.n);
+    const int64_t lih = li * e.heads + h;
+    // (of lists that cannot be carried out page0 may be anything)
+    const int l = (int)(li / e.n), page0 = e.page0[i], s = e.seqs[i], len = e.len[i];
+    const int m = page0 < 0 ? 0 : min(e.keep[i], e.max_keep);
     const int rows = min(kRows, m - j0);
-    __syncthreads();  // the places of the rows before are done with
+    int src = 0;
+    float weight = 0.f;
+    if (tid < rows) src = e.index[lih * e.max_keep + j0 + tid], weight = e.weight[lih * e.max_keep + j0 + tid];
+    if (__syncthreads_or(!asked && !ok)) return;  // and the places of the rows before are done with
+    asked = true;
+    float *mass = e.mass + l * e.layer_stride + s * e.row_stride + h * e.head_stride;
     if (tid < kRows) {
       const int j = j0 + tid;
       if (tid < rows) {
-        const int src = e.index[lih * e.max_keep + j];
         from[tid] = e.old[(int64_t)i * t.max_pages + src / t.page_size] * page_stride + src % t.page_size * slot_stride +
                     h * slot_head_stride;
         to[tid] = e.fresh[page0 + j / t.page_size] * page_stride + j % t.page_size * slot_stride + h * slot_head_stride;
-        mass[j] = e.weight[lih * e.max_keep + j];
+        mass[j] = weight;
         if (e.kept) e.kept[lih * e.max_keep + j] = src;
       } else if (e.kept && j < e.max_keep) {
         e.kept[lih * e.max_keep + j] = page0 < 0 && j < len ? j : -1;
@@ -264,6 +403,7 @@ __global__ void __launch_bounds__(kApplyThreads) apply_kernel(const Evict e, con
         if (v0 + k * kApplyThreads < all) __stcs((V *)dst[k], v[k]);
     }
   }
+  if (__syncthreads_or(!asked && !ok)) return;
   // weights behind what is kept
   const int64_t rows = (int64_t)e.n_layers * e.n * e.heads;
   for (int64_t lih = blockIdx.x; lih < rows; lih += gridDim.x) {
@@ -364,17 +504,12 @@ extern "C" gdn_status gdn_pages_evict(const gdn_page_tables *tables, const int32
   e.seqs = seqs, e.keep = keep, e.mass = h.mass, e.kept = kept;
   e.layer_stride = h.layer_stride, e.row_stride = h.row_stride, e.head_stride = h.head_stride;
   cudaStream_t st = (cudaStream_t)stream;
-  // shared memory for the weights of the longest sequence that can be
-  const int64_t most = std::min<int64_t>(h.mass_len, (int64_t)e.t.max_pages * e.t.page_size);
-  const int held = (int)std::min<int64_t>(most, kHeld);
-  if (cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess)
-    return (void)cudaGetLastError(), GDN_ERR_CUDA;
   const int64_t lists = (int64_t)h.n_layers * n * h.heads;
-  launch_early(choose_kernel, (int)(1 + n + lists), kChooseThreads, st, (size_t)held * 4, e, held);
+  launch_early(choose_kernel, (int)(1 + n + lists), kChooseThreads, st, 0, e);
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   const int per_layer = pools->n_pools / h.n_layers;
   const int64_t work = std::max<int64_t>(lists * ((max_keep + kRows - 1) / kRows), n);
-  const int blocks = (int)std::min<int64_t>(work, 152 * 8);
+  const int blocks = (int)std::min<int64_t>(work, 1 << 16);
   uintptr_t bits = (uintptr_t)pools->page_stride | (uintptr_t)h.slot_stride | (uintptr_t)h.slot_head_stride | (uintptr_t)h.row_bytes;
   for (int i = 0; i < pools->n_pools; ++i) bits |= (uintptr_t)p.p[i];
   auto apply = [&](auto v) {
