@@ -95,8 +95,9 @@ struct TcArgs {
                // one begins an item that the next share continues, that item's head and rows; its first token and row
   int32_t *status;
   int32_t no_wait;
-  // with a shared prefix: units before each slot [slots] and of all, and of each kind (prefix, own) and row of o the sums
-  // of an item that one share holds whole, with its maximum and sum
+  // with a shared prefix: units before each slot [slots] and of all, and of each kind (prefix, own), kv head and row (token
+  // * G + head of the group) the sums of an item that one share holds whole, with its maximum and sum: 32 rows a block,
+  // [column / 4][row] fours
   int64_t *from;
   float *full, *full_ml;
 };
@@ -258,6 +259,10 @@ struct Walk {
   int slot, h, j, n, u, units;
   int64_t left;
 };
+template <class C, bool SHARED>
+__device__ __forceinline__ int32_t units_of(const SharedItem &it) {
+  return SHARED ? shared_units(it, C::kOver) : item_units(it, C::kOver);
+}
 // cuts the next piece at unit u of the item; false where it holds nothing to do
 template <class C>
 __device__ __forceinline__ bool walk_cut(Walk &w) {
@@ -266,10 +271,6 @@ __device__ __forceinline__ bool walk_cut(Walk &w) {
   w.j = unit_tile(w.u, C::kOver);
   w.n = unit_tile(end, C::kOver) - w.j;
   return w.it.n_tiles > 0 ? w.n > 0 : w.u == 0;
-}
-template <class C, bool SHARED>
-__device__ __forceinline__ int32_t units_of(const SharedItem &it) {
-  return SHARED ? shared_units(it, C::kOver) : item_units(it, C::kOver);
 }
 // the item of the next slot
 template <class C, bool SHARED>
@@ -923,11 +924,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
           const int64_t out = out_row();
           const uint32_t to = tm + lq + C::kO + t * D;
           if (SHARED && begins && ends) {
-            // the sums as they are, four lanes a row's 64 bytes at a time
-            int64_t rows4[4];
-            const int64_t at = (it.own ? (int64_t)a.seqs.n_tok * (a.G * a.Hkv) : 0) + out;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(0xffffffffu, valid ? at : -1, (lane & ~3) + k);
+            const int64_t blocks = ((int64_t)a.seqs.n_tok * a.G + 31) / 32, gr = (int64_t)it.t0 * a.G + it.row0 + rr;
+            const int64_t at = ((it.own ? a.Hkv : 0) + w.h) * blocks + gr / 32;
+            uint4 *pp = reinterpret_cast<uint4 *>(a.full) + at * (D / 4 * 32) + gr % 32;
 #pragma unroll 2
             for (int x = 0; x < D; x += 32) {
               uint32_t u[32];
@@ -935,21 +934,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int y = 0; y < 32; ++y) asm volatile("" : "+r"(u[y]));
+              if (valid)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint4 v[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  v[y] = make_uint4(u[16 * half + 4 * y], u[16 * half + 4 * y + 1], u[16 * half + 4 * y + 2],
-                                    u[16 * half + 4 * y + 3]);
-                quad_transpose(v);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (rows4[k] >= 0)
-                    *reinterpret_cast<uint4 *>(a.full + rows4[k] * D + x + 16 * half + (lane & 3) * 4) = v[k];
-              }
+                for (int y = 0; y < 32; y += 4)
+                  pp[(x + y) / 4 * 32] = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
             }
-            if (valid) *reinterpret_cast<float2 *>(a.full_ml + at * 2) = make_float2(m * a.c, l);
+            if (valid) *reinterpret_cast<float2 *>(a.full_ml + (at * 32 + gr % 32) * 2) = make_float2(m * a.c, l);
           } else if (begins && ends) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             // rows of this lane's quad, -1: none
@@ -1154,10 +1144,10 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The kernel and the one that joins its pieces (a block of `threads` each of join_grid).
-template <int D, int NQ, bool PAIR, bool SHARED, typename... P>
+// The kernel and the one that joins its pieces.
+template <int D, int NQ, bool PAIR, bool SHARED>
 gdn_status launch_two(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st, dim3 join_grid,
-                      void (*join)(TcArgs, int, P...), P... more) {
+                      void (*join)(TcArgs, int)) {
   using C = Cfg<D, NQ, PAIR>;
   a.box = std::gcd(s.page_size, C::kRowsK);  // a power of two
   a.box_log2 = __builtin_ctz(a.box);
@@ -1187,7 +1177,7 @@ gdn_status launch_two(const void *k, const void *v, const gdn_cache_shape &s, Tc
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join, (TcArgs)a, kSms / C::kPair, more...) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, join, (TcArgs)a, kSms / C::kPair) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   return launch_status();
 }

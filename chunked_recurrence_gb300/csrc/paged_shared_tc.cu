@@ -14,109 +14,168 @@
 namespace gdn {
 namespace {
 
-// A warp takes `per` rows of o of a kv head, one at a time, a lane 4 (D = 256: 8) of a row's columns.  First each lane finds
-// where the pieces of one of the block's rows lie.
-template <int D, int NQ, bool PAIR>
-__global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs a, int blocks, int per) {
-  using C = Cfg<D, NQ, PAIR>;
-  constexpr int kV = (D + 127) / 128;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+// Where the pieces of a row of o lie: in shares [from, from + n) of each kind, lane `at` of them; or, of one alone, in `full`.
+struct RowPieces {
+  int from[2], n[2], at[2];
+};
+template <class C>
+__device__ __forceinline__ RowPieces find_pieces(const TcArgs &a, int64_t row, int h, int blocks, int64_t &to) {
+  RowPieces p = {};
   const PagedSeqs &q = a.seqs;
   const int R = a.RT * C::kTiles, first = (int)item_slots(q.n_tok, q.n_groups, a.G, R);
   const int slots = first + (int)item_slots(q.n_tok, q.n_seqs, a.G, R);
-  grid_dependency_wait();
-  const int64_t total = a.from[slots], rows = (int64_t)q.n_tok * a.G, all = rows * a.Hkv;
+  const int64_t total = a.from[slots];
   const int shares = (int)min((int64_t)blocks, total);
-  const int64_t row = (int64_t)blockIdx.x * (8 * per) + lane;
-  int from[2] = {0, 0}, to[2] = {-1, -1}, at[2] = {0, 0};  // shares [from, to] that hold pieces, the row's lane in them
-  int64_t out = -1;
-  if (lane < 8 * per && row < rows) {
-    const int t = (int)(row / a.G), i = (int)(row - (int64_t)t * a.G);
-    out = (int64_t)t * (a.G * a.Hkv) + h * a.G + i;
-    const int s = token_seq(q, t), g = seq_group(q, s);
+  const int t = (int)(row / a.G), i = (int)(row - (int64_t)t * a.G), s = token_seq(q, t), g = seq_group(q, s);
+  to = (int64_t)t * (a.G * a.Hkv) + h * a.G + i;
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const int64_t r = (int64_t)(t - cu_at(q, kind ? s : group_at(q, g))) * a.G + i;  // of the sequence, of the group
-      if (r < 0) continue;  // offsets that fall
-      const int slot = (kind ? slot_base(q, s, a.G, R) : group_base(q, g, a.G, R)) + (int)(r / R);
-      if (slot >= (kind ? slots - first : first)) continue;
-      const SharedItem it = kind ? own_item(q, g, s, slot, a.G, R, C::KT) : prefix_item(q, g, slot, a.G, R, C::KT);
-      const int its = shared_units(it, C::kOver), rr = (int)(r - it.row0);
-      const int64_t u = a.from[slot + kind * first] + (int64_t)h * its;
-      if (its == 0 || rr < 0 || rr >= it.rows || u + its > total) continue;
-      from[kind] = share_of(total, u + C::kOver, shares), to[kind] = share_of(total, u + its - 1, shares);
-      at[kind] = rr / a.RT * 128 + rr % a.RT;
-    }
+  for (int kind = 0; kind < 2; ++kind) {
+    const int64_t r = (int64_t)(t - cu_at(q, kind ? s : group_at(q, g))) * a.G + i;  // of the sequence, of the group
+    if (r < 0) continue;  // offsets that fall
+    const int slot = (kind ? slot_base(q, s, a.G, R) : group_base(q, g, a.G, R)) + (int)(r / R);
+    if (slot >= (kind ? slots - first : first)) continue;
+    const int64_t before = a.from[slot + kind * first];
+    const SharedItem it = kind ? own_item(q, g, s, slot, a.G, R, C::KT) : prefix_item(q, g, slot, a.G, R, C::KT);
+    const int its = shared_units(it, C::kOver), rr = (int)(r - it.row0);
+    const int64_t u = before + (int64_t)h * its;
+    if (its == 0 || rr < 0 || rr >= it.rows || u + its > total) continue;
+    p.from[kind] = share_of(total, u + C::kOver, shares);
+    p.n[kind] = share_of(total, u + its - 1, shares) - p.from[kind] + 1;
+    p.at[kind] = rr / a.RT * 128 + rr % a.RT;
   }
-  for (int j = warp * per; j < (warp + 1) * per; ++j) {
-    const int64_t o = __shfl_sync(0xffffffffu, out, j);
-    if (o < 0) break;
-    int f[2], n[2], lr[2];
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      f[kind] = __shfl_sync(0xffffffffu, from[kind], j);
-      n[kind] = __shfl_sync(0xffffffffu, to[kind], j) - f[kind] + 1;
-      lr[kind] = __shfl_sync(0xffffffffu, at[kind], j);
-      if (n[kind] < 0) n[kind] = 0;
-    }
-    const int pieces = n[0] + n[1];
-    // piece i: of the prefix first; of several the first lies behind its share's other one
-    auto which = [&](int i, bool &whole, int &kind) {
-      kind = i >= n[0];
-      const int k = i - (kind ? n[0] : 0);
-      whole = n[kind] == 1;
-      return whole ? kind * all + o : 2 * ((int64_t)f[kind] + k) + (k == 0);
-    };
-    auto ml_of = [&](int i) {
-      bool whole;
-      int kind;
-      if (i >= pieces) return make_float2(-INFINITY, 0.f);
-      const int64_t w = which(i, whole, kind);
-      return *reinterpret_cast<const float2 *>(whole ? a.full_ml + w * 2 : a.part_ml + (w * C::R + lr[kind]) * 2);
-    };
-    float2 ml = ml_of(lane);
-    float top = ml.x;
-    for (int i = 32 + lane; i < pieces; i += 32) top = fmaxf(top, ml_of(i).x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float sum = 0.f;
-    float4 x[kV];
-#pragma unroll
-    for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int base = 0; base < pieces; base += 32) {
-      if (base > 0) ml = ml_of(base + lane);
-      const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
-      sum = fmaf(w, ml.y, sum);
-      const int m = min(32, pieces - base);
+  return p;
+}
+// Piece i of a row, those of the prefix first; of several the first lies behind its share's other one.
+struct Piece {
+  int64_t at;
+  int kind;
+  bool whole;
+};
+__device__ __forceinline__ Piece piece_of(const RowPieces &p, int i, int64_t in_full, int64_t of_kind) {
+  Piece x;
+  x.kind = i >= p.n[0];
+  const int k = i - (x.kind ? p.n[0] : 0), n = x.kind ? p.n[1] : p.n[0], from = x.kind ? p.from[1] : p.from[0];
+  x.whole = n == 1;
+  x.at = x.whole ? in_full + x.kind * of_kind : 2 * ((int64_t)from + k) + (k == 0);
+  return x;
+}
+__device__ __forceinline__ void add(float4 &x, float f, const float4 &y) {
+  x.x = fmaf(f, y.x, x.x);
+  x.y = fmaf(f, y.y, x.y);
+  x.z = fmaf(f, y.z, x.z);
+  x.w = fmaf(f, y.w, x.w);
+}
+__device__ __forceinline__ uint2 rounded(const float4 &x, float f) {
+  return make_uint2(bf16x2(x.x * f, x.y * f), bf16x2(x.z * f, x.w * f));
+}
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+}
+
+// Many rows: 32 of a kv head a block, a lane a row, a warp an eighth of the columns; the rows go out through shared memory,
+// whole.  (2250 tokens, 32/8 heads, D 128: 50 us, the other 71.)
+template <int D, int NQ, bool PAIR>
+__global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs a, int blocks) {
+  using C = Cfg<D, NQ, PAIR>;
+  constexpr int kV = D / 32;  // fours of columns a warp
+  __shared__ uint2 out[32][D / 4 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+  grid_dependency_wait();
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  int64_t to = -1;
+  RowPieces p = {};
+  if (row < (int64_t)a.seqs.n_tok * a.G) p = find_pieces<C>(a, row, h, blocks, to);
+  const int pieces = p.n[0] + p.n[1], most = (int)__reduce_max_sync(0xffffffffu, (unsigned)pieces);
+  const int64_t in_full = (int64_t)h * gridDim.x + blockIdx.x, of_kind = (int64_t)a.Hkv * gridDim.x;
+  auto ml_of = [&](int i) {
+    if (i >= pieces) return make_float2(-INFINITY, 0.f);
+    const Piece x = piece_of(p, i, in_full, of_kind);
+    return *reinterpret_cast<const float2 *>(x.whole ? a.full_ml + (x.at * 32 + lane) * 2
+                                                     : a.part_ml + (x.at * C::R + (x.kind ? p.at[1] : p.at[0])) * 2);
+  };
+  float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        bool whole;
-        int kind;
-        const int64_t p = which(base + i, whole, kind);
-        const float4 *v = whole ? reinterpret_cast<const float4 *>(a.full) + p * (D / 4)
-                                : reinterpret_cast<const float4 *>(a.part) + p * (C::R * D / 4) + lr[kind];
+  for (int i = 0; i < most; ++i) top = fmaxf(top, ml_of(i).x);
+  float4 x[kV];
 #pragma unroll
-        for (int e = 0; e < kV; ++e)
-          if (wi != 0.f && lane + 32 * e < D / 4) {
-            const float4 y = v[(int64_t)(lane + 32 * e) * (whole ? 1 : C::R)];
-            x[e].x = fmaf(wi, y.x, x[e].x);
-            x[e].y = fmaf(wi, y.y, x[e].y);
-            x[e].z = fmaf(wi, y.z, x[e].z);
-            x[e].w = fmaf(wi, y.w, x[e].w);
-          }
-      }
+  for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < most; ++i) {
+    const float2 ml = ml_of(i);
+    const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+    if (f != 0.f) {
+      const Piece y = piece_of(p, i, in_full, of_kind);
+      const int step = y.whole ? 32 : C::R;
+      const float4 *v = y.whole ? reinterpret_cast<const float4 *>(a.full) + y.at * (D / 4 * 32) + lane
+                                : reinterpret_cast<const float4 *>(a.part) + y.at * (C::R * D / 4) + (y.kind ? p.at[1] : p.at[0]);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) add(x[e], f, v[(int64_t)(warp * kV + e) * step]);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < kV; ++e)
-      if (lane + 32 * e < D / 4)
-        *reinterpret_cast<uint2 *>(a.o + o * D + 4 * (lane + 32 * e)) =
-            make_uint2(bf16x2(x[e].x * inv, x[e].y * inv), bf16x2(x[e].z * inv, x[e].w * inv));
-    if (lane == 0 && a.lse) a.lse[o] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kV; ++e) out[lane][warp * kV + e] = rounded(x[e], inv);
+  if (to >= 0 && warp == 0 && a.lse) a.lse[to] = lse_of(top, sum);
+  __syncthreads();
+  for (int r = warp; r < 32; r += 8) {
+    const int64_t o = __shfl_sync(0xffffffffu, to, r);
+    if (o >= 0)
+      for (int c = lane; c < D / 4; c += 32) *reinterpret_cast<uint2 *>(a.o + o * D + 4 * c) = out[r][c];
+  }
+}
+
+// Few rows: a warp a row, a lane its columns; a lane has the maximum and sum of one of 32 pieces.
+template <int D, int NQ, bool PAIR>
+__global__ void __launch_bounds__(256) shared_join_few_kernel(const TcArgs a, int blocks) {
+  using C = Cfg<D, NQ, PAIR>;
+  constexpr int kV = (D + 127) / 128;
+  const int lane = threadIdx.x & 31, h = blockIdx.y;
+  grid_dependency_wait();
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (int64_t)a.seqs.n_tok * a.G;
+  if (row >= rows) return;
+  int64_t to;
+  const RowPieces p = find_pieces<C>(a, row, h, blocks, to);
+  const int pieces = p.n[0] + p.n[1], r = (int)(row % 32);
+  const int64_t of_head = (rows + 31) / 32, in_full = (int64_t)h * of_head + row / 32, of_kind = (int64_t)a.Hkv * of_head;
+  auto ml_of = [&](int i) {
+    if (i >= pieces) return make_float2(-INFINITY, 0.f);
+    const Piece x = piece_of(p, i, in_full, of_kind);
+    return *reinterpret_cast<const float2 *>(x.whole ? a.full_ml + (x.at * 32 + r) * 2
+                                                     : a.part_ml + (x.at * C::R + (x.kind ? p.at[1] : p.at[0])) * 2);
+  };
+  float2 ml = ml_of(lane);
+  float top = ml.x, sum = 0.f;
+  for (int i = 32 + lane; i < pieces; i += 32) top = fmaxf(top, ml_of(i).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float4 x[kV];
+#pragma unroll
+  for (int e = 0; e < kV; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < pieces; base += 32) {
+    if (base > 0) ml = ml_of(base + lane);
+    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+    sum = fmaf(w, ml.y, sum);
+    const int m = min(32, pieces - base);
+#pragma unroll 4
+    for (int i = 0; i < m; ++i) {
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      const Piece y = piece_of(p, base + i, in_full, of_kind);
+      const int step = y.whole ? 32 : C::R;
+      const float4 *v = y.whole ? reinterpret_cast<const float4 *>(a.full) + y.at * (D / 4 * 32) + r
+                                : reinterpret_cast<const float4 *>(a.part) + y.at * (C::R * D / 4) + (y.kind ? p.at[1] : p.at[0]);
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        if (f != 0.f && lane + 32 * e < D / 4) add(x[e], f, v[(int64_t)(lane + 32 * e) * step]);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kV; ++e)
+    if (lane + 32 * e < D / 4) *reinterpret_cast<uint2 *>(a.o + to * D + 4 * (lane + 32 * e)) = rounded(x[e], inv);
+  if (lane == 0 && a.lse) a.lse[to] = lse_of(top, sum);
 }
 
 // The workspace behind the status: the units before each slot, the pieces, the rows of whole items.
@@ -125,7 +184,7 @@ struct Layout {
 };
 Layout layout(const gdn_cache_shape &s, int32_t n_groups, int row_tiles) {
   const int G = s.Hq / s.Hkv, RT = 128 / G * G;
-  const size_t lanes = (size_t)kSms * 2 * 128 * row_tiles, rows = 2 * (size_t)s.n_tok * s.Hq;
+  const size_t lanes = (size_t)kSms * 2 * 128 * row_tiles, rows = 2 * (size_t)s.Hkv * (((size_t)s.n_tok * G + 31) / 32 * 32);
   Layout l;
   l.from = 256;
   l.part_ml = (l.from + (shared_slots(s.n_tok, s.n_seqs, n_groups, G, RT) + 1) * sizeof(int64_t) + 255) & ~(size_t)255;
@@ -144,9 +203,11 @@ gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs
   a.part_ml = (float *)(w + l.part_ml), a.part = (float *)(w + l.part);
   a.full_ml = (float *)(w + l.full_ml), a.full = (float *)(w + l.full);
   const int64_t rows = (int64_t)s.n_tok * a.G;
-  const int per = rows * a.Hkv >= 8 * 8 * kSms * 4 ? 4 : 1;  // a row a warp while the warps are few
-  const dim3 grid((unsigned)((rows + 8 * per - 1) / (8 * per)), a.Hkv);
-  return launch_two<D, NQ, PAIR, true>(k, v, s, a, st, grid, shared_join_kernel<D, NQ, PAIR>, per);
+  if (rows * a.Hkv >= 8 * 32 * kSms)
+    return launch_two<D, NQ, PAIR, true>(k, v, s, a, st, dim3((unsigned)((rows + 31) / 32), a.Hkv),
+                                         shared_join_kernel<D, NQ, PAIR>);
+  return launch_two<D, NQ, PAIR, true>(k, v, s, a, st, dim3((unsigned)((rows + 7) / 8), a.Hkv),
+                                       shared_join_few_kernel<D, NQ, PAIR>);
 }
 
 }  // namespace
