@@ -227,12 +227,26 @@ GDN_HD int32_t row_end(const PagedSeqs &q, const SharedItem &it, int32_t r, int3
 // Units of an item as item_units, none where it has no tiles.
 GDN_HD int32_t shared_units(const Item &it, int32_t over) { return it.rows <= 0 || it.n_tiles <= 0 ? 0 : it.n_tiles + over; }
 
-// The block whose share (share_begin) holds unit u < total, with 1 <= blocks <= total.
-GDN_HD int32_t share_of(int64_t total, int64_t u, int32_t blocks) {
-  int32_t b = (int32_t)((u + 1) * blocks / total);  // u blocks fits: total is at most 2^40 or so
-  if (b >= blocks) b = blocks - 1;
-  while (b > 0 && share_begin(total, b, blocks) > u) --b;
-  while (b + 1 < blocks && share_begin(total, b + 1, blocks) <= u) ++b;
+// share_begin for many blocks of one line, and the block whose share holds unit u < total, with 1 <= blocks <= total: the
+// 64-bit divisions (some 100 cycles each) are made once.
+struct Shares {
+  int64_t each;
+  int32_t rest, blocks;
+  float inverse;  // blocks / total
+};
+GDN_HD Shares shares_of(int64_t total, int32_t blocks) {
+  Shares s;
+  s.each = total / blocks;
+  s.rest = (int32_t)(total - s.each * blocks), s.blocks = blocks;
+  s.inverse = (float)blocks / (float)total;
+  return s;
+}
+GDN_HD int64_t share_begin(const Shares &s, int32_t b) { return s.each * b + s.rest * b / s.blocks; }  // rest < blocks: a few 100
+GDN_HD int32_t share_of(const Shares &s, int64_t u) {
+  int32_t b = (int32_t)((float)u * s.inverse);  // off by one at most
+  if (b >= s.blocks) b = s.blocks - 1;
+  while (b > 0 && share_begin(s, b) > u) --b;
+  while (b + 1 < s.blocks && share_begin(s, b + 1) <= u) ++b;
   return b;
 }
 

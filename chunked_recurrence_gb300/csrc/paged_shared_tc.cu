@@ -25,7 +25,7 @@ __device__ __forceinline__ RowPieces find_pieces(const TcArgs &a, int64_t row, i
   const int R = a.RT * C::kTiles, first = (int)item_slots(q.n_tok, q.n_groups, a.G, R);
   const int slots = first + (int)item_slots(q.n_tok, q.n_seqs, a.G, R);
   const int64_t total = a.from[slots];
-  const int shares = (int)min((int64_t)blocks, total);
+  const Shares shares = shares_of(max(total, (int64_t)1), max((int)min((int64_t)blocks, total), 1));
   const int t = (int)(row / a.G), i = (int)(row - (int64_t)t * a.G), s = token_seq(q, t), g = seq_group(q, s);
   to = (int64_t)t * (a.G * a.Hkv) + h * a.G + i;
 #pragma unroll
@@ -39,8 +39,8 @@ __device__ __forceinline__ RowPieces find_pieces(const TcArgs &a, int64_t row, i
     const int its = shared_units(it, C::kOver), rr = (int)(r - it.row0);
     const int64_t u = before + (int64_t)h * its;
     if (its == 0 || rr < 0 || rr >= it.rows || u + its > total) continue;
-    p.from[kind] = share_of(total, u + C::kOver, shares);
-    p.n[kind] = share_of(total, u + its - 1, shares) - p.from[kind] + 1;
+    p.from[kind] = share_of(shares, u + C::kOver);
+    p.n[kind] = share_of(shares, u + its - 1) - p.from[kind] + 1;
     p.at[kind] = rr / a.RT * 128 + rr % a.RT;
   }
   return p;

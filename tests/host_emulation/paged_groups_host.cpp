@@ -26,6 +26,11 @@ void host_shared_item(const int32_t *lens, const int32_t *cu, int32_t n_seqs, in
   for (int r = 0; r < it.rows && !it.own; ++r) ends[r] = row_end(q, it, it.row0 + r, G);
 }
 int64_t host_share_begin(int64_t total, int32_t b, int32_t blocks) { return share_begin(total, b, blocks); }
-int32_t host_share_of(int64_t total, int64_t u, int32_t blocks) { return share_of(total, u, blocks); }
+int32_t host_share_of(int64_t total, int64_t u, int32_t blocks) { return share_of(shares_of(total, blocks), u); }
+int32_t host_shares_agree(int64_t total, int32_t blocks) {
+  for (int32_t b = 0; b <= blocks; ++b)
+    if (share_begin(shares_of(total, blocks), b) != share_begin(total, b, blocks)) return 0;
+  return 1;
+}
 int32_t host_unit_tile(int32_t u, int32_t over) { return unit_tile(u, over); }
 }

@@ -160,6 +160,9 @@ def test_pieces_are_where_the_join_looks(host, blocks, over):
             assert [b for b, _ in pieces] == list(range(f, last + 1))
             assert pieces[0][1] == 0 and all(j > 0 for _, j in pieces[1:])
             at += n
+    lib = host.host_shares_agree
+    lib.argtypes = [ctypes.c_int64, ctypes.c_int32]
+    assert all(lib(t, min(blocks, t)) for t in (1, 2, 151, 152, 153, 10 ** 6 + 7, (1 << 40) + 12345))
     big = (1 << 40) + 12345
     for u in (0, 1, big // 2, big - 1):
         b = host.host_share_of(big, u, 152)
