@@ -259,17 +259,23 @@ struct Walk {
   int slot, h, j, n, u, units;
   int64_t left;
 };
+// Units that an item costs beyond its tiles: where rows behind a shared prefix fill one of two row tiles, half of the two's (64
+// samples of 16000: 75 us, 85 with 4; chunks of up to 300, which fill both, 348 us with 4 and 415 with 2).
 template <class C, bool SHARED>
-__device__ __forceinline__ int32_t units_of(const SharedItem &it) {
-  return SHARED ? shared_units(it, C::kOver) : item_units(it, C::kOver);
+__device__ __forceinline__ int32_t over_of(const SharedItem &it, int RT) {
+  return SHARED && C::kTiles > C::kPair && it.rows <= RT * C::kPair ? C::kOver / 2 : C::kOver;
+}
+template <class C, bool SHARED>
+__device__ __forceinline__ int32_t units_of(const SharedItem &it, int RT) {
+  return SHARED ? shared_units(it, over_of<C, SHARED>(it, RT)) : item_units(it, C::kOver);
 }
 // cuts the next piece at unit u of the item; false where it holds nothing to do
-template <class C>
-__device__ __forceinline__ bool walk_cut(Walk &w) {
-  const int end = (int)min((int64_t)w.units, w.u + w.left);
+template <class C, bool SHARED>
+__device__ __forceinline__ bool walk_cut(Walk &w, int RT) {
+  const int end = (int)min((int64_t)w.units, w.u + w.left), over = over_of<C, SHARED>(w.it, RT);
   w.left -= end - w.u;
-  w.j = unit_tile(w.u, C::kOver);
-  w.n = unit_tile(end, C::kOver) - w.j;
+  w.j = unit_tile(w.u, over);
+  w.n = unit_tile(end, over) - w.j;
   return w.it.n_tiles > 0 ? w.n > 0 : w.u == 0;
 }
 // the item of the next slot
@@ -302,10 +308,10 @@ __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int s
       do {
         if (++w.slot >= slots) return false;
         walk_slot<C, SHARED>(a, w, R);
-        w.units = units_of<C, SHARED>(w.it);
+        w.units = units_of<C, SHARED>(w.it, a.RT);
       } while (w.units == 0);
     }
-    if (walk_cut<C>(w)) return true;
+    if (walk_cut<C, SHARED>(w, a.RT)) return true;
   }
   return false;
 }
@@ -313,8 +319,8 @@ template <class C, bool SHARED>
 __device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, const Ctl &c, int64_t left) {
   w.slot = c.start_slot, w.h = c.start_h, w.u = c.start_u, w.left = left;
   w.it = c.start;
-  w.units = units_of<C, SHARED>(w.it);
-  return walk_cut<C>(w) || walk_next<C, SHARED>(a, w, R, slots);
+  w.units = units_of<C, SHARED>(w.it, a.RT);
+  return walk_cut<C, SHARED>(w, a.RT) || walk_next<C, SHARED>(a, w, R, slots);
 }
 
 template <int N>
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         static_cast<Item &>(it) = item_at(sq, s, a.G, R, KT, a.window);
       }
       if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
-      cost = (int64_t)units_of<C, SHARED>(it) * a.Hkv;
+      cost = (int64_t)units_of<C, SHARED>(it, a.RT) * a.Hkv;
     }
     x = cost;
 #pragma unroll
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     const int64_t all = slots <= C::kThreads ? total : round(base);
     const int64_t from = before + x - cost;  // units before this slot
     if (cost > 0 && begin >= from && begin < from + cost) {
-      const uint32_t its = units_of<C, SHARED>(it), into = (uint32_t)(begin - from);  // below units * Hkv
+      const uint32_t its = units_of<C, SHARED>(it, a.RT), into = (uint32_t)(begin - from);  // below units * Hkv
       ctl.start_slot = base + tid;
       ctl.start = it;
       ctl.start_h = into / its;

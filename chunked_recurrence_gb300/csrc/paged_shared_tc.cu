@@ -36,10 +36,10 @@ __device__ __forceinline__ RowPieces find_pieces(const TcArgs &a, int64_t row, i
     if (slot >= (kind ? slots - first : first)) continue;
     const int64_t before = a.from[slot + kind * first];
     const SharedItem it = kind ? own_item(q, g, s, slot, a.G, R, C::KT) : prefix_item(q, g, slot, a.G, R, C::KT);
-    const int its = shared_units(it, C::kOver), rr = (int)(r - it.row0);
+    const int over = over_of<C, true>(it, a.RT), its = shared_units(it, over), rr = (int)(r - it.row0);
     const int64_t u = before + (int64_t)h * its;
     if (its == 0 || rr < 0 || rr >= it.rows || u + its > total) continue;
-    p.from[kind] = share_of(shares, u + C::kOver);
+    p.from[kind] = share_of(shares, u + over);
     p.n[kind] = share_of(shares, u + its - 1) - p.from[kind] + 1;
     p.at[kind] = rr / a.RT * 128 + rr % a.RT;
   }
