@@ -2,12 +2,15 @@
 third, prompts in, then tokens one at a time for several beams, losing beams dropped and forked again from
 the winners, the cache's pages brought together now and then.
 
-    python examples/hybrid_beam.py [--tokens 24] [--beams 4] [--dtype bf16]
+    python examples/hybrid_beam.py [--tokens 24] [--beams 4] [--dtype bf16] [--keep 0]
 
 Weights are random.  Projections are plain torch products; the layers between them are this package's:
     recurrent layer:  gdn_layer_fwd for a prompt, gdn_decode_step for a token, its state a row of a tensor
-    attention layer:  gdn_kv_append (rotary positions on q and k on the way), gdn_paged_attn
+    attention layer:  gdn_kv_append (rotary positions on q and k on the way), gdn_paged_attn for the prompt,
+                      gdn_paged_attn_shared for the beams, whose prompt is read once for all of them
     sequences:        gdn_pages_grow / fork / free / compact for the pages, gdn_pages_copy for the recurrent state
+    a long prompt:    with --keep, gdn_paged_mass counts the attention weight of its positions and gdn_pages_evict
+                      leaves that many of them in the cache before the beams begin
 """
 import argparse
 import math
@@ -39,6 +42,7 @@ class Config:
     pages: int = 96
     rows: int = 8              # sequences that may live at once
     max_len: int = 256
+    keep: int = 0              # of a prompt, positions left in the cache (0: all); a quarter of them its last
     dtype: torch.dtype = torch.bfloat16
 
 
@@ -72,6 +76,9 @@ class Hybrid:
         self.table = torch.full((c.rows, -(-c.max_len // c.page)), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(c.rows, dtype=torch.int32, device=device)
         self.refs = torch.zeros(c.pages, dtype=torch.int32, device=device)
+        self.at = torch.zeros(c.rows, dtype=torch.int64, device=device)  # rotary position of a row's next token
+        n_attn = c.layers.count("a")
+        self.mass = torch.zeros((n_attn, c.rows, c.kv_heads, c.max_len), device=device) if c.keep else None
         self.pages_ws = crg.Workspace(crg.gdn_pages_workspace_bytes(c.pages, c.rows), device)
 
     # ------------------------------------------------------------- sequences
@@ -92,9 +99,18 @@ class Hybrid:
         self._pages(crg.gdn_pages_fork, parents, children, self.pools)
         for name in ("state", "last"):
             crg.gdn_pages_copy([x[name] for x in self.layers if name in x], parents, children)
+        self.at[children.long()] = self.at[parents.long()]
 
     def free(self, rows):
         self._pages(crg.gdn_pages_free, self._list(rows))
+        self.at[self._list(rows).long()] = 0
+
+    def evict(self, rows):
+        """Rows cut to `keep` positions: in each layer, for each kv head, those that their tokens looked at most."""
+        c = self.cfg
+        keep = [c.keep] * len(rows)
+        crg.gdn_pages_evict(self.table, self.lens, self.refs, self._list(rows), self._list(keep), self.mass, self.pools,
+                            c.page, max_keep=c.keep, recent=c.keep // 4)
 
     def compact(self):
         self._pages(crg.gdn_pages_compact, self.pools)
@@ -130,19 +146,33 @@ class Hybrid:
             o = crg.gdn_gated_rmsnorm(o, z)
         return o.view(-1, c.Hv * c.V) @ p["out"]
 
-    def _attention(self, p, x, rows, cu, longest):
+    def _attention(self, p, x, rows, cu, longest, positions, mass, groups):
         c, n = self.cfg, x.shape[0]
         q, k, v = ((x @ p[w]).view(n, -1, c.D) for w in "qkv")
         table, lens = self.table[rows], self.lens[rows]
-        q = crg.gdn_kv_append(k, v, p["k_cache"], p["v_cache"], table, lens, cu, q=q, freqs=self.freqs, q_out=q)
-        o, _ = crg.gdn_paged_attn(q, p["k_cache"], p["v_cache"], table, lens, cu, max_new=longest)
+        q = crg.gdn_kv_append(k, v, p["k_cache"], p["v_cache"], table, lens, cu, q=q, freqs=self.freqs, q_out=q,
+                              positions=positions)
+        if groups is not None:
+            o, lse = crg.gdn_paged_attn_shared(q, p["k_cache"], p["v_cache"], table, lens, *groups, cu)
+        else:
+            o, lse = crg.gdn_paged_attn(q, p["k_cache"], p["v_cache"], table, lens, cu, max_new=longest,
+                                        want_lse=mass is not None)
+        if mass is not None and cu is not None:
+            mass[rows] = crg.gdn_paged_mass(q, p["k_cache"], table, lens, lse, mass[rows], cu, max_new=longest,
+                                            accumulate=False)
         return o.view(n, -1) @ p["out"]
 
-    def forward(self, tokens, rows, lengths=None):
-        """New tokens of the sequences in `rows`: whole prompts (lengths, rows empty before), or one token each.
-        Returns the logits of all of them."""
+    def forward(self, tokens, rows, lengths=None, shared=0):
+        """New tokens of the sequences in `rows`: whole prompts (lengths, rows empty before), or one token each, of rows
+        that have their first `shared` positions in common.  Returns the logits of all of them."""
         rows_t = torch.as_tensor(rows, device=tokens.device)
-        self.grow(rows, lengths if lengths is not None else [1] * len(rows))
+        new = lengths if lengths is not None else [1] * len(rows)
+        self.grow(rows, new)
+        positions = torch.cat([torch.arange(n, device=tokens.device) for n in new]) + \
+            self.at[rows_t].repeat_interleave(self._list(new), output_size=sum(new))
+        self.at[rows_t] += self._list(new)
+        groups = (self._list([0, len(rows)]), self._list([shared])) if shared else None
+        masses = iter(self.mass if self.mass is not None else [None] * len(self.layers))
         cu = None if lengths is None else self._list([0] + list(lengths)).cumsum(0).to(torch.int32)
         h = self.embed[tokens]
         for kind, p in zip(self.cfg.layers, self.layers):
@@ -150,7 +180,7 @@ class Hybrid:
             if kind == "r":
                 h = h + self._recurrent(p, x, rows_t, cu, lengths)
             else:
-                h = h + self._attention(p, x, rows_t, cu, max(lengths) if lengths else 1)
+                h = h + self._attention(p, x, rows_t, cu, max(new), positions, next(masses), groups)
         return (self._norm(h) @ self.head).float()
 
 
@@ -160,10 +190,15 @@ def beams(model: Hybrid, prompt, n_beams, n_tokens):
     logits = model.forward(prompt, [0], [prompt.numel()])[-1:]
     score = logits.log_softmax(-1)
     best = score[0].topk(n_beams)
+    shared = prompt.numel()
+    if model.cfg.keep:
+        model.evict([0])
+        shared = min(shared, model.cfg.keep)
     model.fork([0] * (n_beams - 1), rows[1:])
     texts, scores = [[t] for t in best.indices.tolist()], best.values
     for step in range(n_tokens - 1):
-        logp = model.forward(torch.tensor([t[-1] for t in texts], device=prompt.device), rows).log_softmax(-1)
+        logp = model.forward(torch.tensor([t[-1] for t in texts], device=prompt.device), rows,
+                             shared=shared).log_softmax(-1)
         best = (scores[:, None] + logp).flatten().topk(n_beams)
         parents, tokens = (best.indices // logp.shape[1]).tolist(), (best.indices % logp.shape[1]).tolist()
         # a row goes on as its own first child; rows without one are dropped and forked again
@@ -197,8 +232,9 @@ def main():
     ap.add_argument("--tokens", type=int, default=24)
     ap.add_argument("--beams", type=int, default=4)
     ap.add_argument("--dtype", choices=("bf16", "f32"), default="bf16")
+    ap.add_argument("--keep", type=int, default=0)
     args = ap.parse_args()
-    model = Hybrid(Config(dtype=torch.bfloat16 if args.dtype == "bf16" else torch.float32))
+    model = Hybrid(Config(dtype=torch.bfloat16 if args.dtype == "bf16" else torch.float32, keep=args.keep))
     prompt = torch.arange(37, device="cuda") * 11 % model.cfg.vocab
     texts, scores = beams(model, prompt, args.beams, args.tokens)
     for text, score in zip(texts, scores.tolist()):
