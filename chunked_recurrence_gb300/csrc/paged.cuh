@@ -24,8 +24,10 @@ struct PagedSeqs {
   int32_t n_seqs;
   int32_t n_tok;
   int32_t max_tokens;       // max_pages * page_size, clamped to int32: no sequence can hold more
-  // sequences that share a prefix: [n_groups + 1] offsets of the groups' sequences, [n_groups] tokens shared; null: none
-  const int32_t *groups, *prefix;
+};
+// The same where groups of sequences share a prefix (n_groups = 0: none does).
+struct GroupedSeqs : PagedSeqs {
+  const int32_t *groups, *prefix;  // [n_groups + 1] offsets of the groups' sequences, [n_groups] tokens shared
   int32_t n_groups;
 };
 
@@ -126,11 +128,11 @@ struct GroupSpan {
   int32_t s0, s1, prefix;  // sequences [s0, s1), tokens that they share
   bool ok;
 };
-GDN_HD int32_t group_at(const PagedSeqs &q, int32_t g) {
+GDN_HD int32_t group_at(const GroupedSeqs &q, int32_t g) {
   const int32_t s = q.groups[g];
   return s < 0 ? 0 : s > q.n_seqs ? q.n_seqs : s;
 }
-GDN_HD GroupSpan group_span(const PagedSeqs &q, int32_t g) {
+GDN_HD GroupSpan group_span(const GroupedSeqs &q, int32_t g) {
   GroupSpan r;
   r.s0 = group_at(q, g), r.s1 = group_at(q, g + 1);
   const int32_t p = q.prefix[g];
@@ -140,7 +142,7 @@ GDN_HD GroupSpan group_span(const PagedSeqs &q, int32_t g) {
   return r;
 }
 // The group of a sequence, and the sequence of a token: the last whose offset is not past it.
-GDN_HD int32_t seq_group(const PagedSeqs &q, int32_t s) {
+GDN_HD int32_t seq_group(const GroupedSeqs &q, int32_t s) {
   int32_t lo = 0, hi = q.n_groups - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi + 1) >> 1;
@@ -157,7 +159,7 @@ GDN_HD int32_t token_seq(const PagedSeqs &q, int32_t t) {
   }
   return lo;
 }
-GDN_HD int32_t group_base(const PagedSeqs &q, int32_t g, int32_t G, int32_t R) { return cu_at(q, group_at(q, g)) * G / R + g; }
+GDN_HD int32_t group_base(const GroupedSeqs &q, int32_t g, int32_t G, int32_t R) { return cu_at(q, group_at(q, g)) * G / R + g; }
 GDN_HD int64_t shared_slots(int64_t n_tok, int32_t n_seqs, int32_t n_groups, int32_t G, int32_t R) {
   return item_slots(n_tok, n_groups, G, R) + item_slots(n_tok, n_seqs, G, R);
 }
@@ -169,7 +171,7 @@ struct SharedItem : Item {
 
 // Rows of group g against its prefix; it.s is the group's first sequence.  A row sees less than all of the prefix where
 // its token lies in it (row_end).
-GDN_HD SharedItem prefix_item(const PagedSeqs &q, int32_t g, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+GDN_HD SharedItem prefix_item(const GroupedSeqs &q, int32_t g, int32_t slot, int32_t G, int32_t R, int32_t KT) {
   SharedItem it;
   const GroupSpan gs = group_span(q, g);
   const int32_t a = cu_at(q, gs.s0), b = cu_at(q, gs.s1);
@@ -187,7 +189,7 @@ GDN_HD SharedItem prefix_item(const PagedSeqs &q, int32_t g, int32_t slot, int32
   return it;
 }
 // Rows of sequence s, of group g, against its positions behind the prefix.
-GDN_HD SharedItem own_item(const PagedSeqs &q, int32_t g, int32_t s, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+GDN_HD SharedItem own_item(const GroupedSeqs &q, int32_t g, int32_t s, int32_t slot, int32_t G, int32_t R, int32_t KT) {
   SharedItem it;
   static_cast<Item &>(it) = item_of(q, s, slot, G, R, KT, 0);
   const GroupSpan gs = group_span(q, g);
@@ -204,7 +206,7 @@ GDN_HD SharedItem own_item(const PagedSeqs &q, int32_t g, int32_t s, int32_t slo
   }
   return it;
 }
-GDN_HD SharedItem shared_item_at(const PagedSeqs &q, int32_t slot, int32_t G, int32_t R, int32_t KT) {
+GDN_HD SharedItem shared_item_at(const GroupedSeqs &q, int32_t slot, int32_t G, int32_t R, int32_t KT) {
   const int32_t first = (int32_t)item_slots(q.n_tok, q.n_groups, G, R);
   if (slot >= first) {
     const int32_t s = slot_seq(q, slot - first, G, R);

@@ -294,7 +294,7 @@ extern "C" gdn_status gdn_paged_attn(const void *q, const void *k_cache, const v
     return paged_attn_tc(q, k_cache, v_cache, page_table, seqs, s, max_new, scale_log2, window, flags, o, lse,
                          workspace, st);
   const bool simt = flags & GDN_FLAG_SIMT;
-  SimtArgs a{seqs, q, k_cache, v_cache, o, lse, nullptr, page_table, s.table_stride, s.page_stride, s.slot_stride,
+  SimtArgs a{GroupedSeqs{seqs}, q, k_cache, v_cache, o, lse, nullptr, page_table, s.table_stride, s.page_stride, s.slot_stride,
              s.head_stride, s.q_stride, s.Hq, s.Hkv, s.D, s.page_size, s.max_pages, s.n_pages, window,
              simt ? simt_splits(s) : paged_attn_f32_splits(s, max_new, window), scale_log2,
              s.status ? s.status : (int32_t *)workspace};
@@ -338,7 +338,7 @@ extern "C" gdn_status gdn_paged_attn_shared(const void *q, const void *k_cache, 
   if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !group_offsets || !prefix_lens || !o)
     return GDN_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  PagedSeqs seqs = paged_seqs(s, seq_lens, cu_seqlens);
+  GroupedSeqs seqs{paged_seqs(s, seq_lens, cu_seqlens)};
   seqs.groups = group_offsets, seqs.prefix = prefix_lens, seqs.n_groups = n_groups;
   const float scale_log2 = scale * 1.44269504088896340736f;
   const bool simt = flags & GDN_FLAG_SIMT;

@@ -19,13 +19,13 @@ gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int3
 
 // The same where groups of sequences share a prefix (seqs names them).
 size_t paged_shared_tc_workspace(const gdn_cache_shape &s, int32_t n_groups, int32_t max_group_new);
-gdn_status paged_shared_tc(const void *q, const void *k, const void *v, const int32_t *table, const PagedSeqs &seqs,
+gdn_status paged_shared_tc(const void *q, const void *k, const void *v, const int32_t *table, const GroupedSeqs &seqs,
                            const gdn_cache_shape &s, int32_t max_group_new, float scale_log2, uint32_t flags, void *o,
                            float *lse, void *workspace, cudaStream_t st);
 
 // A call as the kernels without tcgen05 take it.
 struct SimtArgs {
-  PagedSeqs seqs;
+  GroupedSeqs seqs;
   const void *q, *k, *v;
   void *o;
   float *lse, *part;  // part: [splits][n_tok * Hq][2 + D] (maximum, sum, weighted sum), or null with one split; with
@@ -56,7 +56,7 @@ __device__ __forceinline__ int simt_row_begin(const SimtArgs &a, const SharedIte
   return a.window > 0 && p >= a.window ? p - a.window + 1 : a.seqs.n_groups ? it.lo : 0;
 }
 inline int64_t simt_slots(const SimtArgs &a, int R) {
-  const PagedSeqs &q = a.seqs;
+  const GroupedSeqs &q = a.seqs;
   return q.n_groups ? shared_slots(q.n_tok, q.n_seqs, q.n_groups, a.Hq / a.Hkv, R)
                     : item_slots(q.n_tok, q.n_seqs, a.Hq / a.Hkv, R);
 }

@@ -5,7 +5,7 @@ namespace gdn {
 namespace {
 
 template <int D, int NQ, bool PAIR>
-gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, void *workspace, cudaStream_t st) {
+gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs<false> &a, void *workspace, cudaStream_t st) {
   using C = Cfg<D, NQ, PAIR>;
   constexpr int units = kSms / C::kPair;
   char *w = (char *)workspace;
@@ -36,7 +36,7 @@ size_t paged_attn_tc_workspace(const gdn_cache_shape &s, int32_t max_new) {
 gdn_status paged_attn_tc(const void *q, const void *k, const void *v, const int32_t *table, const PagedSeqs &seqs,
                          const gdn_cache_shape &s, int32_t max_new, float scale_log2, int32_t window, uint32_t flags,
                          void *o, float *lse, void *workspace, cudaStream_t st) {
-  TcArgs a = tc_args(q, table, seqs, s, scale_log2, window, flags, o, lse, workspace);
+  TcArgs<false> a = tc_args<false>(q, table, seqs, s, scale_log2, window, flags, o, lse, workspace);
   const bool pair = pairs(s, max_new);
   if (s.D == 256)
     return pair ? launch<256, 1, true>(k, v, s, a, workspace, st) : launch<256, 1, false>(k, v, s, a, workspace, st);

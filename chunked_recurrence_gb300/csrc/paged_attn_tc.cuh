@@ -80,8 +80,23 @@ struct Cfg {
   static constexpr int kOver = NQ == 1 && !PAIR ? 2 : 4;
 };
 
-struct TcArgs {
-  PagedSeqs seqs;
+// Without groups the kernel is to stay what it is without them: its schedule moves with what is beside it (8192 over 16384:
+// 1147 us, 1177 with the fields of a shared call in its items).
+template <bool SHARED>
+using SeqsOf = std::conditional_t<SHARED, GroupedSeqs, PagedSeqs>;
+template <bool SHARED>
+using ItemOf = std::conditional_t<SHARED, SharedItem, Item>;
+
+struct PlainArgs {};
+struct SharedSums {
+  // units before each slot [slots] and of all, and of each kind (prefix, own), kv head and row (token * G + head of the
+  // group) the sums of an item that one share holds whole, with its maximum and sum: 32 rows a block, [column / 4][row] fours
+  int64_t *from;
+  float *full, *full_ml;
+};
+template <bool SHARED>
+struct TcArgs : std::conditional_t<SHARED, SharedSums, PlainArgs> {
+  SeqsOf<SHARED> seqs;
   const __nv_bfloat16 *q;
   __nv_bfloat16 *o;
   float *lse;
@@ -95,21 +110,22 @@ struct TcArgs {
                // one begins an item that the next share continues, that item's head and rows; its first token and row
   int32_t *status;
   int32_t no_wait;
-  // with a shared prefix: units before each slot [slots] and of all, and of each kind (prefix, own), kv head and row (token
-  // * G + head of the group) the sums of an item that one share holds whole, with its maximum and sum: 32 rows a block,
-  // [column / 4][row] fours
-  int64_t *from;
-  float *full, *full_ml;
 };
 
+__device__ __forceinline__ bool own_part(const SharedItem &it) { return it.own; }
+__device__ __forceinline__ bool own_part(const Item &) { return true; }
+
+struct SharedStart : SharedItem {
+  int partial;  // some token lies in its group's prefix
+};
+template <bool SHARED>
 struct Ctl {
   uint64_t full[16], empty[16], land[16], sfull[2], pready[2][2], odone[2], qfull[2], qfree[2], drain;
   uint32_t tmem;
   volatile int abort;
   int64_t sum[12];
   int start_slot, start_h, start_u;
-  SharedItem start;
-  int partial;  // some token lies in its group's prefix
+  std::conditional_t<SHARED, SharedStart, Item> start;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
@@ -254,24 +270,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 
 // A block's share of the line of work, piece by piece: `n` tiles from tile `j` of an item and
 // head (n = 0 for one without tiles, whose rows get zeros).
+template <bool SHARED>
 struct Walk {
-  SharedItem it;
+  ItemOf<SHARED> it;
   int slot, h, j, n, u, units;
   int64_t left;
 };
 // Units that an item costs beyond its tiles: where rows behind a shared prefix fill one of two row tiles, half of the two's (64
 // samples of 16000: 75 us, 85 with 4; chunks of up to 300, which fill both, 348 us with 4 and 415 with 2).
 template <class C, bool SHARED>
-__device__ __forceinline__ int32_t over_of(const SharedItem &it, int RT) {
+__device__ __forceinline__ int32_t over_of(const Item &it, int RT) {
   return SHARED && C::kTiles > C::kPair && it.rows <= RT * C::kPair ? C::kOver / 2 : C::kOver;
 }
 template <class C, bool SHARED>
-__device__ __forceinline__ int32_t units_of(const SharedItem &it, int RT) {
+__device__ __forceinline__ int32_t units_of(const Item &it, int RT) {
   return SHARED ? shared_units(it, over_of<C, SHARED>(it, RT)) : item_units(it, C::kOver);
 }
 // cuts the next piece at unit u of the item; false where it holds nothing to do
 template <class C, bool SHARED>
-__device__ __forceinline__ bool walk_cut(Walk &w, int RT) {
+__device__ __forceinline__ bool walk_cut(Walk<SHARED> &w, int RT) {
   const int end = (int)min((int64_t)w.units, w.u + w.left), over = over_of<C, SHARED>(w.it, RT);
   w.left -= end - w.u;
   w.j = unit_tile(w.u, over);
@@ -280,9 +297,10 @@ __device__ __forceinline__ bool walk_cut(Walk &w, int RT) {
 }
 // the item of the next slot
 template <class C, bool SHARED>
-__device__ __forceinline__ void walk_slot(const TcArgs &a, Walk &w, int R) {
-  int s = w.it.s, g = w.it.g, slot = w.slot;
+__device__ __forceinline__ void walk_slot(const TcArgs<SHARED> &a, Walk<SHARED> &w, int R) {
+  int s = w.it.s;
   if constexpr (SHARED) {
+    int g = w.it.g, slot = w.slot;
     const int first = (int)item_slots(a.seqs.n_tok, a.seqs.n_groups, a.G, R);
     if (slot < first) {
       while (g + 1 < a.seqs.n_groups && group_base(a.seqs, g + 1, a.G, R) <= slot) ++g;
@@ -295,12 +313,12 @@ __device__ __forceinline__ void walk_slot(const TcArgs &a, Walk &w, int R) {
     while (g + 1 < a.seqs.n_groups && group_at(a.seqs, g + 1) <= s) ++g;
     w.it = own_item(a.seqs, g, s, slot, a.G, R, C::KT);
   } else {
-    while (s + 1 < a.seqs.n_seqs && slot_base(a.seqs, s + 1, a.G, R) <= slot) ++s;
-    static_cast<Item &>(w.it) = item_of(a.seqs, s, slot, a.G, R, C::KT, a.window);
+    while (s + 1 < a.seqs.n_seqs && slot_base(a.seqs, s + 1, a.G, R) <= w.slot) ++s;
+    w.it = item_of(a.seqs, s, w.slot, a.G, R, C::KT, a.window);
   }
 }
 template <class C, bool SHARED>
-__device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int slots) {
+__device__ __forceinline__ bool walk_next(const TcArgs<SHARED> &a, Walk<SHARED> &w, int R, int slots) {
   while (w.left > 0) {
     w.u = 0;
     if (++w.h == a.Hkv) {
@@ -316,7 +334,7 @@ __device__ __forceinline__ bool walk_next(const TcArgs &a, Walk &w, int R, int s
   return false;
 }
 template <class C, bool SHARED>
-__device__ __forceinline__ bool walk_begin(const TcArgs &a, Walk &w, int R, int slots, const Ctl &c, int64_t left) {
+__device__ __forceinline__ bool walk_begin(const TcArgs<SHARED> &a, Walk<SHARED> &w, int R, int slots, const Ctl<SHARED> &c, int64_t left) {
   w.slot = c.start_slot, w.h = c.start_h, w.u = c.start_u, w.left = left;
   w.it = c.start;
   w.units = units_of<C, SHARED>(w.it, a.RT);
@@ -387,12 +405,12 @@ __device__ __forceinline__ uint32_t idx_v(uint32_t base, int j, int n) {
 template <int D, int NQ, bool PAIR, bool SHARED>
 __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const TcArgs a) {
+                      const __grid_constant__ CUtensorMap tm_v, const TcArgs<SHARED> a) {
   using C = Cfg<D, NQ, PAIR>;
   constexpr int KT = C::KT, kSlots = C::kSlots;
   static_assert(C::kRowsK / 8 * C::kPanelsK <= 32 && KT / 8 * C::kPanelsV <= 32, "a granule has at most one box a lane");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Ctl ctl;
+  __shared__ Ctl<SHARED> ctl;
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = sm + C::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -413,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
 
   if (tid == 0) {
     ctl.abort = 0;
-    ctl.partial = 0;
+    if constexpr (SHARED) ctl.start.partial = 0;
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.full[i], C::kPair);
       mbar_init(&ctl.empty[i], 1);
@@ -458,9 +476,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   // ---- this block's share: the units of all slots summed, then the slot its first unit lies in.  The lengths and
   // offsets go through shared memory (where the ring will be), so that the search in them does not wait on L2.
   const int R = a.RT * C::kTiles;
-  const int slots = (int)(SHARED ? shared_slots(a.seqs.n_tok, a.seqs.n_seqs, a.seqs.n_groups, a.G, R)
-                                 : item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, R));
-  PagedSeqs sq = a.seqs;
+  int slots;
+  if constexpr (SHARED) slots = (int)shared_slots(a.seqs.n_tok, a.seqs.n_seqs, a.seqs.n_groups, a.G, R);
+  else slots = (int)item_slots(a.seqs.n_tok, a.seqs.n_seqs, a.G, R);
+  SeqsOf<SHARED> sq = a.seqs;
   if (a.seqs.n_seqs < C::kSlots * C::kGran / (SHARED ? 16 : 8) - 1) {
     int32_t *len_s = reinterpret_cast<int32_t *>(ring), *cu_s = len_s + a.seqs.n_seqs;
     for (int s = tid; s <= a.seqs.n_seqs; s += C::kThreads) {
@@ -469,20 +488,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     }
     sq.seq_lens = len_s;
     if (a.seqs.cu) sq.cu = cu_s;
-    if (SHARED && a.seqs.n_groups <= a.seqs.n_seqs) {
-      int32_t *groups_s = cu_s + a.seqs.n_seqs + 1, *prefix_s = groups_s + a.seqs.n_groups + 1;
-      for (int g = tid; g <= a.seqs.n_groups; g += C::kThreads) {
-        groups_s[g] = a.seqs.groups[g];
-        if (g < a.seqs.n_groups) prefix_s[g] = a.seqs.prefix[g];
+    if constexpr (SHARED)
+      if (a.seqs.n_groups <= a.seqs.n_seqs) {
+        int32_t *groups_s = cu_s + a.seqs.n_seqs + 1, *prefix_s = groups_s + a.seqs.n_groups + 1;
+        for (int g = tid; g <= a.seqs.n_groups; g += C::kThreads) {
+          groups_s[g] = a.seqs.groups[g];
+          if (g < a.seqs.n_groups) prefix_s[g] = a.seqs.prefix[g];
+        }
+        sq.groups = groups_s, sq.prefix = prefix_s;
       }
-      sq.groups = groups_s, sq.prefix = prefix_s;
-    }
     __syncthreads();
   }
   // Slots in rounds of a thread each: inclusive sums of their units, the rounds before them added.  One round (the usual case)
   // gives the total and the start at once; with more, a first pass finds the total.
   int64_t x = 0, cost = 0, before = 0, total = 0;
-  SharedItem it;
+  ItemOf<SHARED> it;
   auto round = [&](int base) {  // this thread's slot: units, and units up to it in the round; returns the round's
     const int s = base + tid;
     cost = 0;
@@ -490,9 +510,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
       if constexpr (SHARED) {
         it = shared_item_at(sq, s, a.G, R, KT);
         // positions that the first token of the sequence sees end within the prefix
-        if (it.own && it.rows > 0 && it.first + 1 < group_span(sq, it.g).prefix) ctl.partial = 1;
+        if (it.own && it.rows > 0 && it.first + 1 < group_span(sq, it.g).prefix) ctl.start.partial = 1;
       } else {
-        static_cast<Item &>(it) = item_at(sq, s, a.G, R, KT, a.window);
+        it = item_at(sq, s, a.G, R, KT, a.window);
       }
       if (!it.ok && blockIdx.x == 0) set_status(a.status, GDN_ERR_BOUNDS);
       cost = (int64_t)units_of<C, SHARED>(it, a.RT) * a.Hkv;
@@ -514,13 +534,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     }
     return all;
   };
-  if (SHARED) __syncthreads();  // ctl.partial
+  if (SHARED) __syncthreads();  // ctl.start.partial
   for (int base = 0; base < slots; base += C::kThreads) {
     const int64_t all = round(base);
-    if (SHARED && blockIdx.x == 0 && base + tid < slots) a.from[base + tid] = total + x - cost;
+    if constexpr (SHARED)
+      if (blockIdx.x == 0 && base + tid < slots) a.from[base + tid] = total + x - cost;
     total += all;
   }
-  if (SHARED && blockIdx.x == 0 && tid == 0) a.from[slots] = total;
+  if constexpr (SHARED)
+    if (blockIdx.x == 0 && tid == 0) a.from[slots] = total;
   const int shares = (int)min((int64_t)units, total);  // of at least a unit, to the first blocks
   const int64_t begin = share_begin(total, min(unit, shares), max(shares, 1));
   const int64_t end = share_begin(total, min(unit + 1, shares), max(shares, 1));
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     if (cost > 0 && begin >= from && begin < from + cost) {
       const uint32_t its = units_of<C, SHARED>(it, a.RT), into = (uint32_t)(begin - from);  // below units * Hkv
       ctl.start_slot = base + tid;
-      ctl.start = it;
+      static_cast<ItemOf<SHARED> &>(ctl.start) = it;
       ctl.start_h = into / its;
       ctl.start_u = into % its;
     }
@@ -557,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
   uint32_t landed = 0;  // PAIR: phase bits of the land barriers, as this warp has used them
   uint32_t issued = 0, phase = 0;  // ring slots that this warp's copies went to, and their phases at the last of them
   uint32_t q_issued[2] = {0, 0};
-  Walk w;
+  Walk<SHARED> w;
   bool more = false;
 
   if (warp == kWarpTma || warp == kWarpTmaV) {
@@ -765,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
     uint32_t base = 0, steps = 0, sphase[2] = {0, 0}, pieces = 0;
     bool ok = true;
     while (more && ok) {
-      const SharedItem &it = w.it;
+      const ItemOf<SHARED> &it = w.it;
       const int tile = t * C::kPair + rank, rr = tile * a.RT + r;
       const bool valid = r < a.RT && rr < it.rows;
       // this thread's row of o, worked out where it is needed: the loop's registers are few
@@ -791,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         int hi = valid ? max(p + 1, 0) : 0, lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
         if constexpr (SHARED) {
           lo = it.lo;
-          if (!it.own && valid) hi = ctl.partial ? row_end(a.seqs, it, it.row0 + rr, a.G) : it.hi;
+          if (!it.own && valid) hi = ctl.start.partial ? row_end(a.seqs, it, it.row0 + rr, a.G) : it.hi;
         }
         float m = -INFINITY, l = 0.f;
         const bool releases = t == nt - 1;  // this warpgroup gives ring slots back
@@ -929,50 +951,52 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
         if (ok && live) {
           const int64_t out = out_row();
           const uint32_t to = tm + lq + C::kO + t * D;
-          if (SHARED && begins && ends) {
-            const int64_t blocks = ((int64_t)a.seqs.n_tok * a.G + 31) / 32, gr = (int64_t)it.t0 * a.G + it.row0 + rr;
-            const int64_t at = ((it.own ? a.Hkv : 0) + w.h) * blocks + gr / 32;
-            uint4 *pp = reinterpret_cast<uint4 *>(a.full) + at * (D / 4 * 32) + gr % 32;
+          if (begins && ends) {
+            if constexpr (SHARED) {
+              const int64_t blocks = ((int64_t)a.seqs.n_tok * a.G + 31) / 32, gr = (int64_t)it.t0 * a.G + it.row0 + rr;
+              const int64_t at = ((own_part(it) ? a.Hkv : 0) + w.h) * blocks + gr / 32;
+              uint4 *pp = reinterpret_cast<uint4 *>(a.full) + at * (D / 4 * 32) + gr % 32;
 #pragma unroll 2
-            for (int x = 0; x < D; x += 32) {
-              uint32_t u[32];
-              tmem_ld32u(to + x, u);
-              tmem_wait_ld();
+              for (int x = 0; x < D; x += 32) {
+                uint32_t u[32];
+                tmem_ld32u(to + x, u);
+                tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) asm volatile("" : "+r"(u[y]));
-              if (valid)
+                for (int y = 0; y < 32; ++y) asm volatile("" : "+r"(u[y]));
+                if (valid)
 #pragma unroll
-                for (int y = 0; y < 32; y += 4)
-                  pp[(x + y) / 4 * 32] = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
-            }
-            if (valid) *reinterpret_cast<float2 *>(a.full_ml + (at * 32 + gr % 32) * 2) = make_float2(m * a.c, l);
-          } else if (begins && ends) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            // rows of this lane's quad, -1: none
-            int64_t rows4[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(0xffffffffu, valid ? out : -1, (lane & ~3) + k);
-#pragma unroll 2
-            for (int x = 0; x < D; x += 32) {
-              uint32_t u[32];
-              tmem_ld32u(to + x, u);
-              tmem_wait_ld();
-              uint4 v[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t *vv = reinterpret_cast<uint32_t *>(&v[y]);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  asm volatile("" : "+r"(u[8 * y + 2 * z]), "+r"(u[8 * y + 2 * z + 1]));
-                  vv[z] = bf16x2(__uint_as_float(u[8 * y + 2 * z]) * inv, __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
-                }
+                  for (int y = 0; y < 32; y += 4)
+                    pp[(x + y) / 4 * 32] = make_uint4(u[y], u[y + 1], u[y + 2], u[y + 3]);
               }
-              quad_transpose(v);  // now piece k is of row k of the quad, columns 8 (lane % 4) ..
+              if (valid) *reinterpret_cast<float2 *>(a.full_ml + (at * 32 + gr % 32) * 2) = make_float2(m * a.c, l);
+            } else {
+              const float inv = l == 0.f ? 0.f : 1.f / l;
+              // rows of this lane's quad, -1: none
+              int64_t rows4[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (rows4[k] >= 0) *reinterpret_cast<uint4 *>(a.o + rows4[k] * D + x + (lane & 3) * 8) = v[k];
+              for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(0xffffffffu, valid ? out : -1, (lane & ~3) + k);
+#pragma unroll 2
+              for (int x = 0; x < D; x += 32) {
+                uint32_t u[32];
+                tmem_ld32u(to + x, u);
+                tmem_wait_ld();
+                uint4 v[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  uint32_t *vv = reinterpret_cast<uint32_t *>(&v[y]);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    asm volatile("" : "+r"(u[8 * y + 2 * z]), "+r"(u[8 * y + 2 * z + 1]));
+                    vv[z] = bf16x2(__uint_as_float(u[8 * y + 2 * z]) * inv, __uint_as_float(u[8 * y + 2 * z + 1]) * inv);
+                  }
+                }
+                quad_transpose(v);  // now piece k is of row k of the quad, columns 8 (lane % 4) ..
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (rows4[k] >= 0) *reinterpret_cast<uint4 *>(a.o + rows4[k] * D + x + (lane & 3) * 8) = v[k];
+              }
+              if (valid && a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
             }
-            if (valid && a.lse) a.lse[out] = l == 0.f ? -INFINITY : fmaf(m, a.c, log2f(l)) * 0.69314718055994530942f;
           } else {
             // the piece as [column / 4][row] fours, so that neighbouring rows lie side by side
             const int64_t which = 2 * unit + (begins ? 1 : 0);
@@ -1032,7 +1056,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAIR>::kThreads, 1)
 // maxima and sums are loaded at once, the warps taking turns; then a warp sums an eighth of the
 // columns over the pieces, and the rows go out through shared memory, whole rows at a time.
 template <int D, int NQ, bool PAIR>
-__global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs a, int blocks) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const TcArgs<false> a, int blocks) {
   constexpr int R = Cfg<D, NQ, PAIR>::R, kV = D / 32;  // fours of columns a warp
   __shared__ uint2 rows[32][D / 4 + 1];
   __shared__ float weight[kSms][32], part[2][8][32];
@@ -1152,8 +1176,8 @@ bool make_q_map(CUtensorMap *m, const void *base, const gdn_cache_shape &s, int 
 
 // The kernel and the one that joins its pieces.
 template <int D, int NQ, bool PAIR, bool SHARED>
-gdn_status launch_two(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, cudaStream_t st, dim3 join_grid,
-                      void (*join)(TcArgs, int)) {
+gdn_status launch_two(const void *k, const void *v, const gdn_cache_shape &s, TcArgs<SHARED> &a, cudaStream_t st,
+                      dim3 join_grid, void (*join)(TcArgs<SHARED>, int)) {
   using C = Cfg<D, NQ, PAIR>;
   a.box = std::gcd(s.page_size, C::kRowsK);  // a power of two
   a.box_log2 = __builtin_ctz(a.box);
@@ -1177,21 +1201,22 @@ gdn_status launch_two(const void *k, const void *v, const gdn_cache_shape &s, Tc
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, (const TcArgs)a) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, (const TcArgs<SHARED>)a) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   cfg.gridDim = join_grid;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join, (TcArgs)a, kSms / C::kPair) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, join, (TcArgs<SHARED>)a, kSms / C::kPair) != cudaSuccess)
     return (void)cudaGetLastError(), GDN_ERR_CUDA;
   return launch_status();
 }
 
 // What the kernel's forms have in common of a call.
-inline TcArgs tc_args(const void *q, const int32_t *table, const PagedSeqs &seqs, const gdn_cache_shape &s,
-                      float scale_log2, int32_t window, uint32_t flags, void *o, float *lse, void *workspace) {
-  TcArgs a{};
+template <bool SHARED>
+TcArgs<SHARED> tc_args(const void *q, const int32_t *table, const SeqsOf<SHARED> &seqs, const gdn_cache_shape &s,
+                       float scale_log2, int32_t window, uint32_t flags, void *o, float *lse, void *workspace) {
+  TcArgs<SHARED> a{};
   a.seqs = seqs;
   a.q = (const __nv_bfloat16 *)q, a.o = (__nv_bfloat16 *)o, a.lse = lse;
   a.table = table, a.table_stride = s.table_stride, a.q_stride = s.q_stride;

@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
     w = next;
     off[0] = ahead[0], off[1] = ahead[1];
   }
+  cp_async_wait_all();  // what was asked for behind the last tile
 }
 
 template <int D, int NT>

@@ -19,9 +19,9 @@ struct RowPieces {
   int from[2], n[2], at[2];
 };
 template <class C>
-__device__ __forceinline__ RowPieces find_pieces(const TcArgs &a, int64_t row, int h, int blocks, int64_t &to) {
+__device__ __forceinline__ RowPieces find_pieces(const TcArgs<true> &a, int64_t row, int h, int blocks, int64_t &to) {
   RowPieces p = {};
-  const PagedSeqs &q = a.seqs;
+  const GroupedSeqs &q = a.seqs;
   const int R = a.RT * C::kTiles, first = (int)item_slots(q.n_tok, q.n_groups, a.G, R);
   const int slots = first + (int)item_slots(q.n_tok, q.n_seqs, a.G, R);
   const int64_t total = a.from[slots];
@@ -75,7 +75,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // Many rows: 32 of a kv head a block, a lane a row, a warp an eighth of the columns; the rows go out through shared memory,
 // whole.  (2250 tokens, 32/8 heads, D 128: 50 us, the other 71.)
 template <int D, int NQ, bool PAIR>
-__global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs a, int blocks) {
+__global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs<true> a, int blocks) {
   using C = Cfg<D, NQ, PAIR>;
   constexpr int kV = D / 32;  // fours of columns a warp
   __shared__ uint2 out[32][D / 4 + 1];
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs a, int bl
 
 // Few rows: a warp a row, a lane its columns; a lane has the maximum and sum of one of 32 pieces.
 template <int D, int NQ, bool PAIR>
-__global__ void __launch_bounds__(256) shared_join_few_kernel(const TcArgs a, int blocks) {
+__global__ void __launch_bounds__(256) shared_join_few_kernel(const TcArgs<true> a, int blocks) {
   using C = Cfg<D, NQ, PAIR>;
   constexpr int kV = (D + 127) / 128;
   const int lane = threadIdx.x & 31, h = blockIdx.y;
@@ -196,7 +196,7 @@ Layout layout(const gdn_cache_shape &s, int32_t n_groups, int row_tiles) {
 }
 
 template <int D, int NQ, bool PAIR>
-gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs &a, void *workspace, cudaStream_t st) {
+gdn_status launch(const void *k, const void *v, const gdn_cache_shape &s, TcArgs<true> &a, void *workspace, cudaStream_t st) {
   const Layout l = layout(s, a.seqs.n_groups, NQ);  // a pair has half the shares, of twice the lanes
   char *w = (char *)workspace;
   a.from = (int64_t *)(w + l.from);
@@ -217,10 +217,10 @@ size_t paged_shared_tc_workspace(const gdn_cache_shape &s, int32_t n_groups, int
 }
 
 // The kernel's form goes by the rows of a group, which share the long part.
-gdn_status paged_shared_tc(const void *q, const void *k, const void *v, const int32_t *table, const PagedSeqs &seqs,
+gdn_status paged_shared_tc(const void *q, const void *k, const void *v, const int32_t *table, const GroupedSeqs &seqs,
                            const gdn_cache_shape &s, int32_t max_group_new, float scale_log2, uint32_t flags, void *o,
                            float *lse, void *workspace, cudaStream_t st) {
-  TcArgs a = tc_args(q, table, seqs, s, scale_log2, 0, flags, o, lse, workspace);
+  TcArgs<true> a = tc_args<true>(q, table, seqs, s, scale_log2, 0, flags, o, lse, workspace);
   const bool pair = pairs(s, max_group_new), two = two_tiles(s, max_group_new);
   if (s.D == 256)
     return pair ? launch<256, 1, true>(k, v, s, a, workspace, st) : launch<256, 1, false>(k, v, s, a, workspace, st);

@@ -480,7 +480,8 @@ gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cach
  *   A new token may itself lie in the prefix; it sees it up to its own position.
  *   max_group_new: the host's bound on the new tokens of one group (it picks the kernel; more are still right)
  * Offsets or lengths that are none of this set GDN_ERR_BOUNDS; the results of those groups are then unspecified.
- * The other arguments, types and kernels are gdn_paged_attn's without a window.  n_groups up to 2^28. */
+ * The other arguments, types and kernels are gdn_paged_attn's without a window (on the first, an infinity or NaN in v may
+ * also reach queries of the same group that do not see it).  n_groups up to 2^28. */
 size_t gdn_paged_attn_shared_workspace_bytes(const gdn_cache_shape *shape, int32_t n_groups, int32_t max_group_new);
 gdn_status gdn_paged_attn_shared(const void *q, const void *k_cache, const void *v_cache, const int32_t *page_table,
                                  const int32_t *seq_lens, const int32_t *cu_seqlens, const int32_t *group_offsets,

@@ -4,9 +4,9 @@
 
 using namespace gdn;
 
-static PagedSeqs seqs(const int32_t *lens, const int32_t *cu, int32_t n_seqs, int32_t n_tok, int32_t max_tokens,
+static GroupedSeqs seqs(const int32_t *lens, const int32_t *cu, int32_t n_seqs, int32_t n_tok, int32_t max_tokens,
                       const int32_t *groups, const int32_t *prefix, int32_t n_groups) {
-  return PagedSeqs{lens, cu, n_seqs, n_tok, max_tokens, groups, prefix, n_groups};
+  return GroupedSeqs{{lens, cu, n_seqs, n_tok, max_tokens}, groups, prefix, n_groups};
 }
 
 extern "C" {
@@ -18,7 +18,7 @@ int64_t host_shared_slots(int64_t n_tok, int32_t n_seqs, int32_t n_groups, int32
 void host_shared_item(const int32_t *lens, const int32_t *cu, int32_t n_seqs, int32_t n_tok, int32_t max_tokens,
                       const int32_t *groups, const int32_t *prefix, int32_t n_groups, int32_t slot, int32_t G, int32_t R,
                       int32_t KT, int32_t over, int32_t *out, int32_t *ends) {
-  const PagedSeqs q = seqs(lens, cu, n_seqs, n_tok, max_tokens, groups, prefix, n_groups);
+  const GroupedSeqs q = seqs(lens, cu, n_seqs, n_tok, max_tokens, groups, prefix, n_groups);
   const SharedItem it = shared_item_at(q, slot, G, R, KT);
   const int32_t v[13] = {it.s, it.t0, it.first, it.row0, it.rows, it.lo, it.hi, it.tile0, it.n_tiles, it.ok,
                          shared_units(it, over), it.g, it.own};

@@ -13,7 +13,7 @@ static constexpr int BP = 64, OVER = 2;
 static MassArgs args(const int32_t *lens, const int32_t *cu, int32_t n_seqs, int32_t n_tok, int32_t most, int32_t G,
                      int32_t Hkv, int32_t RQ, int32_t window, int32_t all, int32_t room) {
   MassArgs a{};
-  a.seqs = PagedSeqs{lens, cu, n_seqs, n_tok, most, nullptr, nullptr, 0};
+  a.seqs = PagedSeqs{lens, cu, n_seqs, n_tok, most};
   a.G = G, a.Hkv = Hkv, a.RQ = RQ, a.window = window, a.all = all, a.room = room;
   return a;
 }

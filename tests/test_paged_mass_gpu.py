@@ -392,3 +392,13 @@ def test_wait_that_runs_out_is_reported(crg, max_new):
     assert ws.status() == 0
     ref, tol = reference(q, lse, cache, [1, 1], 0, 128 ** -0.5, torch.zeros_like(mass), False)
     assert np.all(np.abs(f64(mass) - ref) <= tol)
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("d,hq,hkv,new", [(64, 12, 1, 1), (64, 16, 2, 2), (64, 15, 1, 2), (128, 16, 1, 1), (128, 6, 2, 5),
+                                          (128, 32, 1, 1), (256, 5, 1, 1), (256, 16, 2, 2), (256, 1, 1, 13)])
+def test_few_rows(crg, d, hq, hkv, new, accumulate, window):
+    """One, two and four tiles of eight query rows, odd numbers of them; sequences that end in a tile or at its edge."""
+    lens = [new, 64, 65, 200, 1000, 0, 127 + new]
+    run(crg, 140, "bf16", [min(new, m) for m in lens], lens, hq, hkv, d, 16, window, accumulate, max_new=new)
