@@ -171,13 +171,14 @@ namespace gdn {
 struct MassStart {
   MassSeq m;
   int32_t s, h, j, u;
-  int64_t sum[12];
+  int64_t sum[20];  // a warp each
 };
 
 // The share [begin, end) of block `unit` of `units`; false where it is empty.  Each thread counts the units of a sequence,
 // the inclusive sums of a round of them give the total and then the sequence that holds the share's first unit.
 template <int BP, int OVER, int THREADS>
 __device__ __forceinline__ bool mass_start(const MassArgs &a, int unit, int units, MassStart &st, int64_t &left) {
+  static_assert(THREADS / 32 <= sizeof(st.sum) / sizeof(st.sum[0]), "a sum a warp");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t x = 0, cost = 0, each = 0, before = 0, total = 0;
   MassSeq m;

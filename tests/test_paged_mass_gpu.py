@@ -402,3 +402,11 @@ def test_few_rows(crg, d, hq, hkv, new, accumulate, window):
     """One, two and four tiles of eight query rows, odd numbers of them; sequences that end in a tile or at its edge."""
     lens = [new, 64, 65, 200, 1000, 0, 127 + new]
     run(crg, 140, "bf16", [min(new, m) for m in lens], lens, hq, hkv, d, 16, window, accumulate, max_new=new)
+
+
+@pytest.mark.parametrize("dtype,most", [("bf16", 40), ("bf16", 2), ("f32", 9)])
+def test_more_sequences_than_threads_of_a_block(crg, dtype, most):
+    n = 1500
+    new = [i % (most + 1) for i in range(n)]
+    lens = [x + 37 * i % 211 for i, x in enumerate(new)]
+    run(crg, 99, dtype, new, lens, 4, 2, 64, 16)
