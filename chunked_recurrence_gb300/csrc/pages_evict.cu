@@ -113,6 +113,9 @@ __device__ void row_block(const Evict &e, int i) {
       if (page < 0 || page >= t.n_pages) {
         set_status(t.status, page == -1 ? GDN_ERR_PAGES : GDN_ERR_BOUNDS);
         bad = true;
+      } else if (t.refs[page] <= 0) {  // might be one of the fresh pages
+        set_status(t.status, GDN_ERR_PAGES);
+        bad = true;
       }
     }
     if (len > e.mass_len) {

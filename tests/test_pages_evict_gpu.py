@@ -292,3 +292,18 @@ def test_pages_past_32_bits(crg):
     table, lens, refs = i32([[3, 1, -1]]), i32([16]), i32([0, 1, 0, 1])
     mass = torch.rand((1, 1, 1, 16), device=DEV)
     assert run(crg, (table, lens, refs, mass, [pool]), 8, [0], [11], 2) is not None
+
+
+@pytest.mark.parametrize("keep", [[10, 10], [60, 40]])
+def test_pages_that_nobody_holds_are_refused(crg, keep):
+    """They are free for the fresh ones: rows would be written over while they are read."""
+    page = 16
+    table, lens, refs, mass, pools = make(13, [100, 60], 2, 2, 16, page, spare=12)
+    refs[int(table[1, 2])] = 0
+    state = [table, lens, refs, mass, *pools]
+    before = [t.clone() for t in state]
+    ws = crg.Workspace(1 << 20, DEV)
+    crg.gdn_pages_evict(table, lens, refs, i32([0, 1]), i32(keep), mass, pools, page, 70, 2, workspace=ws)
+    assert ws.status() == crg.GDN_ERR_PAGES
+    for a, b in zip(state, before):
+        assert torch.equal(a, b)
