@@ -128,6 +128,23 @@ GDN_HD void mass_rows(const MassArgs &a, const MassWalk &w, int32_t pos, int32_t
   hi = i1 > w.i0 ? (int32_t)(i1 - w.i0) * a.G : 0;
 }
 
+// Rows of query tile q0 + t that a kernel may keep from one piece to the next: those from row on of the new tokens of (s, h),
+// n of them.  As many as the sequence has, not as many as see the tile at hand: of the first tile that a window leaves in sight
+// the last tokens may see nothing, of the next one they do.
+struct MassHeld {
+  int32_t s, h, row, n;
+};
+GDN_HD MassHeld mass_held(const MassArgs &a, const MassWalk &w, int32_t t) {
+  MassHeld x;
+  x.s = w.s, x.h = w.h, x.row = w.i0 * a.G + (w.q0 + t) * a.RQ;
+  const int32_t rest = w.m.sp.n_new * a.G - x.row;
+  x.n = rest < a.RQ ? rest : a.RQ;
+  return x;
+}
+GDN_HD bool mass_holds(const MassHeld &held, const MassHeld &want) {
+  return held.s == want.s && held.h == want.h && held.row == want.row;
+}
+
 // cuts the next piece at unit u of the tile; false where it holds nothing to do
 template <int BP, int OVER>
 GDN_HD bool mass_cut(const MassArgs &a, MassWalk &w, int32_t u) {

@@ -141,12 +141,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
   };
   uint4 q[NT][kVecs];
   float nl[NT][2];  // minus lse in base 2 of this lane's columns
-  int q_s = -1, q_h = 0, q_row = 0;
+  MassHeld held{-1, 0, 0, 0};
   auto queries = [&](int t) {  // query tile q0 + t of the piece, unless it is there
-    const int row0 = (w.q0 + t) * a.RQ, row = w.i0 * a.G + row0;
-    if (q_s == w.s && q_h == w.h && q_row == row) return;
-    q_s = w.s, q_h = w.h, q_row = row;
-    const int rows = min(a.RQ, (w.i1 - w.i0) * a.G - row0);
+    const MassHeld want = mass_held(a, w, t);
+    if (mass_holds(held, want)) return;
+    held = want;
+    const int row = want.row, rows = want.n;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = n * 8 + g4, i = (row + r) / a.G, g = row + r - i * a.G;
