@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) paged_mass_few_kernel
       if (w.n > 0) weigh(c, 0, sum[c]);
     }
     if (w.n > 1) {  // more rows than the call said: the tile once more for each 8 NT of them, then the next tile's first rows
+      cp_async_wait_all();  // the next tile's, asked for above: copies to one place have no order
       for (int t = 1; t < w.n; ++t) {
         queries(t);
 #pragma unroll

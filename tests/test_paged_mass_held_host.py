@@ -9,6 +9,7 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 WARPS = 152 * 12  # shares at D 64 and 128
+FURTHER = [(64, 4, 6, 1, 0), (128, 4, 9, 2, 0), (128, 4, 9, 2, 500), (128, 1, 40, 9, 0), (256, 2, 7, 1, 300), (256, 2, 7, 3, 0)]
 
 
 @pytest.fixture(scope="module")
@@ -54,3 +55,12 @@ def test_any_shares(host):
             out = walk(host, np.maximum(lens, 0), new, int(rng.integers(1, 5)), int(rng.integers(1, 4)), tokens,
                        int(rng.choice([0, 1, 60, 130, 500])), bool(rng.random() < 0.5), int(rng.choice([1, 2, 7, 40])))
             assert out[2] == 0
+
+
+def test_more_rows_than_the_call_said(host):
+    """The sizes of test_paged_mass_few_gpu's test of that name: warps take a tile's further query rows with another tile
+    still to come."""
+    for d, group, new, said, window in FURTHER:
+        lens = [900 + 62 * s for s in range(32)]
+        pieces, _, lost, followed = walk(host, lens, [new] * 32, group, 8, said, window, True, 152 * (6 if d == 256 else 12))
+        assert followed > 1000 and lost == 0
