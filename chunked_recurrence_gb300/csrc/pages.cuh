@@ -1,7 +1,8 @@
-// pages.cuh -- what the calls on a cache's pages have in common: the checks of their tables and pools, the block-wide
-// scan, the search for free pages, and launches that overlap the kernel before.
+// pages.cuh -- what the calls on a cache's pages have in common: the checks of their tables and pools, the
+// search for free pages, and launches that overlap the kernel before.
 #pragma once
 
+#include "block_scan.cuh"
 #include "common.cuh"
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -19,31 +20,6 @@ struct PlanWords {
 struct Pools {
   void *p[GDN_MAX_POOLS];
 };
-
-// Inclusive sum over the block's threads; *total gets the whole.  sh: 33 words.
-__device__ __forceinline__ int block_scan(int x, int *sh, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += u;
-  }
-  __syncthreads();  // sh is free
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int y = lane < warps ? sh[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += u;
-    }
-    sh[lane] = y;
-  }
-  __syncthreads();
-  *total = sh[warps - 1];
-  return x + (warp ? sh[warp - 1] : 0);
-}
 
 // Four consecutive refs of a thread, n past the end read as `past`.
 __device__ __forceinline__ int4 load_refs(const int32_t *refs, int i, int n, int past) {
