@@ -311,7 +311,8 @@ gdn_status mass_launch(void (*kernel)(P...), const MassArgs &a, int blocks, int 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
+  // the join goes by what the kernel writes
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return (void)cudaGetLastError(), GDN_ERR_CUDA;
   cfg.gridDim = dim3(shares), cfg.blockDim = dim3(BP), cfg.dynamicSmemBytes = 0;
   cudaLaunchKernelEx(&cfg, mass_join_kernel<BP>, a, shares);
   return launch_status();
