@@ -7,7 +7,7 @@
 // copy waits for another.
 //
 // Two launches.  choose_kernel: one block checks the lists and takes the free pages, one a sequence saves and checks its row of
-// the table, and one a (layer, sequence, head) finds the weights' order: a radix selection over the weights as whole
+// the table, one a range of pages that no page is given back more often than it is held, and one a (layer, sequence, head) finds the weights' order: a radix selection over the weights as whole
 // numbers of the same order (digits of 11, 11 and 10 bits from the top, the counts in shared memory; after the first digit
 // those that are left are few) ends with the m - r th largest T; those above T and the first of those at T are written in
 // order to the workspace.  apply_kernel: nothing where a list or row was refused; else the rows move, 32 positions of a
@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kApplyThreads = 128;
 constexpr int kRows = 32;          // positions of a head that a block moves at a time
+constexpr int kRange = sizeof(ChooseShared) / sizeof(int);  // pages whose holders a block counts
 
 struct Evict {
   gdn_page_tables t;
@@ -41,7 +42,7 @@ struct Evict {
   int64_t layer_stride, row_stride, head_stride;  // of mass
   int32_t *kept;
   // the workspace
-  int32_t *ok;      // [1 + n] 1 where the lists, and each sequence's row, can be carried out
+  int32_t *ok;      // [1 + n + ranges] 1 where the lists, each sequence's row, and each range of pages' refs are in order
   int32_t *len;     // [n] lengths before
   int32_t *page0;   // [n] first of a sequence's fresh pages in `fresh`; -1: nothing to evict
   int32_t *mark;    // [n_rows]
@@ -118,14 +119,49 @@ __device__ void row_block(const Evict &e, int i) {
   if (threadIdx.x == 0) e.ok[1 + i] = !bad;
 }
 
+__host__ __device__ __forceinline__ int ranges_of(const gdn_page_tables &t) { return (t.n_pages + kRange - 1) / kRange; }
+
+// Pages [b kRange, (b + 1) kRange): no more of the sequences that give theirs back may hold one than its refs say.  A block a
+// range, which reads all their rows (a warp a row, or several) and counts in shared memory: counts of all pages in memory
+// would have to be cleared by a launch before.
+__device__ void range_block(const Evict &e, int b, int *count) {
+  const gdn_page_tables &t = e.t;
+  const int first = b * kRange, pages = min(kRange, t.n_pages - first), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int p = threadIdx.x; p < pages; p += kChooseThreads) count[p] = 0;
+  __syncthreads();
+  const int warps = kChooseThreads / 32, parts = max(warps / e.n, 1);
+  for (int w = warp; w / parts < e.n; w += warps / parts * parts) {
+    if (warp >= warps / parts * parts) break;
+    const int i = w / parts, s = e.seqs[i], m = e.keep[i];
+    const int len = s >= 0 && s < t.n_rows ? t.seq_lens[s] : -1;
+    if (!in_range(e, s, len, m) || m >= len) continue;
+    const int32_t *row = table_row(t, s);
+    const int held = pages_for(len, t.page_size);
+#pragma unroll 4
+    for (int k = w % parts * 32 + lane; k < held; k += parts * 32) {
+      const uint32_t p = (uint32_t)row[k] - first;
+      if (p < (uint32_t)pages) atomicAdd(&count[p], 1);
+    }
+  }
+  __syncthreads();
+  bool bad = false;
+  for (int p = threadIdx.x; p < pages; p += kChooseThreads) bad = bad || (count[p] > 0 && count[p] > t.refs[first + p]);
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(t.status, GDN_ERR_PAGES);
+    bad = true;
+  }
+  if (threadIdx.x == 0) e.ok[1 + e.n + b] = !bad;
+}
+
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const Evict e) {
   __shared__ ChooseShared sm;
   grid_dependency_wait();
   launch_dependents();
   // the lists of the largest index first: the plan and the rows are shorter
-  const int lists = gridDim.x - 1 - e.n;
-  if (blockIdx.x == lists) return plan_block(e, sm.sh);
-  if ((int)blockIdx.x > lists) return row_block(e, blockIdx.x - lists - 1);
+  const int lists = gridDim.x - 1 - e.n - ranges_of(e.t), other = (int)blockIdx.x - lists;
+  if (other == 0) return plan_block(e, sm.sh);
+  if (other > e.n) return range_block(e, other - 1 - e.n, reinterpret_cast<int *>(&sm));
+  if (other > 0) return row_block(e, other - 1);
   const int64_t lih = blockIdx.x;
   const int h = (int)(lih % e.heads), i = (int)(lih / e.heads % e.n), l = (int)(lih / e.heads / e.n);
   const int s = e.seqs[i], m = e.keep[i];
@@ -152,7 +188,7 @@ __global__ void __launch_bounds__(kApplyThreads) apply_kernel(const Evict e, con
   const int tid = threadIdx.x;
   grid_dependency_wait();
   bool ok = e.ok[0];
-  for (int i = tid; i < e.n; i += kApplyThreads) ok = ok && e.ok[1 + i];
+  for (int i = tid; i < e.n + ranges_of(t); i += kApplyThreads) ok = ok && e.ok[1 + i];
   bool asked = false;  // whether the lists can be carried out: after the first loads, which wait as long
 
   const int chunks = (e.max_keep + kRows - 1) / kRows;
@@ -223,10 +259,7 @@ __global__ void __launch_bounds__(kApplyThreads) apply_kernel(const Evict e, con
       const int page = e.old[(int64_t)i * t.max_pages + k], now = k < a ? e.fresh[e.page0[i] + k] : -1;
       row[k] = now;
       if (now >= 0) t.refs[now] = 1;
-      if (atomicSub(&t.refs[page], 1) <= 0) {  // held by nobody: stays at 0
-        atomicAdd(&t.refs[page], 1);
-        set_status(t.status, GDN_ERR_PAGES);
-      }
+      atomicSub(&t.refs[page], 1);
     }
     if (tid == 0) t.seq_lens[e.seqs[i]] = m;
   }
@@ -255,7 +288,7 @@ bool heads_ok(const gdn_page_heads *in, const gdn_page_tables &t, gdn_page_heads
 size_t lay_out(Evict &e, void *workspace) {
   const size_t lists = (size_t)e.n_layers * e.n * e.heads * e.max_keep;
   int32_t *w = (int32_t *)((char *)workspace + 256);
-  e.ok = w, w += 1 + e.n;
+  e.ok = w, w += 1 + e.n + ranges_of(e.t);
   e.len = w, w += e.n;
   e.page0 = w, w += e.n;
   e.mark = w, w += e.t.n_rows;
@@ -298,7 +331,7 @@ extern "C" gdn_status gdn_pages_evict(const gdn_page_tables *tables, const int32
                          slots * h.slot_stride + others * h.slot_head_stride > room))
     return GDN_ERR_INVALID_ARG;
   // the blocks of a launch, and the vectors of a block's rows, fit 32 bits
-  if ((int64_t)h.n_layers * n * h.heads > 1 << 30 || h.row_bytes > 1 << 16) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)h.n_layers * n * h.heads > 1 << 29 || h.row_bytes > 1 << 16) return GDN_ERR_UNSUPPORTED;
   e.n = n, e.max_keep = max_keep, e.recent = recent, e.n_layers = h.n_layers, e.heads = h.heads, e.mass_len = h.mass_len;
   if (!ws_ok(workspace, workspace_bytes, lay_out(e, workspace))) return GDN_ERR_WORKSPACE;
   if (n == 0) return GDN_OK;
@@ -307,7 +340,7 @@ extern "C" gdn_status gdn_pages_evict(const gdn_page_tables *tables, const int32
   e.layer_stride = h.layer_stride, e.row_stride = h.row_stride, e.head_stride = h.head_stride;
   cudaStream_t st = (cudaStream_t)stream;
   const int64_t lists = (int64_t)h.n_layers * n * h.heads;
-  launch_early(choose_kernel, (int)(1 + n + lists), kChooseThreads, st, 0, e);
+  launch_early(choose_kernel, (int)(lists + 1 + n + ranges_of(e.t)), kChooseThreads, st, 0, e);
   if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
   const int per_layer = pools->n_pools / h.n_layers;
   const int64_t work = std::max<int64_t>(lists * ((max_keep + kRows - 1) / kRows), n);

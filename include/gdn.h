@@ -585,9 +585,9 @@ typedef struct {
  * append later tokens with explicit positions.
  *   pools: n_pools a multiple of n_layers: pool j belongs to layer j / (n_pools / n_layers) (k and v caches: k0 v0 k1 v1 ...)
  *   kept: [n_layers][n][heads][max_keep] int32 out or NULL: the positions that stay, then -1
- * A list that cannot be carried out (a row outside the tables or twice, keep[i] outside [0, max_keep], an entry of -1 or
- * a page of refs 0 in use, too few free pages) sets GDN_ERR_PAGES, a page outside the cache or a length past mass_len GDN_ERR_BOUNDS; then
- * nothing changes.  workspace: gdn_pages_evict_workspace_bytes(t, n, max_keep, n_layers, heads), 256-byte aligned. */
+ * A list that cannot be carried out (a row outside the tables or twice, keep[i] outside [0, max_keep], an entry of -1, a
+ * page that the sequences to be cut hold more often than its refs say, too few free pages) sets GDN_ERR_PAGES, a page outside
+ * the cache or a length past mass_len GDN_ERR_BOUNDS; then nothing changes.  workspace: gdn_pages_evict_workspace_bytes(t, n, max_keep, n_layers, heads), 256-byte aligned. */
 size_t gdn_pages_evict_workspace_bytes(const gdn_page_tables *t, int32_t n, int32_t max_keep, int32_t n_layers,
                                        int32_t heads);
 gdn_status gdn_pages_evict(const gdn_page_tables *t, const int32_t *seqs, const int32_t *keep, int32_t n,
