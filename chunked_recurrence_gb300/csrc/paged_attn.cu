@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_simt_kernel(const Simt
 // A block per row: the parts' maxima, sums and weighted sums joined.  A lane has the maximum and sum of parts lane
 // and lane + 32 (there are at most 64); a warp adds up every fourth part.
 template <typename T>
-__global__ void __launch_bounds__(kJoin) simt_join_kernel(const float *part, int splits, int64_t rows, int D, T *o,
-                                                          float *lse) {
+__global__ void __launch_bounds__(kJoin) simt_join_kernel(const PagedSeqs seqs, int Hq, const float *part, int splits,
+                                                          int64_t rows, int D, T *o, float *lse) {
   __shared__ float s_x[kJoin / 32][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sm100::grid_dependency_wait();
-  const int64_t r = blockIdx.x, step = rows * (D + 2);
+  const int64_t r = blockIdx.x, step = rows * (D + 2), all = (int64_t)cu_at(seqs, seqs.n_seqs) * Hq;
   const float *p = part + r * (D + 2);
   float m[2], l[2], w[2], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kJoin) simt_join_kernel(const float *part, int
     s_x[warp][d] = x;
   }
   __syncthreads();
+  if (r >= all) return;  // behind the last sequence: nothing left its parts
   for (int d = threadIdx.x; d < D; d += kJoin) {
     float x = 0.f;
 #pragma unroll
@@ -242,7 +243,9 @@ gdn_status launch_join(const SimtArgs &a, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr, cfg.numAttrs = 1;
   const int parts = a.seqs.n_groups ? 2 * a.splits : a.splits;
-  cudaLaunchKernelEx(&cfg, simt_join_kernel<T>, (const float *)a.part, parts, rows, (int)a.D, (T *)a.o, a.lse);
+  const PagedSeqs seqs = a.seqs;
+  cudaLaunchKernelEx(&cfg, simt_join_kernel<T>, seqs, (int)a.Hq, (const float *)a.part, parts, rows, (int)a.D, (T *)a.o,
+                     a.lse);
   return launch_status();
 }
 

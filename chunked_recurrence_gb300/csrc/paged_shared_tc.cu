@@ -86,10 +86,11 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const TcArgs<true> a, 
   __shared__ uint2 out[32][D / 4 + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
   grid_dependency_wait();
-  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane, all = (int64_t)cu_at(a.seqs, a.seqs.n_seqs) * a.G;
   int64_t to = -1;
   RowPieces p = {};
   if (row < (int64_t)a.seqs.n_tok * a.G) p = find_pieces<C>(a, row, h, blocks, to);
+  if (row >= all) to = -1;  // behind the last sequence
   const int pieces = p.n[0] + p.n[1], most = (int)__reduce_max_sync(0xffffffffu, (unsigned)pieces);
   const int64_t in_full = (int64_t)h * gridDim.x + blockIdx.x, of_kind = (int64_t)a.Hkv * gridDim.x;
   auto ml_of = [&](int i) {
@@ -139,8 +140,10 @@ __global__ void __launch_bounds__(256) shared_join_few_kernel(const TcArgs<true>
   grid_dependency_wait();
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (int64_t)a.seqs.n_tok * a.G;
   if (row >= rows) return;
+  const int64_t all = (int64_t)cu_at(a.seqs, a.seqs.n_seqs) * a.G;
   int64_t to;
   const RowPieces p = find_pieces<C>(a, row, h, blocks, to);
+  if (row >= all) return;  // behind the last sequence
   const int pieces = p.n[0] + p.n[1], r = (int)(row % 32);
   const int64_t of_head = (rows + 31) / 32, in_full = (int64_t)h * of_head + row / 32, of_kind = (int64_t)a.Hkv * of_head;
   auto ml_of = [&](int i) {

@@ -370,7 +370,9 @@ gdn_status gdn_cu_seqlens_from_position_ids(const int64_t *position_ids, int64_t
  * Device-side checks: a length past max_pages * page_size, offsets that fall or leave
  * [0, n_tok], and a page outside [0, n_pages) set GDN_ERR_BOUNDS in the status word (the
  * workspace's first, or the one that the shape or tables name) and are not followed; the
- * results of that sequence are then unspecified.
+ * results of that sequence are then unspecified.  Tokens behind the last sequence's
+ * (cu_seqlens[n_seqs] below n_tok, a padded batch) count for nothing: attention leaves their rows of o
+ * and lse as they are; gdn_kv_append stores none of them and sets GDN_ERR_BOUNDS.
  * ------------------------------------------------------------------------------------ */
 
 typedef struct {
