@@ -330,7 +330,10 @@ extern "C" gdn_status gdn_pages_evict(const gdn_page_tables *tables, const int32
   if (pools->n_pools && (room < 0 || (slots && h.slot_stride > room / slots) || (others && h.slot_head_stride > room / others) ||
                          slots * h.slot_stride + others * h.slot_head_stride > room))
     return GDN_ERR_INVALID_ARG;
-  // the blocks of a launch, and the vectors of a block's rows, fit 32 bits
+  // a thread's place in a list (up to two rounds past its end), the blocks of a launch, and the vectors of a block's rows
+  // fit 32 bits
+  constexpr int32_t kMost = INT32_MAX - 4 * 4 * kChooseThreads + 1;
+  if (h.mass_len > kMost || max_keep > kMost) return GDN_ERR_UNSUPPORTED;
   if ((int64_t)h.n_layers * n * h.heads > 1 << 29 || h.row_bytes > 1 << 16) return GDN_ERR_UNSUPPORTED;
   e.n = n, e.max_keep = max_keep, e.recent = recent, e.n_layers = h.n_layers, e.heads = h.heads, e.mass_len = h.mass_len;
   if (!ws_ok(workspace, workspace_bytes, lay_out(e, workspace))) return GDN_ERR_WORKSPACE;

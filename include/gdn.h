@@ -587,6 +587,7 @@ typedef struct {
  * append later tokens with explicit positions.
  *   pools: n_pools a multiple of n_layers: pool j belongs to layer j / (n_pools / n_layers) (k and v caches: k0 v0 k1 v1 ...)
  *   kept: [n_layers][n][heads][max_keep] int32 out or NULL: the positions that stay, then -1
+ *   mass_len and max_keep at most 2^31 - 2^14, n_layers n heads at most 2^29 (else GDN_ERR_UNSUPPORTED)
  * A list that cannot be carried out (a row outside the tables or twice, keep[i] outside [0, max_keep], an entry of -1, a
  * page that the sequences to be cut hold more often than its refs say, too few free pages) sets GDN_ERR_PAGES, a page outside
  * the cache or a length past mass_len GDN_ERR_BOUNDS; then nothing changes.  workspace: gdn_pages_evict_workspace_bytes(t, n, max_keep, n_layers, heads), 256-byte aligned. */
