@@ -6,8 +6,8 @@ the winners, the cache's pages brought together now and then.
 
 Weights are random.  Projections are plain torch products; the layers between them are this package's:
     recurrent layer:  gdn_layer_fwd for a prompt, gdn_decode_step for a token, its state a row of a tensor
-    attention layer:  gdn_kv_append (rotary positions on q and k on the way), gdn_paged_attn for the prompt,
-                      gdn_paged_attn_shared for the beams, whose prompt is read once for all of them
+    attention layer:  gdn_kv_append (rotary positions on q and k on the way), gdn_paged_attn; for beams whose prompt is
+                      long enough gdn_paged_attn_shared, which reads it once for all of them
     sequences:        gdn_pages_grow / fork / free / compact for the pages, gdn_pages_copy for the recurrent state
     a long prompt:    with --keep, gdn_paged_mass counts the attention weight of its positions and gdn_pages_evict
                       leaves that many of them in the cache before the beams begin
@@ -43,6 +43,8 @@ class Config:
     rows: int = 8              # sequences that may live at once
     max_len: int = 256
     keep: int = 0              # of a prompt, positions left in the cache (0: all); a quarter of them its last
+    pays: int = 1 << 28        # bytes of a layer's k and v of the prompt, counted once a beam, from which it is read once for
+                               # all (16 beams over 4000 positions, 4096 bytes each, 39 -> 32 us; 4 over 37 11 -> 20)
     dtype: torch.dtype = torch.bfloat16
 
 
@@ -190,10 +192,12 @@ def beams(model: Hybrid, prompt, n_beams, n_tokens):
     logits = model.forward(prompt, [0], [prompt.numel()])[-1:]
     score = logits.log_softmax(-1)
     best = score[0].topk(n_beams)
-    shared = prompt.numel()
-    if model.cfg.keep:
+    c, shared = model.cfg, prompt.numel()
+    if c.keep:
         model.evict([0])
-        shared = min(shared, model.cfg.keep)
+        shared = min(shared, c.keep)
+    if n_beams * shared * 2 * c.kv_heads * c.D * c.dtype.itemsize < c.pays:
+        shared = 0
     model.fork([0] * (n_beams - 1), rows[1:])
     texts, scores = [[t] for t in best.indices.tolist()], best.values
     for step in range(n_tokens - 1):
