@@ -6,8 +6,9 @@
 // 16 bytes of the row that lie together, for two products, and the queries' fragments, which stay in registers, are taken
 // the same way.  So a lane reads back from shared memory only what it copied there itself: a queue of its own, in which the
 // rows of 16 positions are asked for three products ahead (asynchronous copies), the pages of the next tile a tile ahead.
-// 64 single tokens over 500 to 16000, 32 / 8 heads, D 128: 197 us with the join, 87% of a copy's rate (tcgen05 with four of
-// a tile's 256 columns in use: some 440; fragments straight from global memory, without the queue: 290).
+// 64 single tokens over 500 to 16000, 32 / 8 heads, D 128: 206 us, some 10 of them the masses put back, 83% of a copy's rate
+// (tcgen05 with four of a tile's 256 columns in use: 452; fragments straight from global memory, without the queue: 301).  64 x 4
+// drafted tokens over 4000 to 8000: 148 us, with windows of 4096 and 1024 121 and 39 (by bytes alone 121, 83 and 21).
 #include <algorithm>
 
 #include "common.cuh"

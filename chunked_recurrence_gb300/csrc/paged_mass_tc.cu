@@ -13,7 +13,8 @@
 // one unit bounds it (products of 16 columns, weights without the exponential, Q copied once: each less than 10%
 // faster): it is the step's hand-over of a slot and two FMAs, an exponential and an add a weight, 46% of issue slots.
 // Slower: part of the exponentials by a polynomial (392 -> 417), query tiles of 128 rows (457), two softmax warpgroups of more
-// registers (283 to 328), 16 columns a TMEM load (280 -> 311).
+// registers (283 to 328), 16 columns a TMEM load (280 -> 311).  Not built: pairs of blocks, each with half of a query tile (at
+// D 256 the ring holds one such tile, so the next one's copy waits for this one's products).
 #include <cuda.h>
 
 #include <algorithm>

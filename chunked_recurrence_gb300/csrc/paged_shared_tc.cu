@@ -10,10 +10,11 @@
 // shared_join_kernel finds the pieces of both items of each row of o from the units before each slot, which the first block
 // leaves, and adds them up: nothing waits between the two kinds.
 //
-// What bounds it, 32 query and 8 kv heads of D 128: 64 single tokens over a prompt of 16000 and up to 500 of their own, 71 us,
-// because own items of a few tiles of keys are chains of copy, S, softmax and O with nothing to overlap (the bytes take 20
-// us); 15 chunks of up to 300 over 9001, 343 us, some 300 of them the first kernel, its tensor pipe 52% active, and 45 the
-// join, which reads 94 MB of partial sums with dependent loads.
+// What bounds it, 32 query and 8 kv heads of D 128: 64 single tokens over a prompt of 16000 and up to 500 of their own, 70 us,
+// because own items of a few tiles of keys are chains of copy, S, softmax and O, one at a time, in a form that the group's
+// rows chose: of two row tiles, or of the two blocks of a pair, one has no row (the bytes take 20 us; the plain call 426);
+// 15 chunks of up to 300 over 9001, 343 us, some 300 of them the first kernel, its tensor pipe 52% active, and 45 the join, which
+// reads 94 MB of partial sums with dependent loads (the plain call 350: it reads a prefix once for 512 rows).
 #include "paged_attn_tc.cuh"
 
 namespace gdn {

@@ -6,18 +6,19 @@
 // own, so other sequences that share its old pages keep theirs as they are, every row is read and written once, and no
 // copy waits for another.
 //
-// Two launches.  choose_kernel: one block checks the lists and takes the free pages, one a sequence saves and checks its row of
-// the table, one a range of pages that no page is given back more often than it is held, and one a (layer, sequence, head) finds the weights' order: a radix selection over the weights as whole
-// numbers of the same order (digits of 11, 11 and 10 bits from the top, the counts in shared memory; after the first digit
-// those that are left are few) ends with the m - r th largest T; those above T and the first of those at T are written in
-// order to the workspace.  apply_kernel: nothing where a list or row was refused; else the rows move, 32 positions of a
-// head a block with its place in the old and new pages worked out once for all pools of the layer, the weights follow, and
-// tables, lengths and refs are written.
+// Two launches.  choose_kernel: one block checks the lists and takes the free pages, one a sequence saves and checks its row
+// of the table, one a range of pages checks that none is given back more often than it is held, and one a (layer, sequence,
+// head) finds the weights' order: a radix selection over the weights as whole numbers of the same order (digits of 11, 11 and
+// 10 bits from the top, the counts in shared memory; after the first digit those that are left are few) ends with the
+// m - r th largest T; those above T and the first of those at T are written in order to the workspace.  apply_kernel: nothing
+// where a list, row or range was refused; else the rows move, 32 positions of a head a block with its place in the old and
+// new pages worked out once for all pools of the layer, the weights follow, and tables, lengths and refs are written.
 //
 // Bounds: the second kernel moves bytes, scattered rows of 256 in and whole pages out.  24 sequences of 700 to 6000 tokens cut
 // to 1900, 2 kv heads, D 256, two layers (256 MB): 50 us, 5.1 TB/s; blocks of 16 and 64 positions took as long.  The first
 // takes 14 to 18 us: a block a list, passes over it from registers for the digits, each with its barriers, and the lists
-// written in order.  Dividing a list among blocks would put a barrier across the GPU between the digits.
+// written in order (pages_choose.cuh).  48 lists are 48 of 152 SMs; a list over a cluster of blocks, counts added through
+// their shared memory, is not built.
 #include <algorithm>
 
 #include "pages.cuh"

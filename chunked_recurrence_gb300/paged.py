@@ -129,9 +129,10 @@ def _device_words(device, stream):
 
 
 def gdn_paged_status(device="cuda", stream=None) -> int:
-    """The status of a device's gdn_kv_append, gdn_paged_attn and gdn_pages_* calls without a workspace (those with
-    one leave theirs in it): GDN_OK, or the first error that one of them found on the GPU since the last
-    gdn_paged_status_reset: GDN_ERR_PAGES (a grow or fork was refused), GDN_ERR_BOUNDS, GDN_ERR_TIMEOUT.
+    """The status of a device's gdn_kv_append, gdn_paged_attn, gdn_paged_attn_shared, gdn_paged_mass and gdn_pages_* calls
+    without a workspace (those with one leave theirs in it): GDN_OK, or the first error that one of them found on the GPU
+    since the last gdn_paged_status_reset: GDN_ERR_PAGES (a grow, fork or eviction was refused), GDN_ERR_BOUNDS,
+    GDN_ERR_TIMEOUT.
     Synchronises `stream` (default: the current one)."""
     words, stream = _device_words(device, stream)
     out = ctypes.c_int32(0)
@@ -397,7 +398,8 @@ def gdn_paged_attn_shared(q, k_cache, v_cache, page_table, seq_lens, group_offse
     """gdn_paged_attn where groups of sequences share a prefix: sequences group_offsets[g] .. group_offsets[g + 1] - 1 hold
     the same tokens in their first prefix_lens[g] positions (device int32 [n_groups + 1], from 0 to n_seqs, and
     [n_groups]), which are read once for the group, from its first sequence's pages.  max_group_new: a bound on
-    the new tokens of one group (default: all of them).  Returns (o, lse or None) as gdn_paged_attn, without gradients."""
+    the new tokens of one group (default: all of them).  Returns (o, lse or None) as gdn_paged_attn, without gradients.
+    For few sequences, short prefixes and long chunks gdn_paged_attn is the faster one; include/gdn.h has the figures."""
 
     def make():
         _need_cuda(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens, o, lse)
@@ -581,8 +583,9 @@ def gdn_pages_evict(page_table, seq_lens, refs, seqs, keep, mass, pools, page_si
     [n_layers, n_rows, heads, length]; ties to the lowest position), moved in their order to fresh pages.
     pools: each layer's [n_pages, page_size, heads, D] caches in turn (k0, v0, k1, v1, ...).  Masses move along, the tables
     follow.  Returns the positions that stayed, int32 [n_layers, n, heads, max_keep] filled up with -1, or None without
-    want_kept.  Nothing changes, and nothing is returned that means anything, if a list cannot be carried out or the free
-    pages do not suffice: GDN_ERR_PAGES, as for gdn_pages_grow."""
+    want_kept.  Nothing changes, and nothing is returned that means anything, if a list cannot be carried out (pages held more
+    often than refs says among the reasons) or the free pages do not suffice, ceil(keep / page_size) for each sequence that is
+    cut, before its old ones are given back: GDN_ERR_PAGES, as for gdn_pages_grow."""
     pools = tuple(pools)
     t, n, _ = _page_tables(page_table, seq_lens, refs, page_size, workspace, ("seqs", "keep"), seqs, keep)
     p, _keep = _page_pools(pools, refs.shape[0])
