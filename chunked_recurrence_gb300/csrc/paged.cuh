@@ -137,7 +137,7 @@ GDN_HD GroupSpan group_span(const GroupedSeqs &q, int32_t g) {
   r.s0 = group_at(q, g), r.s1 = group_at(q, g + 1);
   const int32_t p = q.prefix[g];
   r.prefix = p < 0 ? 0 : p > q.max_tokens ? q.max_tokens : p;
-  r.ok = q.groups[g] == r.s0 && q.groups[g + 1] == r.s1 && r.s0 <= r.s1 && r.prefix == p &&
+  r.ok = q.groups[g] == r.s0 && q.groups[g + 1] == r.s1 && r.s0 <= r.s1 && (r.prefix == p || r.s0 == r.s1) &&
          (g > 0 || r.s0 == 0) && (g + 1 < q.n_groups || r.s1 == q.n_seqs);
   return r;
 }

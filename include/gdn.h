@@ -479,6 +479,7 @@ gdn_status gdn_paged_attn(const void *q, const void *k_cache, const void *v_cach
  *   first prefix_lens[g] positions of each of the group's sequences hold the same tokens.  They are read from the
  *   pages of the group's first sequence; the others' pages (shared or copies of their own) only behind them.
  *   prefix_lens[g] is at most the length of each of the group's sequences that has new tokens, and of its first.
+ *   (Of a group of no sequences it is not used.)
  *   A new token may itself lie in the prefix; it sees it up to its own position.
  *   max_group_new: the host's bound on the new tokens of one group (it picks the kernel; more are still right)
  * Offsets or lengths that are none of this set GDN_ERR_BOUNDS; the results of those groups are then unspecified.
